@@ -11,9 +11,18 @@ Entry points (same names as the C ABI):
   chain_bwd_workspace_size(A, C)
   sp_relayout(shards, p, head_group, out, stream=None)
   sp_relayout_inverse(inp, p, head_group, shards, stream=None)
+  chain_qk_norm_rope(Q, K, gq, gk, inv_freq, positions, eps, pairs, Qo, Ko, stream=None)
+  chain_qk_norm_rope_bwd(dQo, dKo, Q, K, gq, gk, inv_freq, positions, eps, pairs, dQ, dK, dgq, dgk,
+                         workspace, stream=None)
+  chain_paged_append(K, V, cu_seqlens, kv_lens, page_table, Kc, Vc, stream=None)
+  chain_qk_norm_rope_append(Q, K, V, gq, gk, inv_freq, eps, pairs, cu_seqlens, kv_lens, page_table,
+                            Kc, Vc, Qo, stream=None)
+  chain_fwd_paged(Q, Kc, Vc, cu_seqlens, kv_lens, page_table, mask, scale, O, LSE, workspace,
+                  stream=None)
   chain_check(stream=None)
 plus allocating conveniences ``attention_fwd``, ``attention_bwd``,
-``mlp_chain_fwd`` and ``relayout``.
+``mlp_chain_fwd``, ``relayout``, ``qk_norm_rope``, ``qk_norm_rope_bwd``,
+``qk_norm_rope_append`` and ``attention_fwd_paged``.
 """
 from __future__ import annotations
 
@@ -25,6 +34,7 @@ import torch
 
 F_IDENTITY, F_SOFTMAX, F_GELU_TANH = 0, 1, 2
 MASK_NONE, MASK_CAUSAL = 0, 1
+PAIRS_HALF, PAIRS_NEIGHBOUR = 0, 1
 BF16, F32, E4M3 = 0, 1, 2
 
 OK, ERR_ARG, ERR_DTYPE, ERR_DEVICE, ERR_CUDA, ERR_TIMEOUT, ERR_UNSUPPORTED = 0, -1, -2, -3, -4, -5, -6
@@ -93,6 +103,18 @@ def _load():
             lib.chain_fwd_f16pv_workspace_size.restype = ctypes.c_size_t
             lib.chain_fwd_fp8_workspace_size.argtypes = [P]
             lib.chain_fwd_fp8_workspace_size.restype = ctypes.c_size_t
+            i64, sz = ctypes.c_int64, ctypes.c_size_t
+            lib.chain_qk_norm_rope.argtypes = [P, P, P, P, P, vp, fl, ci, P, P, vp]
+            lib.chain_qk_norm_rope_bwd.argtypes = [P, P, P, P, P, P, P, vp, fl, ci, P, P, P, P, vp, sz,
+                                                   vp]
+            lib.chain_paged_append.argtypes = [P, P, vp, vp, vp, i64, ci, ci, P, P, vp]
+            lib.chain_qk_norm_rope_append.argtypes = [P, P, P, P, P, P, fl, ci, vp, vp, vp, i64, ci, ci,
+                                                      P, P, P, vp]
+            lib.chain_fwd_paged.argtypes = [P, P, P, vp, vp, vp, i64, ci, ci, ci, fl, P, P, vp, sz, vp]
+            for fn, n in (("chain_qk_norm_rope_bwd_workspace_size", 1),
+                          ("chain_fwd_paged_workspace_size", 2)):
+                getattr(lib, fn).argtypes = [P] * n
+                getattr(lib, fn).restype = sz
             lib.sp_relayout.argtypes = [P, ci, ci, P, vp]
             lib.sp_relayout_inverse.argtypes = [P, ci, ci, P, vp]
             lib.chain_check.argtypes = [vp, ctypes.POINTER(ci)]
@@ -107,6 +129,8 @@ def _load():
             for fn in ("chain_fwd", "chain_fwd_sp", "chain_fwd_varlen", "chain_bwd", "chain_bwd_varlen",
                        "chain_bwd_noalloc", "chain_fwd_fp8", "chain_fwd_f16pv",
                        "chain_fwd_sp_f16pv",
+                       "chain_qk_norm_rope", "chain_qk_norm_rope_bwd", "chain_paged_append",
+                       "chain_qk_norm_rope_append", "chain_fwd_paged",
                        "sp_relayout",
                        "sp_relayout_inverse",
                        "chain_check", "chain_selftest_wait_timeout", "chain_umma_selftest",
@@ -303,6 +327,121 @@ def chain_bwd_noalloc(dO, A, B, C, O, LSE, f, mask, scale, dA, dB, dC, stream=No
         "chain_bwd_noalloc")
 
 
+# Norm + rotation and the paged cache: these calls take bf16 and f32 by their
+# values, so a tensor of another type is refused here (desc() would pass an
+# f16 tensor's two-byte payload as bf16), as is one that is not on the current
+# device, where the kernels launch.
+_FLOATS = {torch.bfloat16: BF16, torch.float32: F32}
+_I64x4 = ctypes.c_int64 * 4
+
+
+def _fdesc(t):
+    dt = _FLOATS.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"chain_gb300: bf16 or f32 tensors only, not {t.dtype}")
+    shape = t.shape
+    if not 1 <= len(shape) <= 4:
+        raise ValueError("chain_gb300: tensors must have 1 to 4 dimensions")
+    return ctypes.byref(TensorDesc(t.data_ptr(), dt, len(shape), _I64x4(*shape), _I64x4(*t.stride())))
+
+
+def _on_current_device(*ts):
+    dev = torch.cuda.current_device()
+    for t in ts:
+        if t is not None and not (t.is_cuda and t.get_device() == dev):
+            raise ValueError(f"chain_gb300: tensors must be on the current device, cuda:{dev}")
+
+
+def _i32(t, what, ndim=1):
+    if t.dtype != torch.int32 or t.dim() != ndim:
+        raise ValueError(f"{what} must be a CUDA int32 tensor of {ndim} dimension{'s' * (ndim > 1)}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
+
+
+def _positions(positions, tokens):
+    if positions is None:
+        return None
+    if not positions.is_contiguous():
+        raise ValueError("positions must be contiguous")
+    if positions.numel() != tokens:
+        raise ValueError("positions must hold one position for each token")
+    return _i32(positions, "positions", positions.dim())
+
+
+def _paged(cu_seqlens, kv_lens, page_table):
+    """The C ABI's arguments from cu_seqlens to max_pages."""
+    batch = kv_lens.shape[0] if kv_lens.dim() == 1 else -1
+    cu, lens = _i32(cu_seqlens, "cu_seqlens"), _i32(kv_lens, "kv_lens")
+    table = _i32(page_table, "page_table", 2)
+    if cu_seqlens.shape[0] != batch + 1 or page_table.shape[0] != batch:
+        raise ValueError("cu_seqlens [batch + 1], kv_lens [batch] and page_table [batch][max_pages] "
+                         "must agree on the batch")
+    return cu, lens, table, page_table.stride(0) if batch > 1 else page_table.shape[1], batch, \
+        page_table.shape[1]
+
+
+def chain_qk_norm_rope(Q, K, gq, gk, inv_freq, positions, eps, pairs, Qo, Ko, stream=None):
+    """Per-head RMS norm and rotary embedding of Q and K; see include/chain.h."""
+    _on_current_device(Q, K, gq, gk, inv_freq, positions, Qo, Ko)
+    _ok(_load().chain_qk_norm_rope(_fdesc(Q), _fdesc(K), _fdesc(gq), _fdesc(gk),
+                                   None if inv_freq is None else _fdesc(inv_freq),
+                                   _positions(positions, Q.numel() // max(1, Q.shape[-1] * Q.shape[-2])),
+                                   eps, pairs, _fdesc(Qo), _fdesc(Ko), _stream(stream)),
+        "chain_qk_norm_rope")
+
+
+def chain_qk_norm_rope_bwd_workspace_size(Q) -> int:
+    return int(_load().chain_qk_norm_rope_bwd_workspace_size(_fdesc(Q)))
+
+
+def chain_qk_norm_rope_bwd(dQo, dKo, Q, K, gq, gk, inv_freq, positions, eps, pairs, dQ, dK, dgq, dgk,
+                           workspace, stream=None):
+    """Gradients of chain_qk_norm_rope; see include/chain.h."""
+    _on_current_device(dQo, dKo, Q, K, gq, gk, inv_freq, positions, dQ, dK, dgq, dgk, workspace)
+    _ok(_load().chain_qk_norm_rope_bwd(_fdesc(dQo), _fdesc(dKo), _fdesc(Q), _fdesc(K), _fdesc(gq),
+                                       _fdesc(gk), None if inv_freq is None else _fdesc(inv_freq),
+                                       _positions(positions,
+                                                  Q.numel() // max(1, Q.shape[-1] * Q.shape[-2])),
+                                       eps, pairs, _fdesc(dQ), _fdesc(dK), _fdesc(dgq), _fdesc(dgk),
+                                       workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                       _stream(stream)), "chain_qk_norm_rope_bwd")
+
+
+def chain_paged_append(K, V, cu_seqlens, kv_lens, page_table, Kc, Vc, stream=None):
+    """Writes the new tokens' K and V into their pages; see include/chain.h."""
+    _on_current_device(K, V, cu_seqlens, kv_lens, page_table, Kc, Vc)
+    _ok(_load().chain_paged_append(_fdesc(K), _fdesc(V), *_paged(cu_seqlens, kv_lens, page_table),
+                                   _fdesc(Kc), _fdesc(Vc), _stream(stream)), "chain_paged_append")
+
+
+def chain_qk_norm_rope_append(Q, K, V, gq, gk, inv_freq, eps, pairs, cu_seqlens, kv_lens, page_table, Kc,
+                              Vc, Qo, stream=None):
+    """chain_qk_norm_rope at the tokens' cache positions with K and V written
+    into their pages; see include/chain.h."""
+    _on_current_device(Q, K, V, gq, gk, inv_freq, cu_seqlens, kv_lens, page_table, Kc, Vc, Qo)
+    _ok(_load().chain_qk_norm_rope_append(_fdesc(Q), _fdesc(K), _fdesc(V), _fdesc(gq), _fdesc(gk),
+                                          None if inv_freq is None else _fdesc(inv_freq), eps, pairs,
+                                          *_paged(cu_seqlens, kv_lens, page_table), _fdesc(Kc), _fdesc(Vc),
+                                          _fdesc(Qo), _stream(stream)), "chain_qk_norm_rope_append")
+
+
+def chain_fwd_paged_workspace_size(Q, Kc) -> int:
+    return int(_load().chain_fwd_paged_workspace_size(_fdesc(Q), _fdesc(Kc)))
+
+
+def chain_fwd_paged(Q, Kc, Vc, cu_seqlens, kv_lens, page_table, mask, scale, O, LSE, workspace,
+                    stream=None):
+    """Attention of a chunk of new tokens over a paged cache; see include/chain.h."""
+    _on_current_device(Q, Kc, Vc, cu_seqlens, kv_lens, page_table, O, LSE, workspace)
+    _ok(_load().chain_fwd_paged(_fdesc(Q), _fdesc(Kc), _fdesc(Vc),
+                                *_paged(cu_seqlens, kv_lens, page_table), mask, scale, _fdesc(O),
+                                _fdesc(LSE), workspace.data_ptr(),
+                                workspace.numel() * workspace.element_size(), _stream(stream)),
+        "chain_fwd_paged")
+
+
 def sp_relayout(shards, p, head_group, out, stream=None):
     _ok(_load().sp_relayout(_ref(desc(shards)), int(p), int(head_group), _ref(desc(out)),
                             _stream(stream)), "sp_relayout")
@@ -496,3 +635,58 @@ def relayout(shards, p: int, head_group: int, stream=None):
     out = torch.empty(H // p, p * n_loc, d, dtype=shards.dtype, device=shards.device)
     sp_relayout(shards, p, head_group, out, stream)
     return out
+
+
+def _dense_like(t):
+    return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
+def qk_norm_rope(q, k, gq, gk, inv_freq, positions=None, eps: float = 1e-6, interleaved: bool = False,
+                 stream=None):
+    """RMS norm and rotary embedding of q [T, H, d] and k [T, Hkv, d] (or
+    [B, n, heads, d]), any head and token strides.  Returns dense (q, k)."""
+    qo, ko = _dense_like(q), _dense_like(k)
+    chain_qk_norm_rope(q, k, gq, gk, inv_freq, positions, eps, int(interleaved), qo, ko, stream)
+    return qo, ko
+
+
+def qk_norm_rope_bwd(dqo, dko, q, k, gq, gk, inv_freq, positions=None, eps: float = 1e-6,
+                     interleaved: bool = False, workspace=None, stream=None):
+    """Gradients of qk_norm_rope: returns (dq, dk, dgq, dgk), dgq and dgk f32."""
+    dq, dk = _dense_like(q), _dense_like(k)
+    dg = torch.empty(2, q.shape[-1], dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = torch.empty(max(chain_qk_norm_rope_bwd_workspace_size(q), 16), dtype=torch.uint8,
+                                device=q.device)
+    dgq, dgk = dg[0], dg[1]
+    chain_qk_norm_rope_bwd(dqo, dko, q, k, gq, gk, inv_freq, positions, eps, int(interleaved), dq, dk,
+                           dgq, dgk, workspace, stream)
+    return dq, dk, dgq, dgk
+
+
+def qk_norm_rope_append(q, k, v, gq, gk, inv_freq, k_cache, v_cache, cu_seqlens, kv_lens, page_table,
+                        eps: float = 1e-6, interleaved: bool = False, stream=None):
+    """qk_norm_rope of packed new tokens q [total, H, d], k, v [total, Hkv, d]
+    at their cache positions; the rotated k and v go into their pages of
+    k_cache, v_cache [pages, page, Hkv, d].  Returns the rotated q (rows behind
+    the last sequence are not written)."""
+    qo = _dense_like(q)
+    chain_qk_norm_rope_append(q, k, v, gq, gk, inv_freq, eps, int(interleaved), cu_seqlens, kv_lens,
+                              page_table, k_cache, v_cache, qo, stream)
+    return qo
+
+
+def attention_fwd_paged(q, k_cache, v_cache, cu_seqlens, kv_lens, page_table, causal: bool,
+                        scale: float | None = None, workspace=None, stream=None):
+    """Packed new tokens q [total, H, d] over a paged cache that already holds
+    them.  Returns (O [total, H, d], LSE [H, total]); rows behind the last
+    sequence are not written."""
+    scale = q.shape[-1] ** -0.5 if scale is None else scale
+    o = _dense_like(q)
+    lse = torch.empty(q.shape[1], q.shape[0], dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = torch.empty(max(chain_fwd_paged_workspace_size(q, k_cache), 16), dtype=torch.uint8,
+                                device=q.device)
+    chain_fwd_paged(q, k_cache, v_cache, cu_seqlens, kv_lens, page_table,
+                    MASK_CAUSAL if causal else MASK_NONE, scale, o, lse, workspace, stream)
+    return o, lse

@@ -893,6 +893,293 @@ int chain_fwd_fp8(const chain_tensor_t *Q, const chain_tensor_t *K, const chain_
   return e == cudaSuccess ? CHAIN_OK : cuda_fail(e);
 }
 
+// ------------------------------------------- norm + rotation, paged cache
+// [T][heads][d] or [B][n][heads][d], d contiguous, the other strides positive
+// multiples of 16 bytes (any where the extent is 1).  Tokens count B n.
+static int heads_view(const chain_tensor_t *t, int max_nd, NormRopeSide *s, int64_t *batch, int64_t *n,
+                      int64_t *heads, int64_t *d) {
+  if (!t || t->ndim < 3 || t->ndim > max_nd) return CHAIN_ERR_ARG;
+  if (t->dtype != CHAIN_BF16 && t->dtype != CHAIN_F32) return CHAIN_ERR_DTYPE;
+  const int nd = t->ndim, es = esize(t->dtype);
+  for (int i = 0; i < nd; ++i)
+    if (t->shape[i] < 0) return CHAIN_ERR_ARG;
+  *batch = nd == 4 ? t->shape[0] : 1;
+  *n = t->shape[nd - 3];
+  *heads = t->shape[nd - 2];
+  *d = t->shape[nd - 1];
+  s->ptr = t->ptr;
+  s->s_batch = s->s_tok = s->s_head = 0;
+  if (*d != 64 && *d != 128) return CHAIN_ERR_ARG;
+  if (*heads < 1 || *heads > 65535 || *n > (1 << 30) || *batch > (1 << 30) || *batch * *n > (1 << 30))
+    return CHAIN_ERR_ARG;
+  if (*batch == 0 || *n == 0) return CHAIN_OK;  // no tokens: the pointer may be null
+  if (!t->ptr || !aligned16(t->ptr) || t->stride[nd - 1] != 1) return CHAIN_ERR_ARG;
+  for (int i = 0; i + 1 < nd; ++i)
+    if (t->shape[i] > 1 && (t->stride[i] <= 0 || (t->stride[i] * es) % 16 ||
+                            t->stride[i] > (int64_t(1) << 40)))
+      return CHAIN_ERR_ARG;
+  if (nd == 4 && *batch > 1) s->s_batch = t->stride[0];
+  if (*n > 1) s->s_tok = t->stride[nd - 3];
+  if (*heads > 1) s->s_head = t->stride[nd - 2];
+  return CHAIN_OK;
+}
+
+static int norm_weight(const chain_tensor_t *t, int64_t d, NormRopeWeight *w) {
+  if (!t || !t->ptr || t->ndim != 1 || t->shape[0] != d || t->stride[0] != 1) return CHAIN_ERR_ARG;
+  if (t->dtype != CHAIN_BF16 && t->dtype != CHAIN_F32) return CHAIN_ERR_DTYPE;
+  if (!aligned16(t->ptr)) return CHAIN_ERR_ARG;
+  w->ptr = t->ptr;
+  w->bf16 = t->dtype == CHAIN_BF16;
+  return CHAIN_OK;
+}
+
+// inv_freq [rot/2] f32, or null for no rotation
+static int rope_freq(const chain_tensor_t *t, int64_t d, const float **f, int *rot) {
+  *f = nullptr;
+  *rot = 0;
+  if (!t) return CHAIN_OK;
+  if (t->dtype != CHAIN_F32) return CHAIN_ERR_DTYPE;
+  if (!t->ptr || t->ndim != 1 || t->shape[0] < 1 || t->shape[0] * 2 > d || t->shape[0] % 8)
+    return CHAIN_ERR_ARG;
+  if (t->stride[0] != 1 || (reinterpret_cast<uintptr_t>(t->ptr) & 3u)) return CHAIN_ERR_ARG;
+  *f = static_cast<const float *>(t->ptr);
+  *rot = (int)t->shape[0] * 2;
+  return CHAIN_OK;
+}
+
+static bool valid_eps(float eps) { return eps > 0.0f && eps < 1e30f; }
+
+static bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// The arguments the forward and the backward share; `qs` and `ks` are tensors
+// that have Q's and K's shapes (qs[0], ks[0] = Q, K; qs[1], ks[1] = outputs).
+static int norm_rope_args(const chain_tensor_t *const *qs, const chain_tensor_t *const *ks, int count,
+                          const chain_tensor_t *gq, const chain_tensor_t *gk,
+                          const chain_tensor_t *inv_freq, const int32_t *positions, float eps, int pairs,
+                          NormRopeSide *qv, NormRopeSide *kv, NormRopeArgs *a) {
+  if (pairs != CHAIN_PAIRS_HALF && pairs != CHAIN_PAIRS_NEIGHBOUR) return CHAIN_ERR_ARG;
+  if (!valid_eps(eps)) return CHAIN_ERR_ARG;
+  int64_t B = 0, n = 0, H = 0, Hkv = 0, d = 0;
+  for (int i = 0; i < count; ++i) {
+    int64_t b1, n1, h1, d1, b2, n2, h2, d2;
+    int rc;
+    if ((rc = heads_view(qs[i], 4, &qv[i], &b1, &n1, &h1, &d1)) ||
+        (rc = heads_view(ks[i], 4, &kv[i], &b2, &n2, &h2, &d2)))
+      return rc;
+    if (qs[i]->dtype != qs[0]->dtype || ks[i]->dtype != qs[0]->dtype) return CHAIN_ERR_DTYPE;
+    if (i == 0) {
+      B = b1; n = n1; H = h1; Hkv = h2; d = d1;
+    }
+    if (qs[i]->ndim != qs[0]->ndim || ks[i]->ndim != qs[0]->ndim || b1 != B || b2 != B || n1 != n ||
+        n2 != n || h1 != H || h2 != Hkv || d1 != d || d2 != d)
+      return CHAIN_ERR_ARG;
+  }
+  int rc;
+  if ((rc = norm_weight(gq, d, &a->gq)) || (rc = norm_weight(gk, d, &a->gk)) ||
+      (rc = rope_freq(inv_freq, d, &a->inv_freq, &a->rot)))
+    return rc;
+  if (!aligned4(positions)) return CHAIN_ERR_ARG;
+  a->q = qv[0]; a->k = kv[0]; a->qo = qv[1]; a->ko = kv[1];
+  a->positions = positions;
+  a->tokens = B * n; a->n = n;
+  a->H = (int)H; a->Hkv = (int)Hkv; a->d = (int)d;
+  a->neighbour = pairs == CHAIN_PAIRS_NEIGHBOUR; a->f32 = qs[0]->dtype == CHAIN_F32; a->eps = eps;
+  return CHAIN_OK;
+}
+
+int chain_qk_norm_rope(const chain_tensor_t *Q, const chain_tensor_t *K, const chain_tensor_t *gq,
+                       const chain_tensor_t *gk, const chain_tensor_t *inv_freq,
+                       const int32_t *positions, float eps, int pairs, chain_tensor_t *Qo,
+                       chain_tensor_t *Ko, void *stream) {
+  const chain_tensor_t *qs[2] = {Q, Qo}, *ks[2] = {K, Ko};
+  NormRopeSide qv[2], kv[2];
+  NormRopeArgs a;
+  int rc = norm_rope_args(qs, ks, 2, gq, gk, inv_freq, positions, eps, pairs, qv, kv, &a);
+  if (rc) return rc;
+  if (a.tokens == 0) return CHAIN_OK;
+  DevInfo *di = nullptr;
+  if ((rc = device_ready(&di))) return rc;
+  cudaError_t e = launch_norm_rope(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? CHAIN_OK : cuda_fail(e);
+}
+
+static size_t norm_rope_ws(int64_t d) { return (size_t)kNormRopeBwdMaxGrid * 2 * d * sizeof(float); }
+
+size_t chain_qk_norm_rope_bwd_workspace_size(const chain_tensor_t *Q) {
+  NormRopeSide s;
+  int64_t b, n, h, d;
+  if (heads_view(Q, 4, &s, &b, &n, &h, &d)) return 0;
+  return norm_rope_ws(d);
+}
+
+int chain_qk_norm_rope_bwd(const chain_tensor_t *dQo, const chain_tensor_t *dKo, const chain_tensor_t *Q,
+                           const chain_tensor_t *K, const chain_tensor_t *gq, const chain_tensor_t *gk,
+                           const chain_tensor_t *inv_freq, const int32_t *positions, float eps, int pairs,
+                           chain_tensor_t *dQ, chain_tensor_t *dK, chain_tensor_t *dgq,
+                           chain_tensor_t *dgk, void *workspace, size_t ws_bytes, void *stream) {
+  const chain_tensor_t *qs[3] = {Q, dQ, dQo}, *ks[3] = {K, dK, dKo};
+  NormRopeSide qv[3], kv[3];
+  NormRopeBwdArgs b;
+  int rc = norm_rope_args(qs, ks, 3, gq, gk, inv_freq, positions, eps, pairs, qv, kv, &b.fwd);
+  if (rc) return rc;
+  for (const chain_tensor_t *g : {dgq, dgk}) {
+    if (!g || !g->ptr || g->ndim != 1 || g->shape[0] != b.fwd.d || g->stride[0] != 1) return CHAIN_ERR_ARG;
+    if (g->dtype != CHAIN_F32) return CHAIN_ERR_DTYPE;
+    if (!aligned4(g->ptr)) return CHAIN_ERR_ARG;
+  }
+  if (!workspace || !aligned16(workspace) || ws_bytes < norm_rope_ws(b.fwd.d)) return CHAIN_ERR_ARG;
+  b.dqo = qv[2]; b.dko = kv[2];
+  b.dgq = static_cast<float *>(dgq->ptr); b.dgk = static_cast<float *>(dgk->ptr);
+  b.workspace = workspace;
+  DevInfo *di = nullptr;
+  if ((rc = device_ready(&di))) return rc;
+  cudaError_t e = launch_norm_rope_bwd(b, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? CHAIN_OK : cuda_fail(e);
+}
+
+// [num_pages][page][Hkv][d] bf16 pool
+static int pool_view(const chain_tensor_t *t, PagedSide *s, int64_t (&shape)[4]) {
+  if (!t || !t->ptr || t->ndim != 4) return CHAIN_ERR_ARG;
+  if (t->dtype != CHAIN_BF16) return CHAIN_ERR_DTYPE;
+  for (int i = 0; i < 4; ++i) shape[i] = t->shape[i];
+  if (shape[0] < 1 || shape[0] > 0x7ffffffe || shape[1] < 1 || shape[2] < 1 || shape[2] > 65535 ||
+      (shape[3] != 64 && shape[3] != 128) || t->stride[3] != 1 || !aligned16(t->ptr))
+    return CHAIN_ERR_ARG;
+  int64_t st[3];
+  for (int i = 0; i < 3; ++i) {
+    st[i] = t->stride[i];
+    if (shape[i] == 1) st[i] = shape[3];  // any value is allowed there: a valid one for the tensor map
+    if (st[i] < shape[3] || (st[i] * 2) % 16 || st[i] * 2 >= (int64_t(1) << 40)) return CHAIN_ERR_ARG;
+  }
+  s->ptr = t->ptr;
+  s->s_page = st[0]; s->s_slot = st[1]; s->s_head = st[2];
+  if (shape[1] < 16 || shape[1] > 1024 || (shape[1] & (shape[1] - 1))) return CHAIN_ERR_UNSUPPORTED;
+  return CHAIN_OK;
+}
+
+static int paged_seqs(const int32_t *cu, const int32_t *lens, const int32_t *table, int64_t stride,
+                      int batch, int max_pages, const int64_t (&pool)[4], PagedSeqs *s) {
+  if (batch < 0 || batch > (1 << 20) || max_pages < 0) return CHAIN_ERR_ARG;
+  s->cu = cu; s->lens = lens; s->table = table; s->table_stride = stride;
+  s->batch = batch; s->max_pages = max_pages; s->num_pages = pool[0];
+  s->page_shift = 0;
+  while ((int64_t(1) << s->page_shift) < pool[1]) ++s->page_shift;
+  if (batch == 0) return CHAIN_OK;
+  if (!cu || !lens || !table || !aligned4(cu) || !aligned4(lens) || !aligned4(table)) return CHAIN_ERR_ARG;
+  if (max_pages < 1 || (batch > 1 && stride < max_pages) || stride < 0) return CHAIN_ERR_ARG;
+  if (((int64_t)max_pages << s->page_shift) > (1 << 30)) return CHAIN_ERR_ARG;
+  return CHAIN_OK;
+}
+
+static int append_common(const chain_tensor_t *Q, const chain_tensor_t *K, const chain_tensor_t *V,
+                         const chain_tensor_t *gq, const chain_tensor_t *gk,
+                         const chain_tensor_t *inv_freq, float eps, int pairs, const int32_t *cu,
+                         const int32_t *lens, const int32_t *table, int64_t stride, int batch,
+                         int max_pages, const chain_tensor_t *Kc, const chain_tensor_t *Vc,
+                         const chain_tensor_t *Qo, int norm, void *stream) {
+  AppendArgs a = {};
+  int64_t b1, total, Hkv, d, n2, h2, d2;
+  int rc;
+  const chain_tensor_t *all[4] = {K, V, Q, Qo};
+  NormRopeSide *side[4] = {&a.k, &a.v, &a.q, &a.qo};
+  a.H = 0;
+  for (int i = 0; i < (norm ? 4 : 2); ++i) {
+    if ((rc = heads_view(all[i], 3, side[i], &b1, &n2, &h2, &d2))) return rc;
+    if (all[i]->dtype != CHAIN_BF16) return CHAIN_ERR_DTYPE;
+    if (i == 0) {
+      total = n2; Hkv = h2; d = d2;
+    }
+    if (i == 2) a.H = (int)h2;
+    if (n2 != total || d2 != d || h2 != (i < 2 ? Hkv : a.H)) return CHAIN_ERR_ARG;
+  }
+  int64_t pk[4], pv[4];
+  if ((rc = pool_view(Kc, &a.kc, pk)) || (rc = pool_view(Vc, &a.vc, pv))) return rc;
+  for (int i = 0; i < 4; ++i)
+    if (pk[i] != pv[i]) return CHAIN_ERR_ARG;
+  if (pk[2] != Hkv || pk[3] != d) return CHAIN_ERR_ARG;
+  if (norm) {
+    if (pairs != CHAIN_PAIRS_HALF && pairs != CHAIN_PAIRS_NEIGHBOUR) return CHAIN_ERR_ARG;
+    if (!valid_eps(eps)) return CHAIN_ERR_ARG;
+    if ((rc = norm_weight(gq, d, &a.gq)) || (rc = norm_weight(gk, d, &a.gk)) ||
+        (rc = rope_freq(inv_freq, d, &a.inv_freq, &a.rot)))
+      return rc;
+  }
+  if ((rc = paged_seqs(cu, lens, table, stride, batch, max_pages, pk, &a.seqs))) return rc;
+  if (total == 0 || batch == 0) return CHAIN_OK;
+  a.tokens = total; a.Hkv = (int)Hkv; a.d = (int)d;
+  a.neighbour = pairs == CHAIN_PAIRS_NEIGHBOUR; a.norm = norm; a.eps = eps;
+  DevInfo *di = nullptr;
+  if ((rc = device_ready(&di))) return rc;
+  a.status = di->status;
+  cudaError_t e = launch_append(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? CHAIN_OK : cuda_fail(e);
+}
+
+int chain_paged_append(const chain_tensor_t *K, const chain_tensor_t *V, const int32_t *cu_seqlens,
+                       const int32_t *kv_lens, const int32_t *page_table, int64_t page_table_stride,
+                       int batch, int max_pages, chain_tensor_t *Kc, chain_tensor_t *Vc, void *stream) {
+  return append_common(nullptr, K, V, nullptr, nullptr, nullptr, 0.0f, 0, cu_seqlens, kv_lens, page_table,
+                       page_table_stride, batch, max_pages, Kc, Vc, nullptr, 0, stream);
+}
+
+int chain_qk_norm_rope_append(const chain_tensor_t *Q, const chain_tensor_t *K, const chain_tensor_t *V,
+                              const chain_tensor_t *gq, const chain_tensor_t *gk,
+                              const chain_tensor_t *inv_freq, float eps, int pairs,
+                              const int32_t *cu_seqlens, const int32_t *kv_lens,
+                              const int32_t *page_table, int64_t page_table_stride, int batch,
+                              int max_pages, chain_tensor_t *Kc, chain_tensor_t *Vc, chain_tensor_t *Qo,
+                              void *stream) {
+  return append_common(Q, K, V, gq, gk, inv_freq, eps, pairs, cu_seqlens, kv_lens, page_table,
+                       page_table_stride, batch, max_pages, Kc, Vc, Qo, 1, stream);
+}
+
+size_t chain_fwd_paged_workspace_size(const chain_tensor_t *Q, const chain_tensor_t *Kc) {
+  NormRopeSide s;
+  PagedSide p;
+  int64_t b, n, H, d, pool[4];
+  if (heads_view(Q, 3, &s, &b, &n, &H, &d) || Q->dtype != CHAIN_BF16 || pool_view(Kc, &p, pool)) return 0;
+  if (pool[3] != d || H % pool[2] || H / pool[2] > 128) return 0;
+  return paged_attn_workspace((int)d);
+}
+
+int chain_fwd_paged(const chain_tensor_t *Q, const chain_tensor_t *Kc, const chain_tensor_t *Vc,
+                    const int32_t *cu_seqlens, const int32_t *kv_lens, const int32_t *page_table,
+                    int64_t page_table_stride, int batch, int max_pages, int mask, float scale,
+                    chain_tensor_t *O, chain_tensor_t *LSE, void *workspace, size_t ws_bytes,
+                    void *stream) {
+  if (mask != CHAIN_MASK_NONE && mask != CHAIN_MASK_CAUSAL) return CHAIN_ERR_ARG;
+  if (!(scale > 0.0f) || !(scale < 1e30f)) return CHAIN_ERR_ARG;
+  PagedAttnArgs a;
+  NormRopeSide q, o;
+  int64_t b1, total, H, d, n2, h2, d2, pk[4], pv[4];
+  int rc;
+  if ((rc = heads_view(Q, 3, &q, &b1, &total, &H, &d)) || (rc = heads_view(O, 3, &o, &b1, &n2, &h2, &d2)))
+    return rc;
+  if (Q->dtype != CHAIN_BF16 || O->dtype != CHAIN_BF16) return CHAIN_ERR_DTYPE;
+  if (n2 != total || h2 != H || d2 != d) return CHAIN_ERR_ARG;
+  if ((rc = pool_view(Kc, &a.kc, pk)) || (rc = pool_view(Vc, &a.vc, pv))) return rc;
+  for (int i = 0; i < 4; ++i)
+    if (pk[i] != pv[i]) return CHAIN_ERR_ARG;
+  if (pk[3] != d || H % pk[2]) return CHAIN_ERR_ARG;
+  if ((rc = paged_seqs(cu_seqlens, kv_lens, page_table, page_table_stride, batch, max_pages, pk, &a.seqs)))
+    return rc;
+  if (H / pk[2] > 128 || batch > 8192) return CHAIN_ERR_UNSUPPORTED;
+  if (total == 0 || batch == 0) return CHAIN_OK;
+  int64_t lse_shead = 0;
+  if ((rc = lse_view(LSE, H, total, &lse_shead))) return rc;
+  if (!workspace || !aligned16(workspace) || ws_bytes < paged_attn_workspace((int)d)) return CHAIN_ERR_ARG;
+  a.Q = q.ptr; a.q_stok = q.s_tok; a.q_shead = q.s_head;
+  a.O = o.ptr; a.o_stok = o.s_tok; a.o_shead = o.s_head;
+  a.LSE = static_cast<float *>(LSE->ptr); a.lse_shead = lse_shead;
+  a.total = (int)total; a.H = (int)H; a.Hkv = (int)pk[2]; a.d = (int)d;
+  a.causal = mask == CHAIN_MASK_CAUSAL; a.scale = scale; a.workspace = workspace;
+  DevInfo *di = nullptr;
+  if ((rc = device_ready(&di))) return rc;
+  cudaError_t e = launch_paged_attn(a, wait_cfg(di), static_cast<cudaStream_t>(stream));
+  if (e == cudaErrorNotSupported) return CHAIN_ERR_UNSUPPORTED;
+  return e == cudaSuccess ? CHAIN_OK : cuda_fail(e);
+}
+
 int sp_relayout(const chain_tensor_t *shards, int p, int head_group, chain_tensor_t *out,
                 void *stream) {
   return relayout_common(shards, out, p, head_group, 0, stream);

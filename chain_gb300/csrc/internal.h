@@ -68,6 +68,78 @@ struct AttnBwdArgs {
 };
 cudaError_t launch_attn_bwd(const AttnBwdArgs &a, const WaitCfg &wc, cudaStream_t st);
 
+// ---- norm + rotation of queries and keys, paged cache (qk_norm_rope.cu,
+// paged_attn.cu)
+
+// One operand [tokens][heads][d], tokens optionally as [B][n]: element strides.
+struct NormRopeSide {
+  void *ptr;
+  int64_t s_batch, s_tok, s_head;
+};
+struct NormRopeWeight {
+  const void *ptr;  // [d]
+  int bf16;         // else f32
+};
+struct NormRopeArgs {
+  NormRopeSide q, k, qo, ko;  // the backward: q, k inputs, qo, ko = dQ, dK
+  NormRopeWeight gq, gk;
+  const float *inv_freq;  // [rot / 2]
+  const int *positions;   // [tokens], or null: the index in its batch entry
+  int64_t tokens, n;      // n: tokens a batch entry (tokens when there is one)
+  int H, Hkv, d, rot, neighbour, f32;
+  float eps;
+};
+cudaError_t launch_norm_rope(const NormRopeArgs &a, cudaStream_t st);
+struct NormRopeBwdArgs {
+  NormRopeArgs fwd;
+  NormRopeSide dqo, dko;
+  float *dgq, *dgk;  // [d]
+  void *workspace;   // kNormRopeBwdMaxGrid x 2 x d floats
+};
+constexpr int kNormRopeBwdMaxGrid = 152 * 4;
+cudaError_t launch_norm_rope_bwd(const NormRopeBwdArgs &b, cudaStream_t st);
+
+// Sequences of a paged cache: sequence b's new tokens are rows [cu[b],
+// cu[b+1]) of the packed tensors, its cache holds lens[b] positions, position
+// p in page table[b][p >> page_shift].  All three arrays are on the device.
+struct PagedSeqs {
+  const int *cu, *lens, *table;
+  int64_t table_stride;
+  int batch, max_pages, page_shift;
+  int64_t num_pages;
+};
+struct PagedSide {
+  void *ptr;
+  int64_t s_page, s_slot, s_head;  // elements
+};
+struct AppendArgs {
+  NormRopeSide q, k, v, qo;  // q, qo unused without norm
+  PagedSide kc, vc;
+  NormRopeWeight gq, gk;
+  const float *inv_freq;
+  PagedSeqs seqs;
+  int64_t tokens;
+  int H, Hkv, d, rot, neighbour, norm;
+  float eps;
+  DevStatus *status;
+};
+cudaError_t launch_append(const AppendArgs &a, cudaStream_t st);
+
+struct PagedAttnArgs {
+  const void *Q;
+  void *O;
+  int64_t q_stok, q_shead, o_stok, o_shead;
+  PagedSide kc, vc;
+  float *LSE;
+  int64_t lse_shead;
+  PagedSeqs seqs;
+  int total, H, Hkv, d, causal;
+  float scale;
+  void *workspace;
+};
+size_t paged_attn_workspace(int d);
+cudaError_t launch_paged_attn(const PagedAttnArgs &a, const WaitCfg &wc, cudaStream_t st);
+
 struct MlpBwdArgs {
   const void *X, *W1, *W2, *dO;  // [M][K], [K][N], [N][P], [M][P] bf16 row-major
   void *dX, *dW1, *dW2;          // [M][K], [K][N], [N][P] bf16

@@ -15,7 +15,10 @@
  *   - f = identity, O = (A B) C.
  * plus the Ulysses sequence-shard -> head-major relayout that precedes
  * attention ("Ulysses Sequence Parallelism", "Contexte Technique") and its
- * inverse (the second exchange of "Analyse et Implications").
+ * inverse (the second exchange of "Analyse et Implications"); and, beside the
+ * attention of a model that is trained or answers with it, the norm and
+ * position rotation of its queries and keys, and a paged K/V cache: its write
+ * and the attention of a chunk of new tokens over it.
  *
  * Conventions common to every entry point
  *  - Tensors are described by chain_tensor_t: a DEVICE pointer, an element
@@ -75,6 +78,10 @@ typedef enum {
 } chain_f_t;
 
 typedef enum { CHAIN_MASK_NONE = 0, CHAIN_MASK_CAUSAL = 1 } chain_mask_t;
+
+/* Which elements of a head the position rotation pairs, for rot rotated
+ * elements: HALF (i, i + rot/2), NEIGHBOUR (2i, 2i + 1), i < rot/2. */
+typedef enum { CHAIN_PAIRS_HALF = 0, CHAIN_PAIRS_NEIGHBOUR = 1 } chain_pairs_t;
 
 typedef struct {
   void *ptr;          /* device address of element [0, 0, ...] */
@@ -425,6 +432,150 @@ int chain_fwd_fp8(const chain_tensor_t *Q, const chain_tensor_t *K,
                   size_t ws_bytes, void *stream);
 
 /*
+ * chain_qk_norm_rope -- RMS norm of every query and key head with the rotary
+ * position embedding in the same pass: what lies between a model's
+ * projections and the Q and K of chain_fwd.  (An addition of this library:
+ * the method's write-ups have no counterpart.)  For a head x in R^d of the token at
+ * position p, with weight g and frequencies w_i, i < rot/2:
+ *   u = x g / sqrt(mean(x^2) + eps),   y = R(p) u,
+ * R(p) rotating the pairs that `pairs` names by the angle p w_i
+ * (y_a = u_a cos - u_b sin, y_b = u_a sin + u_b cos); elements from rot on
+ * are not rotated.
+ *   Q, Qo      [T][H][d], K, Ko [T][Hkv][d]; or 4-D [B][n][heads][d].  All of one
+ *              type, bf16 or f32; d = 64 or 128, contiguous; each tensor has
+ *              its own other strides, multiples of 16 bytes and positive, so views
+ *              of one fused projection are taken, and head-major tensors
+ *              through their transposed view.  Qo, Ko may be Q, K themselves
+ *              (same pointer and strides); otherwise no tensor written may
+ *              overlap another.
+ *   gq, gk     [d] weights, bf16 or f32, contiguous, 16-byte aligned.
+ *   inv_freq   [rot/2] f32, contiguous, |w| < 2^24; rot a multiple of 16,
+ *              at most d.  NULL: no rotation (positions are then ignored).
+ *   positions  DEVICE int32, one for each token in order, any value; NULL:
+ *              the token's index in its batch entry.
+ *   eps        > 0, finite.
+ * Arithmetic: fp32, one rounding to bf16 at the store; angles p w_i exact
+ * modulo a turn to within 2^-32 turns before their sine and cosine, at any
+ * int32 position.  T = 0 returns CHAIN_OK and launches nothing.  Returns
+ * CHAIN_ERR_DTYPE for other or mixed types, CHAIN_ERR_ARG for a shape,
+ * stride, alignment or value violation.  Asynchronous on `stream`.
+ */
+int chain_qk_norm_rope(const chain_tensor_t *Q, const chain_tensor_t *K,
+                       const chain_tensor_t *gq, const chain_tensor_t *gk,
+                       const chain_tensor_t *inv_freq, const int32_t *positions, float eps,
+                       int pairs, chain_tensor_t *Qo, chain_tensor_t *Ko, void *stream);
+
+/*
+ * chain_qk_norm_rope_bwd -- gradients of chain_qk_norm_rope.  With
+ * a = R(p)^T dy, h = a g, r = 1 / sqrt(mean(x^2) + eps):
+ *   dx = r (h - x r^2 mean(h x)),   dg = sum over tokens and heads of a x r.
+ *   dQo, dKo   gradients of Qo, Ko; Q, K, gq, gk, inv_freq, positions, eps,
+ *              pairs as given to the forward (r is recomputed from Q and K).
+ *   dQ, dK     shaped and typed as Q, K, strides of their own.  They may be
+ *              dQo, dKo or Q, K themselves (same pointer and strides).
+ *   dgq, dgk   [d] f32, contiguous, 4-byte aligned; written, not added to.
+ *   workspace  at least chain_qk_norm_rope_bwd_workspace_size(Q) bytes,
+ *              16-byte aligned, contents ignored on entry.
+ * No atomics: results are deterministic.  T = 0 writes zeros to dgq and dgk.  Errors
+ * as for chain_qk_norm_rope; chain_qk_norm_rope_bwd_workspace_size returns 0
+ * for a Q it cannot take.
+ */
+size_t chain_qk_norm_rope_bwd_workspace_size(const chain_tensor_t *Q);
+int chain_qk_norm_rope_bwd(const chain_tensor_t *dQo, const chain_tensor_t *dKo,
+                           const chain_tensor_t *Q, const chain_tensor_t *K,
+                           const chain_tensor_t *gq, const chain_tensor_t *gk,
+                           const chain_tensor_t *inv_freq, const int32_t *positions, float eps,
+                           int pairs, chain_tensor_t *dQ, chain_tensor_t *dK,
+                           chain_tensor_t *dgq, chain_tensor_t *dgk, void *workspace,
+                           size_t ws_bytes, void *stream);
+
+/*
+ * A paged K/V cache (chain_paged_append, chain_qk_norm_rope_append,
+ * chain_fwd_paged; additions of this library) is two pools of pages,
+ *   Kc, Vc     [num_pages][page][Hkv][d] bf16, page a power of two from 16 to
+ *              1024 (else CHAIN_ERR_UNSUPPORTED), d = 64 or 128, contiguous.  The
+ *              other strides are multiples of 16 bytes, positive and in any order of
+ *              size, so a pool laid out [num_pages][Hkv][page][d] is passed
+ *              through its transposed view.
+ * and, for `batch` sequences, three DEVICE int32 arrays, 4-byte aligned:
+ *   cu_seqlens [batch + 1]  sequence b's new tokens are rows [cu_seqlens[b],
+ *              cu_seqlens[b+1]) of the packed tensors; nondecreasing, first
+ *              0; clamped to the packed rows.  Rows from cu_seqlens[batch]
+ *              on are left as they were.
+ *   kv_lens    [batch]  cached positions of sequence b, its new tokens
+ *              included: new token i of n_b is position kv_lens[b] - n_b + i.
+ *   page_table [batch][max_pages], rows page_table_stride elements apart:
+ *              position p of sequence b is slot p % page of page
+ *              page_table[b][p / page].  Only the entries of positions below
+ *              kv_lens[b] are read.
+ * What only the device can see is checked there and reported by the next
+ * chain_check() as CHAIN_ERR_ARG, never accessed: a page index outside
+ * [0, num_pages), kv_lens[b] below 0 or above max_pages * page.
+ */
+
+/*
+ * chain_paged_append -- writes the new tokens' K and V into their pages.
+ *   K, V       [total][Hkv][d] bf16, d contiguous, other strides positive
+ *              multiples of 16 bytes, 16-byte aligned.
+ * A token whose position is negative, or whose page is missing, is not
+ * written and is reported.  Slots of other positions are left as they were.
+ * Two tokens of one call must not name the same slot.  total = 0 or batch = 0
+ * returns CHAIN_OK and launches nothing.  Asynchronous on `stream`.
+ */
+int chain_paged_append(const chain_tensor_t *K, const chain_tensor_t *V,
+                       const int32_t *cu_seqlens, const int32_t *kv_lens,
+                       const int32_t *page_table, int64_t page_table_stride, int batch,
+                       int max_pages, chain_tensor_t *Kc, chain_tensor_t *Vc, void *stream);
+
+/*
+ * chain_qk_norm_rope_append -- chain_qk_norm_rope of the new tokens' queries
+ * and keys at their cache positions, with the rotated keys and the values
+ * written straight into their pages: chain_qk_norm_rope with positions
+ * kv_lens[b] - n_b + i, then chain_paged_append, in one pass.
+ *   Q, Qo      [total][H][d], K, V [total][Hkv][d] bf16, strides as above;
+ *              Qo may be Q.  gq, gk, inv_freq, eps, pairs as for chain_qk_norm_rope.
+ * Same results, bit for bit, as the two calls.  A token that cannot be
+ * written still gets its row of Qo.
+ */
+int chain_qk_norm_rope_append(const chain_tensor_t *Q, const chain_tensor_t *K,
+                              const chain_tensor_t *V, const chain_tensor_t *gq,
+                              const chain_tensor_t *gk, const chain_tensor_t *inv_freq, float eps,
+                              int pairs, const int32_t *cu_seqlens, const int32_t *kv_lens,
+                              const int32_t *page_table, int64_t page_table_stride, int batch,
+                              int max_pages, chain_tensor_t *Kc, chain_tensor_t *Vc,
+                              chain_tensor_t *Qo, void *stream);
+
+/*
+ * chain_fwd_paged -- softmax attention of a chunk of new tokens (one token
+ * of each sequence, a piece of a prompt, or a mix) over a paged K/V cache that
+ * already holds the new tokens' keys and values.
+ *   Q, O       [total][H][d] bf16, H a multiple of Hkv and H / Hkv at most
+ *              128 (else CHAIN_ERR_UNSUPPORTED): query head h attends K/V
+ *              head h / (H / Hkv).  O must not overlap another tensor.
+ *   LSE        [H][total] f32, natural log, scale included.
+ *   mask       CAUSAL: new token i of sequence b sees positions
+ *              j <= kv_lens[b] - n_b + i; NONE: every j < kv_lens[b].  A row
+ *              that sees no key gets O = 0 and LSE = -infinity.
+ *   scale      > 0, finite.
+ *   workspace  at least chain_fwd_paged_workspace_size(Q, Kc) bytes, 16-byte
+ *              aligned, contents ignored on entry; calls that may overlap on the
+ *              GPU need one each.
+ * Cached K and V must be finite at positions below kv_lens[b]; slots of later
+ * positions may hold anything, NaN included.  A missing page counts as keys and values of zeros.
+ * Arithmetic: Q K^T, the softmax's statistics and P V accumulate in fp32;
+ * P enters the P V product as bf16.  batch at most 8192 (else
+ * CHAIN_ERR_UNSUPPORTED).  total = 0 or batch = 0 returns CHAIN_OK and
+ * launches nothing.  Asynchronous on `stream`.
+ * chain_fwd_paged_workspace_size returns 0 for a Q or Kc it cannot take.
+ */
+size_t chain_fwd_paged_workspace_size(const chain_tensor_t *Q, const chain_tensor_t *Kc);
+int chain_fwd_paged(const chain_tensor_t *Q, const chain_tensor_t *Kc, const chain_tensor_t *Vc,
+                    const int32_t *cu_seqlens, const int32_t *kv_lens, const int32_t *page_table,
+                    int64_t page_table_stride, int batch, int max_pages, int mask, float scale,
+                    chain_tensor_t *O, chain_tensor_t *LSE, void *workspace, size_t ws_bytes,
+                    void *stream);
+
+/*
  * sp_relayout -- Ulysses sequence shards -> head-major for one head group
  * ("Ulysses Sequence Parallelism", "Contexte Technique": every position of
  * the sequence, a subset of the heads).
@@ -452,7 +603,8 @@ int sp_relayout_inverse(const chain_tensor_t *in, int p, int head_group,
  * chain_check -- synchronise `stream`, then read and clear the device
  * status word.  Returns CHAIN_ERR_TIMEOUT if a bounded wait expired in any
  * kernel since the last check, CHAIN_ERR_ARG if a kernel met an argument only
- * it could check (chain_fwd_varlen: a sequence longer than max_seqlen),
+ * it could check (chain_fwd_varlen: a sequence longer than max_seqlen; the
+ * paged cache: a missing page or a length out of range),
  * CHAIN_ERR_CUDA on a CUDA error, else 0.
  * `detail` (may be NULL) receives the code of the wait site that expired.
  */
