@@ -7,101 +7,865 @@
 // only j <= lens[b] - n_b + i under the causal mask.  A row that sees none
 // gets O = 0 and LSE = -inf.
 //
-// One block per (token, head): its four warps take every fourth key, each
-// with the running maximum and sum of its keys' softmax, and join at the end.
+// Rows.  The G = H / Hkv query heads of a K/V head share its keys, so a
+// 128-row query tile holds TPT = floor(128 / G) tokens times G heads (row
+// = token * G + head): one token of grouped heads reads each cached key
+// once.  A unit of work is one sequence, one K/V head and up to two tiles
+// (2 TPT tokens), over the 128-key tiles its last token sees.
+//
+// Split.  The lengths are on the device, so the work is dealt there: the
+// units' key tiles, laid end to end, are cut into one equal run for each of
+// the CTAS persistent blocks, whatever the mix of lengths.  A block works
+// through the units of its run; a unit cut by a run's end leaves partial
+// (O, m, l) in the workspace, which paged_combine_kernel joins.  A block has
+// at most two partial units, the first and the last of its run.
+//
+// Inside a block (384 threads, one block an SM):
+//   warps 0-3, 4-7  softmax of streams 0 and 1, one row a thread, as in the
+//              forward kernels: S from tensor memory, running maximum and sum in
+//              fp32, P back into S's columns as bf16, O rescaled only when the
+//              maximum grew by 2^8.  P's rounding (2^-9 of each weight at
+//              most, unbiased) is below O's own once summed over keys, and one
+//              bf16 product costs half of a compensated pair; l sums the unrounded P.
+//   warp 8     TMA producer: Q tiles, then K and V tiles through one ring of
+//              NS tile slots in the order K0 V0 K1 V1 ...; a tile of 128 keys is
+//              128 / page boxes, their pages looked up one tile ahead, one lane a box.
+//   warp 9     MMA issuer.
+//   warp 10    scheduler: finds the run's units and hands them to the other
+//              warps through a small ring.
+// Two streams share the tensor core, so that one multiplies while the other
+// exponentiates.  With more than TPT tokens the streams are the unit's two
+// query tiles over the same keys; with fewer (single tokens, short chunks) they are
+// its even and odd key tiles for one query tile, joined before the store.
+// Tensor memory: S0/P0 [0,128), S1/P1 [128,256), O0 [256,384), O1 [384,512).
 #include "internal.h"
 
 namespace chain {
 namespace {
 
+constexpr int BM = 128, BN = 128;
+constexpr int CTAS = 152;     // one block on each SM
+constexpr int THREADS = 384;
+constexpr int NU = 4;         // units in flight between the scheduler and the other warps
+constexpr int MAX_BATCH = 8192;
+constexpr uint32_t REGS_SOFTMAX = 184, REGS_CONTROL = 136;  // 256 x 184 + 128 x 136 = 384 x 168
+constexpr float RESCALE_THRESHOLD = 8.0f;                   // log2 units
+
+enum : int {
+  SITE_PAGED_PROD = 0x601,
+  SITE_PAGED_MMA = 0x602,
+  SITE_PAGED_SOFTMAX = 0x603,
+  SITE_PAGED_EPI = 0x604,
+  SITE_PAGED_SCHED = 0x605,
+  SITE_PAGED_DRAIN = 0x606
+};
+
+// One unit's part of a block's run, as the scheduler hands it over.
+struct Unit {
+  int tok0, ntok;  // packed rows
+  int head, b;     // K/V head (-1: no more units), sequence
+  int j0, j1;      // key tiles
+  int ja;          // end of the key tiles that tile 0 sees
+  int lim0;        // keys that the first token sees (any value up to len)
+  int len;         // keys of the sequence
+  int slot;        // -1: all of the unit's key tiles, else the workspace slot
+};
+static_assert(sizeof(Unit) <= 48, "unit ring");
+
+// Where a run begins, for the join: written by every block, valid or not.
+struct Boundary {
+  long long u0, u1;  // first and last+1 key tile of the unit it falls into
+  long long total;   // all key tiles
+  int cut;           // it falls inside a unit
+  int tok0, ntok, head;
+};
+
 template <int D>
-__global__ void __launch_bounds__(128) paged_attn_kernel(const PagedAttnArgs a, DevStatus *status) {
-  constexpr int E = D / 32;  // elements a lane
-  __shared__ float sm[4], sl[4], so[4][D];
-  const PagedSeqs &s = a.seqs;
-  const int t = blockIdx.x, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int b = 0, e = s.batch;
-  while (e - b > 1) {
-    const int m = (b + e) >> 1;
-    if (__ldg(s.cu + m) <= t)
-      b = m;
-    else
-      e = m;
-  }
-  const int first = __ldg(s.cu + b), end = __ldg(s.cu + b + 1);
-  if (t < first || t >= end) return;
-  const int64_t most = (int64_t)s.max_pages << s.page_shift;
-  int64_t len = __ldg(s.lens + b);
+struct Layout {
+  static constexpr uint32_t TILE = BM * D * 2;  // a Q, K or V tile
+  static constexpr int NS = D == 128 ? 5 : 10;  // 160 KB of K and V in flight
+  static constexpr uint32_t OFF_Q = 0;
+  static constexpr uint32_t OFF_RING = 2 * TILE;
+  static constexpr uint32_t OFF_BAR = OFF_RING + NS * TILE;
+  // q_full[2], q_empty[2], full[NS], empty[NS], s_full[2], p_ready[2],
+  // pv_done[2], u_full[NU], u_empty[NU], joined[2], drain
+  static constexpr uint32_t NBAR = 4 + 2 * NS + 6 + 2 * NU + 2 + 1;
+  static constexpr uint32_t OFF_UNITS = (OFF_BAR + NBAR * 8 + 15) & ~15u;
+  static constexpr uint32_t OFF_ML = OFF_UNITS + NU * 48;
+  static constexpr uint32_t OFF_MISC = OFF_ML + BM * 8;
+  static constexpr uint32_t BYTES = OFF_MISC + 16;
+  static constexpr uint32_t ALLOC = BYTES + 1024;
+  static_assert(ALLOC <= 232448, "shared memory");
+  static_assert(MAX_BATCH * 8 <= NS * TILE, "the schedule's sums use the ring");
+};
+
+struct Params {
+  PagedSeqs s;
+  int total, G, Hkv, tpt, causal;
+  float scale_log2;
+  __nv_bfloat16 *O;
+  int64_t o_stok, o_shead;
+  float *LSE;
+  int64_t lse_shead;
+  float *part_o;   // [CTAS][2][2 BM][D]
+  float2 *part_ml; // [CTAS][2][2 BM]
+  Boundary *bounds;
+  WaitCfg wc;
+};
+
+__device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity, const WaitCfg &wc) {
+  volatile int never = 0;
+  mbar_wait(bar, parity, wc, &never, SITE_PAGED_DRAIN);
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15])
+      : "memory");
+}
+
+// ------------------------------------------------------------------ schedule
+struct Seq {
+  int lo, n, len;  // first packed row, new tokens, cached positions
+};
+
+__device__ __forceinline__ Seq seq_of(const Params &p, int b, bool report) {
+  int lo = __ldg(p.s.cu + b), hi = __ldg(p.s.cu + b + 1), len = __ldg(p.s.lens + b);
+  lo = lo < 0 ? 0 : (lo > p.total ? p.total : lo);
+  hi = hi < lo ? lo : (hi > p.total ? p.total : hi);
+  const int most = p.s.max_pages << p.s.page_shift;
   if (len < 0 || len > most) {
-    if (threadIdx.x == 0) atomicExch(&status->reserved[0], 1);
+    if (report) atomicExch(&p.wc.status->reserved[0], 1);
     len = len < 0 ? 0 : most;
   }
-  const int64_t seen = a.causal ? len - end + t + 1 : len;
-  const int hk = h / (a.H / a.Hkv);
-  float q[E], o[E], m = -INFINITY, l = 0.0f;
-  const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(a.Q) + t * a.q_stok + h * a.q_shead;
+  return Seq{lo, hi - lo, len};
+}
+
+// Key tiles that tokens below `end` of the sequence see; at least one, so
+// that rows which see nothing are still written.
+__device__ __forceinline__ int tiles_to(const Params &p, const Seq &s, int end) {
+  const int seen = p.causal ? s.len - s.n + (end < s.n ? end : s.n) : s.len;
+  return seen <= BN ? 1 : (seen + BN - 1) / BN;
+}
+
+__device__ __forceinline__ int units_of(const Params &p, const Seq &s) {
+  return (s.n + 2 * p.tpt - 1) / (2 * p.tpt);
+}
+
+// Key tiles of one K/V head of the sequence
+__device__ __forceinline__ long long tiles_of_head(const Params &p, const Seq &s) {
+  const int nu = units_of(p, s);
+  if (!p.causal) return (long long)nu * tiles_to(p, s, s.n);
+  long long t = 0;
+  for (int q = 0; q < nu; ++q) t += tiles_to(p, s, (q + 1) * 2 * p.tpt);
+  return t;
+}
+
+struct Place {
+  int b, head, q, j;  // sequence, K/V head, unit of the head, key tile of the unit
+};
+
+// The warp finds key tile `t` (below the total) of the whole work; sums[b]
+// = key tiles of sequence b over all heads.
+__device__ __forceinline__ Place locate(const Params &p, const long long *sums, long long t, int lane) {
+  Place at = {0, 0, 0, 0};
+  for (int c = 0; c < p.s.batch; c += 32) {
+    const long long own = c + lane < p.s.batch ? sums[c + lane] : 0;
+    long long upto = own;
 #pragma unroll
-  for (int k = 0; k < E; ++k) {
-    q[k] = __bfloat162float(qp[lane + 32 * k]) * a.scale * 1.4426950408889634f;
-    o[k] = 0.0f;
-  }
-  for (int64_t j = warp; j < seen; j += 4) {
-    const int page = __ldg(s.table + b * s.table_stride + (j >> s.page_shift));
-    if (page < 0 || page >= s.num_pages) {  // reported; the key counts as zeros
-      if (lane == 0) atomicExch(&status->reserved[0], 1);
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
     }
-    const bool ok = page >= 0 && page < s.num_pages;
-    const int64_t slot = j & ((1 << s.page_shift) - 1);
-    const __nv_bfloat16 *kp = static_cast<const __nv_bfloat16 *>(a.kc.ptr) + page * a.kc.s_page +
-                              slot * a.kc.s_slot + hk * a.kc.s_head;
-    const __nv_bfloat16 *vp = static_cast<const __nv_bfloat16 *>(a.vc.ptr) + page * a.vc.s_page +
-                              slot * a.vc.s_slot + hk * a.vc.s_head;
-    float x = 0.0f;
-#pragma unroll
-    for (int k = 0; k < E; ++k) x += ok ? q[k] * __bfloat162float(kp[lane + 32 * k]) : 0.0f;
-#pragma unroll
-    for (int i = 16; i > 0; i >>= 1) x += __shfl_xor_sync(0xffffffffu, x, i);
-    const float mn = fmaxf(m, x), f = ex2(m - mn), w = ex2(x - mn);
-    l = l * f + w;
-#pragma unroll
-    for (int k = 0; k < E; ++k) o[k] = o[k] * f + (ok ? w * __bfloat162float(vp[lane + 32 * k]) : 0.0f);
-    m = mn;
+    const uint32_t hit = __ballot_sync(0xffffffffu, t < upto);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      at.b = c + l;
+      t -= __shfl_sync(0xffffffffu, upto - own, l);
+      break;
+    }
+    t -= __shfl_sync(0xffffffffu, upto, 31);
   }
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
+  const Seq s = seq_of(p, at.b, false);
+  const int nu = units_of(p, s);
+  const long long per = sums[at.b] / p.Hkv;
+  at.head = (int)(t / per);
+  t -= at.head * per;
+  if (!p.causal) {
+    const int nt = tiles_to(p, s, s.n);
+    at.q = (int)(t / nt);
+    at.j = (int)(t - (long long)at.q * nt);
+    return at;
   }
+  for (int c = 0; c < nu; c += 32) {
+    const int own = c + lane < nu ? tiles_to(p, s, (c + lane + 1) * 2 * p.tpt) : 0;
+    long long upto = own;
 #pragma unroll
-  for (int k = 0; k < E; ++k) so[warp][lane + 32 * k] = o[k];
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, t < upto);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      at.q = c + l;
+      at.j = (int)(t - __shfl_sync(0xffffffffu, upto - own, l));
+      return at;
+    }
+    t -= __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return at;
+}
+
+__device__ __forceinline__ long long run_start(long long total, int cta) { return total * cta / CTAS; }
+
+// --------------------------------------------------------------- main kernel
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1)
+    paged_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ CUtensorMap tmV, const Params p) {
+  using L = Layout<D>;
+  constexpr int NS = L::NS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t *q_full = reinterpret_cast<uint64_t *>(smem + L::OFF_BAR);  // [2]
+  uint64_t *q_empty = q_full + 2;                                      // [2]
+  uint64_t *full = q_empty + 2;                                        // [NS]
+  uint64_t *empty = full + NS;                                         // [NS]
+  uint64_t *s_full = empty + NS;                                       // [2]
+  uint64_t *p_ready = s_full + 2;                                      // [2]
+  uint64_t *pv_done = p_ready + 2;                                     // [2]
+  uint64_t *u_full = pv_done + 2;                                      // [NU]
+  uint64_t *u_empty = u_full + NU;                                     // [NU]
+  uint64_t *joined = u_empty + NU;                                     // [2]: stream 1's (m, l); O1 read
+  uint64_t *mma_drain = joined + 2;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::OFF_MISC);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_MISC + 4);
+  float2 *ml = reinterpret_cast<float2 *>(smem + L::OFF_ML);
+  long long *sums = reinterpret_cast<long long *>(smem + L::OFF_RING);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&q_full[t], 1);
+      mbar_init(&q_empty[t], 1);
+      mbar_init(&s_full[t], 1);
+      mbar_init(&p_ready[t], 128);
+      mbar_init(&pv_done[t], 1);
+      mbar_init(&joined[t], 128);
+    }
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < NU; ++s) {
+      mbar_init(&u_full[s], 1);
+      mbar_init(&u_empty[s], 2 + 8);  // producer, MMA warp, eight softmax warps
+    }
+    mbar_init(mma_drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  if (warp == 8 && lane == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  for (int b = threadIdx.x; b < p.s.batch; b += THREADS)
+    sums[b] = p.Hkv * tiles_of_head(p, seq_of(p, b, blockIdx.x == 0));
+  fence_proxy_async_smem();  // the ring's first copies come after these writes and their reads
+  tc_fence_before();
   __syncthreads();
-  const float top = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-  float w[4], sum = 0.0f;
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_launch_dependents();  // the join may be launched; it waits for this grid
+
+  // Every lane waits, and the warp goes on or gives up as one: what follows
+  // holds warp-wide instructions.
+  auto warp_wait = [&](uint64_t *bar, uint32_t parity, int site) -> bool {
+    const bool ok = mbar_wait(bar, parity, p.wc, abort_flag, site);
+    return __all_sync(0xffffffffu, ok);
+  };
+  // Reads the next unit; false when the run is done or a wait expired.
+  auto next_unit = [&](int &k, Unit &u, int site) -> bool {
+    const int s = k % NU;
+    if (!warp_wait(&u_full[s], (k / NU) & 1, site)) return false;
+    u = *reinterpret_cast<const Unit *>(smem + L::OFF_UNITS + s * 48);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&u_empty[s]);
+    ++k;
+    return u.head >= 0;
+  };
+
+  auto role_scheduler = [&]() {
+    long long total = 0;
+    for (int b = lane; b < p.s.batch; b += 32) total += sums[b];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    w[i] = top == -INFINITY ? 0.0f : ex2(sm[i] - top);
-    sum += w[i] * sl[i];
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    long long t = run_start(total, blockIdx.x);
+    const long long t1 = run_start(total, blockIdx.x + 1);
+    Boundary bd = {0, 0, total, 0, 0, 0, 0};
+    Place at = {0, 0, 0, 0};
+    Seq s = {0, 0, 0};
+    if (t < total) {
+      at = locate(p, sums, t, lane);
+      s = seq_of(p, at.b, false);
+      const int i0 = at.q * 2 * p.tpt;
+      bd.u0 = t - at.j;
+      bd.u1 = bd.u0 + tiles_to(p, s, i0 + 2 * p.tpt);
+      bd.cut = at.j > 0;
+      bd.tok0 = s.lo + i0;
+      bd.ntok = min(s.n - i0, 2 * p.tpt);
+      bd.head = at.head;
+    }
+    if (lane == 0) p.bounds[blockIdx.x] = bd;
+    int k = 0;
+    bool ok = true;
+    while (true) {
+      Unit u = {};
+      u.head = -1;
+      if (t < t1) {
+        const int i0 = at.q * 2 * p.tpt, nt = tiles_to(p, s, i0 + 2 * p.tpt);
+        u.tok0 = s.lo + i0;
+        u.ntok = min(s.n - i0, 2 * p.tpt);
+        u.head = at.head;
+        u.b = at.b;
+        u.j0 = at.j;
+        u.j1 = (int)min((long long)nt, at.j + (t1 - t));
+        u.ja = tiles_to(p, s, i0 + p.tpt);
+        u.lim0 = p.causal ? s.len - s.n + i0 + 1 : s.len;
+        u.len = s.len;
+        u.slot = u.j0 > 0 ? 0 : (u.j1 < nt ? 1 : -1);
+        t += u.j1 - u.j0;
+        // on to the next unit: of the head, the next head, the next sequence with new tokens
+        at.j = 0;
+        if (t < t1 && ++at.q == units_of(p, s)) {
+          at.q = 0;
+          if (++at.head == p.Hkv) {
+            at.head = 0;
+            do {
+              s = seq_of(p, ++at.b, false);
+            } while (s.n == 0 && at.b + 1 < p.s.batch);
+          }
+        }
+      }
+      const int sl = k % NU;
+      if (k >= NU) ok = mbar_wait_warp(&u_empty[sl], ((k / NU) - 1) & 1, p.wc, abort_flag, SITE_PAGED_SCHED);
+      if (!ok) break;
+      if (lane == 0) {
+        *reinterpret_cast<Unit *>(smem + L::OFF_UNITS + sl * 48) = u;
+        mbar_arrive(&u_full[sl]);
+      }
+      ++k;
+      if (u.head < 0) break;
+    }
+    __syncwarp();
+  };
+
+  auto role_producer = [&]() {
+    Unit u;
+    int k = 0;
+    uint32_t q_uses[2] = {0, 0}, qsel = 0;
+    uint32_t seq = 0;  // tiles put into the ring
+    bool ok = true;
+    constexpr int HALVES = D / 64;
+    const int page = 1 << p.s.page_shift;
+    const int rows = page < BN ? page : BN;        // of a box
+    const int boxes = BN / rows * HALVES;          // of a tile, at most 16
+    const int part = lane / HALVES, half = lane % HALVES;
+    const uint32_t q_bytes = (uint32_t)(p.G * p.tpt) * D * 2;
+    while (ok && next_unit(k, u, SITE_PAGED_PROD)) {
+      const bool two = u.ntok > p.tpt;
+      // this lane's page of key tile j: the pool's end, which reads as zeros, where the
+      // sequence has no keys or the table names no page
+      const int *table = p.s.table + u.b * p.s.table_stride;
+      auto page_of = [&](int j) {
+        const int at = (j * BN >> p.s.page_shift) + part;
+        int pg = (int)p.s.num_pages;
+        if (lane < boxes && j < u.j1 && (at << p.s.page_shift) < u.len) {
+          pg = __ldg(table + at);
+          if (pg < 0 || pg >= p.s.num_pages) {
+            atomicExch(&p.wc.status->reserved[0], 1);
+            pg = (int)p.s.num_pages;
+          }
+        }
+        return pg;
+      };
+      int pg = page_of(u.j0);
+      for (int t = 0; t < (two ? 2 : 1); ++t) {
+        const int buf = two ? t : (int)qsel;
+        if (q_uses[buf] > 0)
+          ok = ok && mbar_wait_warp(&q_empty[buf], (q_uses[buf] - 1) & 1, p.wc, abort_flag, SITE_PAGED_PROD);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&q_full[buf], q_bytes);
+#pragma unroll
+          for (int c = 0; c < HALVES; ++c)
+            tma_load_3d(smem + L::OFF_Q + buf * L::TILE + c * (BM * 128), &tmQ, &q_full[buf], c * 64,
+                        u.head * p.G, u.tok0 + t * p.tpt);
+        }
+        ++q_uses[buf];
+      }
+      if (!two) qsel ^= 1;
+      for (int j = u.j0; ok && j < u.j1; ++j) {
+        const int next = page_of(j + 1);
+        const int at = page > BN ? (j * BN) & (page - 1) : 0;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const int st = seq % NS;
+          if (seq >= NS)
+            ok = mbar_wait_warp(&empty[st], ((seq / NS) - 1) & 1, p.wc, abort_flag, SITE_PAGED_PROD);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&full[st], L::TILE);
+          __syncwarp();
+          if (lane < boxes)
+            tma_load_4d(smem + L::OFF_RING + st * L::TILE + half * (BN * 128) + part * (rows * 128),
+                        kv ? &tmV : &tmK, &full[st], half * 64, at, u.head, pg);
+          ++seq;
+        }
+        pg = next;
+      }
+    }
+    if (*abort_flag && lane == 0) {
+      // let every copy still in flight land before shared memory is freed
+      for (int t = 0; t < 2; ++t)
+        if (q_uses[t]) drain_wait(&q_full[t], (q_uses[t] - 1) & 1, p.wc);
+      for (uint32_t s = seq > NS ? seq - NS : 0; s < seq; ++s)
+        drain_wait(&full[s % NS], (s / NS) & 1, p.wc);
+    }
+    __syncwarp();
+  };
+
+  auto role_mma = [&]() {
+    const uint32_t idS = idesc_bf16_f32(BM, BN, 0, 0), idO = idesc_bf16_f32(BM, D, 0, 1);
+    const SDesc dQ = sdesc_make(smem_u32(smem + L::OFF_Q), 16, 1024);
+    const SDesc dK = sdesc_make(smem_u32(smem + L::OFF_RING), 16, 1024);
+    const SDesc dV = sdesc_make(smem_u32(smem + L::OFF_RING), BN * 128, 1024);
+    Unit u;
+    int k = 0;
+    uint32_t q_uses[2] = {0, 0}, qsel = 0;
+    uint32_t base = 0;            // ring number of the unit's first K tile
+    uint32_t steps[2] = {0, 0};   // P V products of each stream so far
+    bool ok = true;
+    while (ok && next_unit(k, u, SITE_PAGED_MMA)) {
+      const bool two = u.ntok > p.tpt;
+      const int n = u.j1 - u.j0;
+      int ns[2];
+      ns[0] = two ? max(0, min(u.ja, u.j1) - u.j0) : (n + 1) / 2;
+      ns[1] = two ? n : n / 2;
+      const int buf0 = two ? 0 : (int)qsel;
+      ok = mbar_wait_warp(&q_full[buf0], q_uses[buf0] & 1, p.wc, abort_flag, SITE_PAGED_MMA);
+      ++q_uses[buf0];
+      if (two) {
+        ok = ok && mbar_wait_warp(&q_full[1], q_uses[1] & 1, p.wc, abort_flag, SITE_PAGED_MMA);
+        ++q_uses[1];
+        if (ok && ns[0] == 0 && elect_one()) umma_commit(&q_empty[0]);
+        __syncwarp();
+      } else {
+        qsel ^= 1;
+      }
+      // S_t of step i into columns [128 t, 128 t + 128)
+      auto issue_s = [&](int t, int i) -> bool {
+        const int x = two ? i : 2 * i + t;
+        const uint32_t seq = base + 2 * x, st = seq % NS;
+        if (!mbar_wait_warp(&full[st], (seq / NS) & 1, p.wc, abort_flag, SITE_PAGED_MMA)) return false;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t qo = (uint32_t)(two ? t : buf0) * L::TILE, ko = st * L::TILE;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * (BM * 128) + (kk & 3) * 32;
+            umma_f16_ss(tmem + t * BN, sdesc_at(dQ, qo + off), sdesc_at(dK, ko + off), idS, kk > 0);
+          }
+          umma_commit(&s_full[t]);
+          if (!two || t == 1) umma_commit(&empty[st]);
+          if (two ? i == ns[t] - 1 : x == n - 1) umma_commit(&q_empty[two ? t : buf0]);
+        }
+        __syncwarp();
+        return true;
+      };
+      for (int t = 0; ok && t < 2; ++t)
+        if (ns[t] > 0) ok = issue_s(t, 0);
+      const int most = max(ns[0], ns[1]);
+      for (int i = 0; ok && i < most; ++i) {
+        for (int t = 0; ok && t < 2; ++t) {
+          if (i >= ns[t]) continue;
+          const int x = two ? i : 2 * i + t;
+          const uint32_t seq = base + 2 * x + 1, st = seq % NS;
+          ok = mbar_wait_warp(&full[st], (seq / NS) & 1, p.wc, abort_flag, SITE_PAGED_MMA);
+          if (!ok) break;
+          // The last page may hold anything behind the sequence's end, and 0 times a
+          // NaN is not 0: those rows of V become zeros.
+          const int valid = u.len - (u.j0 + x) * BN;
+          if (valid > 0 && valid < BN && (!two || t == 0 || i >= ns[0])) {
+            const int page = 1 << p.s.page_shift;
+            const int end = min(BN, (valid + page - 1) & ~(page - 1));
+            for (int c = lane; c < (end - valid) * (D / 8); c += 32) {
+              const int r = valid + c / (D / 8), q = c % (D / 8);
+              st_shared_v4(smem_u32(smem + L::OFF_RING + st * L::TILE + (q >> 3) * (BN * 128) + r * 128 + (q & 7) * 16),
+                           0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          ok = mbar_wait_warp(&p_ready[t], steps[t] & 1, p.wc, abort_flag, SITE_PAGED_MMA);
+          if (!ok) break;
+          ++steps[t];
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t vo = st * L::TILE;
+#pragma unroll
+            for (int kk = 0; kk < BN / 16; ++kk)
+              umma_f16_ts(tmem + 256 + t * 128, tmem + t * BN + kk * 8, sdesc_at(dV, vo + kk * 2048), idO,
+                          i > 0 || kk > 0);
+            umma_commit(&pv_done[t]);
+            if (!two || t == 1) umma_commit(&empty[st]);
+          }
+          __syncwarp();
+          if (i + 1 < ns[t]) ok = issue_s(t, i + 1);
+        }
+      }
+      base += 2 * n;
+    }
+    // no MMA may still be running when tensor memory is released
+    if (elect_one()) umma_commit(mma_drain);
+    __syncwarp();
+    if (lane == 0) drain_wait(mma_drain, 0, p.wc);
+    __syncwarp();
+  };
+
+  auto role_softmax = [&]() {
+    const int t = warp >> 2;
+    const int row = threadIdx.x & 127;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_off + t * BN;
+    const int rtok = row / p.G, rhead = row - rtok * p.G;  // token of the tile, head of the group
+    Unit u;
+    int k = 0;
+    uint32_t steps[2] = {0, 0}, joins = 0;  // S tiles of each stream, units joined
+    bool ok = true;
+    while (ok && next_unit(k, u, SITE_PAGED_SOFTMAX)) {
+      const bool two = u.ntok > p.tpt;
+      const int n = u.j1 - u.j0;
+      const int n0 = two ? max(0, min(u.ja, u.j1) - u.j0) : (n + 1) / 2;
+      const int n1 = two ? n : n / 2;
+      const int mine = t ? n1 : n0;
+      const int tok = (two ? t * p.tpt : 0) + rtok;  // of the unit
+      const bool valid = rtok < p.tpt && tok < u.ntok;
+      const bool active = __any_sync(0xffffffffu, valid);
+      const int lim = valid ? (p.causal ? u.lim0 + tok : u.len) : u.len;  // keys below it are seen
+      float m = -INFINITY, l = 0.0f;
+      for (int i = 0; i < mine; ++i) {
+        ok = warp_wait(&s_full[t], (steps[t] + i) & 1, SITE_PAGED_SOFTMAX);
+        if (!ok) break;
+        tc_fence_after();
+        if (active) {
+          const int kv0 = (u.j0 + (two ? i : 2 * i + t)) * BN;
+          uint32_t s[BN];
+#pragma unroll
+          for (int c = 0; c < BN / 32; ++c)
+            tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[c * 32]));
+          tmem_wait_ld();
+          if (kv0 + BN > lim) {
+#pragma unroll
+            for (int e = 0; e < BN; ++e)
+              if (kv0 + e >= lim) s[e] = __float_as_uint(-INFINITY);
+          }
+          float mx4[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            mx4[e] = fmaxf(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+#pragma unroll
+          for (int c = 8; c < BN; c += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              mx4[e] = fmax3(mx4[e], __uint_as_float(s[c + 2 * e]), __uint_as_float(s[c + 2 * e + 1]));
+          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.scale_log2;
+          float alpha = 1.0f;
+          bool rescale = false;
+          if (i == 0) {
+            m = mx;
+          } else if (mx > m + RESCALE_THRESHOLD) {
+            alpha = ex2(m - mx);
+            m = mx;
+            rescale = true;
+          }
+          const float mref = m == -INFINITY ? 0.0f : m;
+          // P = 2^(s scale log2e - m): keys [32 g, 32 g + 32) to columns [16 g, 16 g + 16)
+          const uint64_t sc2 = f32x2(p.scale_log2, p.scale_log2), nm2 = f32x2(-mref, -mref);
+          uint64_t rs2[4] = {0, 0, 0, 0};
+#pragma unroll
+          for (int g = 0; g < BN / 32; ++g) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              float x0, x1;
+              f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[g * 32 + e]), __uint_as_float(s[g * 32 + e + 1])),
+                                    sc2, nm2),
+                          x0, x1);
+              const float p0 = ex2(x0), p1 = ex2(x1);
+              rs2[(e >> 1) & 3] = add_f32x2(rs2[(e >> 1) & 3], f32x2(p0, p1));
+              pk[e >> 1] = pack_bf16(p0, p1);
+            }
+            tmem_st16(tS + g * 16, pk);
+          }
+          float rs = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float a0, a1;
+            f32x2_split(rs2[e], a0, a1);
+            rs += a0 + a1;
+          }
+          // S of this step was issued after the previous step's P V: O holds every earlier key
+          if (__any_sync(0xffffffffu, rescale)) {
+            const uint32_t tO = tmem + lane_off + 256 + t * 128;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(tO + c * 32, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st32(tO + c * 32, o);
+            }
+          }
+          l = l * alpha + rs;
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        mbar_arrive(&p_ready[t]);
+      }
+      if (!ok) break;
+      steps[0] += n0;
+      steps[1] += n1;
+      // ----------------------------------------------------------- epilogue
+      if (!two && t == 1) {
+        // stream 1's row statistics to stream 0, which reads its O too
+        ml[row] = make_float2(m, l);
+        mbar_arrive(&joined[0]);
+        ok = warp_wait(&joined[1], joins & 1, SITE_PAGED_EPI);
+        tc_fence_after();
+        ++joins;
+        continue;
+      }
+      float w[2] = {1.0f, 0.0f};  // weights of the two streams' O
+      bool has[2] = {t == 0 ? n0 > 0 : false, t == 1 ? n1 > 0 : false};
+      if (t == 1) {
+        w[0] = 0.0f;
+        w[1] = 1.0f;
+      }
+      if (!two) {
+        ok = warp_wait(&joined[0], joins & 1, SITE_PAGED_EPI);
+        if (!ok) break;
+        has[1] = n1 > 0;
+        const float2 o = ml[row];
+        const float top = fmaxf(m, o.x);
+        if (top != -INFINITY) {
+          w[0] = ex2(m - top);
+          w[1] = ex2(o.x - top);
+          l = l * w[0] + o.y * w[1];
+        }
+        m = top;
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (has[e] && ok) ok = warp_wait(&pv_done[e], (steps[e] - 1) & 1, SITE_PAGED_EPI);
+      if (!ok) break;
+      tc_fence_after();
+      if (active) {
+        const bool whole = u.slot < 0;
+        if (whole) {
+          const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+          w[0] *= inv;
+          w[1] *= inv;
+        }
+        const int64_t qrow = (int64_t)u.tok0 + tok, qhead = (int64_t)u.head * p.G + rhead;
+        const int64_t prow = ((int64_t)blockIdx.x * 2 + u.slot) * (2 * BM) + t * BM + row;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t x[32];
+          float o[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0.0f;
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            if (!has[y]) continue;
+            tmem_ld32(tmem + lane_off + 256 + y * 128 + c * 32, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(x[e]), w[y], o[e]);
+          }
+          if (valid && whole) {
+            uint4 *dst = reinterpret_cast<uint4 *>(p.O + qrow * p.o_stok + qhead * p.o_shead + c * 32);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              dst[e] = make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]), pack_bf16(o[8 * e + 2], o[8 * e + 3]),
+                                  pack_bf16(o[8 * e + 4], o[8 * e + 5]), pack_bf16(o[8 * e + 6], o[8 * e + 7]));
+          } else if (valid) {
+            float4 *dst = reinterpret_cast<float4 *>(p.part_o + prow * D + c * 32);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+          __syncwarp();
+        }
+        if (valid) {
+          if (whole)
+            p.LSE[qhead * p.lse_shead + qrow] = l > 0.0f ? (m + lg2(l)) * 0.69314718055994531f : -INFINITY;
+          else
+            p.part_ml[prow] = make_float2(m, l);
+        }
+      }
+      if (!two) {
+        tc_fence_before();
+        mbar_arrive(&joined[1]);
+        ++joins;
+      }
+    }
+  };
+
+  if (warp >= 8) {  // warp 11 only hands its registers over
+    setmaxnreg_dec<REGS_CONTROL>();
+    if (warp == 8)
+      role_producer();
+    else if (warp == 9)
+      role_mma();
+    else if (warp == 10)
+      role_scheduler();
+  } else {
+    setmaxnreg_inc<REGS_SOFTMAX>();
+    role_softmax();
   }
-  const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-  __nv_bfloat16 *op = static_cast<__nv_bfloat16 *>(a.O) + t * a.o_stok + h * a.o_shead;
-  for (int i = threadIdx.x; i < D; i += 128)
-    op[i] = __float2bfloat16((w[0] * so[0][i] + w[1] * so[1][i] + w[2] * so[2][i] + w[3] * so[3][i]) * inv);
-  if (threadIdx.x == 0)
-    a.LSE[h * a.lse_shead + t] = sum > 0.0f ? (top + lg2(sum)) * 0.69314718055994531f : -INFINITY;
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins a unit that runs' ends cut into parts: block (c, y) the unit that
+// boundary c + 1 falls into, if that is the unit's first boundary.  A warp to
+// a row; parts in the order of the keys.
+template <int D>
+__global__ void __launch_bounds__(256) paged_combine_kernel(const Params p) {
+  constexpr int E = D / 32;
+  pdl_wait();  // the parts and boundaries
+  const int c = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Boundary bd = p.bounds[c];
+  if (!bd.cut || run_start(bd.total, c - 1) > bd.u0) return;
+  // rows are numbered as in the unit's tiles
+  const int tiles = bd.ntok > p.tpt ? 2 : 1;
+  for (int r = warp * gridDim.y + blockIdx.y; r < tiles * BM; r += gridDim.y * 8) {
+    const int rt = (r % BM) / p.G, tok = (r / BM) * p.tpt + rt;
+    if (rt >= p.tpt || tok >= bd.ntok) continue;
+    float m = -INFINITY, l = 0.0f, o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.0f;
+    for (int k = c - 1; k < CTAS; ++k) {
+      const long long t0 = run_start(bd.total, k);
+      if (t0 >= bd.u1) break;
+      if (k >= c && run_start(bd.total, k + 1) == t0) continue;  // an empty run
+      const int64_t prow = ((int64_t)k * 2 + (k < c ? 1 : 0)) * (2 * BM) + r;
+      const float2 x = p.part_ml[prow];
+      const float *po = p.part_o + prow * D + lane * E;
+      float v[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = po[e];
+      const float top = fmaxf(m, x.x);
+      if (top == -INFINITY) continue;
+      const float w0 = ex2(m - top), w1 = ex2(x.x - top);
+      m = top;
+      l = l * w0 + x.y * w1;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = o[e] * w0 + v[e] * w1;
+    }
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    const int64_t qrow = (int64_t)bd.tok0 + tok, qhead = (int64_t)bd.head * p.G + r % BM - rt * p.G;
+    __nv_bfloat16 *dst = p.O + qrow * p.o_stok + qhead * p.o_shead + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+      *reinterpret_cast<uint32_t *>(dst + e) = pack_bf16(o[e] * inv, o[e + 1] * inv);
+    if (lane == 0)
+      p.LSE[qhead * p.lse_shead + qrow] = l > 0.0f ? (m + lg2(l)) * 0.69314718055994531f : -INFINITY;
+  }
+}
+
+size_t part_bytes(int d) { return (size_t)CTAS * 2 * 2 * BM * d * sizeof(float); }
+size_t ml_bytes() { return (size_t)CTAS * 2 * 2 * BM * sizeof(float2); }
+
+template <int D>
+cudaError_t launch(const PagedAttnArgs &a, const WaitCfg &wc, cudaStream_t st) {
+  using L = Layout<D>;
+  Params p;
+  p.s = a.seqs;
+  p.total = a.total;
+  p.G = a.H / a.Hkv;
+  p.Hkv = a.Hkv;
+  p.tpt = BM / p.G;
+  p.causal = a.causal;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.O = static_cast<__nv_bfloat16 *>(a.O);
+  p.o_stok = a.o_stok;
+  p.o_shead = a.o_shead;
+  p.LSE = a.LSE;
+  p.lse_shead = a.lse_shead;
+  uint8_t *ws = static_cast<uint8_t *>(a.workspace);
+  p.part_o = reinterpret_cast<float *>(ws);
+  p.part_ml = reinterpret_cast<float2 *>(ws + part_bytes(D));
+  p.bounds = reinterpret_cast<Boundary *>(ws + part_bytes(D) + ml_bytes());
+  p.wc = wc;
+  // Q: {d, head, token}, a tile's box G heads of TPT tokens.  Strides of
+  // extents of one are not given: any valid value does.
+  CUtensorMap mq, mk, mv;
+  const uint64_t row_bytes = (uint64_t)D * 2;
+  const uint64_t dq[3] = {(uint64_t)D, (uint64_t)a.H, (uint64_t)a.total};
+  const uint64_t sq[2] = {a.q_shead ? (uint64_t)a.q_shead * 2 : row_bytes,
+                          a.q_stok ? (uint64_t)a.q_stok * 2 : row_bytes};
+  const uint32_t bq[3] = {64, (uint32_t)p.G, (uint32_t)p.tpt};
+  // K, V: {d, slot, head, page}
+  const int page = 1 << a.seqs.page_shift;
+  const uint64_t dk[4] = {(uint64_t)D, (uint64_t)page, (uint64_t)a.Hkv, (uint64_t)a.seqs.num_pages};
+  const uint64_t sk[3] = {(uint64_t)a.kc.s_slot * 2, (uint64_t)a.kc.s_head * 2, (uint64_t)a.kc.s_page * 2};
+  const uint64_t sv[3] = {(uint64_t)a.vc.s_slot * 2, (uint64_t)a.vc.s_head * 2, (uint64_t)a.vc.s_page * 2};
+  const uint32_t bk[4] = {64, (uint32_t)(page < BN ? page : BN), 1, 1};
+  cudaError_t e;
+  if ((e = make_tmap(&mq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.Q, dq, sq, bq)) != cudaSuccess ||
+      (e = make_tmap(&mk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, a.kc.ptr, dk, sk, bk)) != cudaSuccess ||
+      (e = make_tmap(&mv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, a.vc.ptr, dk, sv, bk)) != cudaSuccess)
+    return e;
+  e = cudaFuncSetAttribute(paged_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC);
+  if (e != cudaSuccess) return e;
+  timing_mark(st, 0);
+  paged_attn_kernel<D><<<CTAS, THREADS, L::ALLOC, st>>>(mq, mk, mv, p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  timing_mark(st, 1);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(CTAS - 1, 4);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_combine_kernel<D>, p);
 }
 
 }  // namespace
 
-size_t paged_attn_workspace(int) { return 256; }
+size_t paged_attn_workspace(int d) { return part_bytes(d) + ml_bytes() + CTAS * sizeof(Boundary) + 256; }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs &a, const WaitCfg &wc, cudaStream_t st) {
-  timing_mark(st, 0);
-  const dim3 grid((unsigned)a.total, (unsigned)a.H);
-  if (a.d == 128)
-    paged_attn_kernel<128><<<grid, 128, 0, st>>>(a, wc.status);
-  else
-    paged_attn_kernel<64><<<grid, 128, 0, st>>>(a, wc.status);
-  timing_mark(st, 1);
-  return cudaGetLastError();
+  return a.d == 128 ? launch<128>(a, wc, st) : launch<64>(a, wc, st);
 }
 
 }  // namespace chain
