@@ -14,8 +14,8 @@
 // (2 TPT tokens), over the 128-key tiles its last token sees.
 //
 // Split.  The lengths are on the device, so the work is dealt there: the
-// units' key tiles, laid end to end, are cut into one equal run for each of
-// the CTAS persistent blocks, whatever the mix of lengths.  A block works
+// units' costs (key tiles), laid end to end, are cut into one equal run for
+// each of the CTAS persistent blocks, whatever the mix of lengths.  A block works
 // through the units of its run; a unit cut by a run's end leaves partial
 // (O, m, l) in the workspace, which paged_combine_kernel joins.  A block has
 // at most two partial units, the first and the last of its run.
@@ -48,6 +48,7 @@ constexpr int CTAS = 152;     // one block on each SM
 constexpr int THREADS = 384;
 constexpr int NU = 4;         // units in flight between the scheduler and the other warps
 constexpr int MAX_BATCH = 8192;
+constexpr int OVERHEAD = 2;   // cost of a unit's start and end, in key tiles
 constexpr uint32_t REGS_SOFTMAX = 184, REGS_CONTROL = 136;  // 256 x 184 + 128 x 136 = 384 x 168
 constexpr float RESCALE_THRESHOLD = 8.0f;                   // log2 units
 
@@ -72,11 +73,12 @@ struct Unit {
 };
 static_assert(sizeof(Unit) <= 48, "unit ring");
 
-// Where a run begins, for the join: written by every block, valid or not.
+// Where a run begins, for the join: written by every block, cut or not.
 struct Boundary {
-  long long u0, u1;  // first and last+1 key tile of the unit it falls into
-  long long total;   // all key tiles
-  int cut;           // it falls inside a unit
+  long long u0;     // cost at which the unit that it falls into begins
+  long long total;  // cost of all units
+  int nt, w;        // the unit's key tiles, cost of each
+  int cut;          // it falls behind the unit's first key tile
   int tok0, ntok, head;
 };
 
@@ -107,7 +109,7 @@ struct Params {
   int64_t o_stok, o_shead;
   float *LSE;
   int64_t lse_shead;
-  float *part_o;   // [CTAS][2][2 BM][D]
+  float *part_o;   // [CTAS][2][D / 4][2 BM][4]
   float2 *part_ml; // [CTAS][2][2 BM]
   Boundary *bounds;
   WaitCfg wc;
@@ -126,6 +128,34 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
       "r"(r[15])
       : "memory");
+}
+
+// Each lane holds 64 bytes of its own row and `at`, their place in memory.
+// Four lanes exchange 16-byte chunks, so that one store writes 64 bytes of each of
+// eight rows: a lane storing its own row would touch 32 lines an instruction,
+// and the stores of a tile took 4,000 cycles.
+__device__ __forceinline__ void store_rows(uint4 (&v)[4], __nv_bfloat16 *at, bool valid, int lane) {
+  auto trade = [&](uint4 &a, uint4 &b, int bit) {
+    // of a pair of lanes, the lower one keeps a and the upper one b
+    const bool up = lane & bit;
+    uint4 give = up ? a : b;
+    give.x = __shfl_xor_sync(0xffffffffu, give.x, bit);
+    give.y = __shfl_xor_sync(0xffffffffu, give.y, bit);
+    give.z = __shfl_xor_sync(0xffffffffu, give.z, bit);
+    give.w = __shfl_xor_sync(0xffffffffu, give.w, bit);
+    (up ? a : b) = give;
+  };
+  trade(v[0], v[1], 1);
+  trade(v[2], v[3], 1);
+  trade(v[0], v[2], 2);
+  trade(v[1], v[3], 2);
+  // v[i] is now chunk lane % 4 of the row of lane lane - lane % 4 + i
+  const unsigned long long own = valid ? reinterpret_cast<unsigned long long>(at) : 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const unsigned long long a = __shfl_sync(0xffffffffu, own, (lane & ~3) + i);
+    if (a) reinterpret_cast<uint4 *>(a)[lane & 3] = v[i];
+  }
 }
 
 // ------------------------------------------------------------------ schedule
@@ -156,68 +186,76 @@ __device__ __forceinline__ int units_of(const Params &p, const Seq &s) {
   return (s.n + 2 * p.tpt - 1) / (2 * p.tpt);
 }
 
-// Key tiles of one K/V head of the sequence
-__device__ __forceinline__ long long tiles_of_head(const Params &p, const Seq &s) {
+// Cost of a unit: its key tiles, a tile of two query tiles counting twice (it
+// has twice the products and exponentials), and OVERHEAD for its start and end.
+__device__ __forceinline__ int tile_cost(const Params &p, int ntok) { return ntok > p.tpt ? 2 : 1; }
+__device__ __forceinline__ long long unit_cost(const Params &p, const Seq &s, int q) {
+  const int i0 = q * 2 * p.tpt;
+  return OVERHEAD + (long long)tile_cost(p, s.n - i0) * tiles_to(p, s, i0 + 2 * p.tpt);
+}
+// Key tile at a cost offset into a unit.
+__device__ __forceinline__ int tile_at(long long off, int w) {
+  return off <= OVERHEAD ? 0 : (int)((off - OVERHEAD) / w);
+}
+
+// Cost of one K/V head of the sequence
+__device__ __forceinline__ long long head_cost(const Params &p, const Seq &s) {
   const int nu = units_of(p, s);
-  if (!p.causal) return (long long)nu * tiles_to(p, s, s.n);
   long long t = 0;
-  for (int q = 0; q < nu; ++q) t += tiles_to(p, s, (q + 1) * 2 * p.tpt);
+  for (int q = 0; q < nu; ++q) t += unit_cost(p, s, q);
   return t;
 }
 
+// 64-bit division takes hundreds of cycles and is hardly ever needed
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
 struct Place {
-  int b, head, q, j;  // sequence, K/V head, unit of the head, key tile of the unit
+  int b, head, q;  // sequence, K/V head, unit of the head
+  long long off;   // cost offset into the unit
 };
 
-// The warp finds key tile `t` (below the total) of the whole work; sums[b]
-// = key tiles of sequence b over all heads.
+// Of 32 lanes' costs `own`, the lane that `t` falls into, or -1; t becomes the
+// offset into it, or past all of them.
+__device__ __forceinline__ int find(long long own, long long &t, int lane) {
+  long long upto = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += x;
+  }
+  const uint32_t hit = __ballot_sync(0xffffffffu, t < upto);
+  const int l = hit ? __ffs(hit) - 1 : -1;
+  t -= __shfl_sync(0xffffffffu, hit ? upto - own : upto, hit ? l : 31);
+  return l;
+}
+
+// The warp finds cost `t` (below the total) in the whole work; sums[b] = cost of
+// one head of sequence b.
 __device__ __forceinline__ Place locate(const Params &p, const long long *sums, long long t, int lane) {
   Place at = {0, 0, 0, 0};
-  for (int c = 0; c < p.s.batch; c += 32) {
-    const long long own = c + lane < p.s.batch ? sums[c + lane] : 0;
-    long long upto = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += x;
-    }
-    const uint32_t hit = __ballot_sync(0xffffffffu, t < upto);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
+  for (int c = 0; c < p.s.batch && p.s.batch > 1; c += 32) {
+    const int l = find(c + lane < p.s.batch ? sums[c + lane] * p.Hkv : 0, t, lane);
+    if (l >= 0) {
       at.b = c + l;
-      t -= __shfl_sync(0xffffffffu, upto - own, l);
       break;
     }
-    t -= __shfl_sync(0xffffffffu, upto, 31);
   }
   const Seq s = seq_of(p, at.b, false);
   const int nu = units_of(p, s);
-  const long long per = sums[at.b] / p.Hkv;
-  at.head = (int)(t / per);
+  const long long per = sums[at.b];
+  at.head = (int)quotient(t, per);
   t -= at.head * per;
-  if (!p.causal) {
-    const int nt = tiles_to(p, s, s.n);
-    at.q = (int)(t / nt);
-    at.j = (int)(t - (long long)at.q * nt);
-    return at;
-  }
-  for (int c = 0; c < nu; c += 32) {
-    const int own = c + lane < nu ? tiles_to(p, s, (c + lane + 1) * 2 * p.tpt) : 0;
-    long long upto = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += x;
-    }
-    const uint32_t hit = __ballot_sync(0xffffffffu, t < upto);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
+  for (int c = 0; c < nu && nu > 1; c += 32) {
+    const int l = find(c + lane < nu ? unit_cost(p, s, c + lane) : 0, t, lane);
+    if (l >= 0) {
       at.q = c + l;
-      at.j = (int)(t - __shfl_sync(0xffffffffu, upto - own, l));
-      return at;
+      break;
     }
-    t -= __shfl_sync(0xffffffffu, upto, 31);
   }
+  at.off = t;
   return at;
 }
 
@@ -281,7 +319,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     tma_prefetch_desc(&tmV);
   }
   for (int b = threadIdx.x; b < p.s.batch; b += THREADS)
-    sums[b] = p.Hkv * tiles_of_head(p, seq_of(p, b, blockIdx.x == 0));
+    sums[b] = head_cost(p, seq_of(p, b, blockIdx.x == 0));
   fence_proxy_async_smem();  // the ring's first copies come after these writes and their reads
   tc_fence_before();
   __syncthreads();
@@ -311,18 +349,20 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int b = lane; b < p.s.batch; b += 32) total += sums[b];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    total *= p.Hkv;
     long long t = run_start(total, blockIdx.x);
     const long long t1 = run_start(total, blockIdx.x + 1);
-    Boundary bd = {0, 0, total, 0, 0, 0, 0};
+    Boundary bd = {0, total, 0, 1, 0, 0, 0, 0};
     Place at = {0, 0, 0, 0};
     Seq s = {0, 0, 0};
     if (t < total) {
       at = locate(p, sums, t, lane);
       s = seq_of(p, at.b, false);
       const int i0 = at.q * 2 * p.tpt;
-      bd.u0 = t - at.j;
-      bd.u1 = bd.u0 + tiles_to(p, s, i0 + 2 * p.tpt);
-      bd.cut = at.j > 0;
+      bd.u0 = t - at.off;
+      bd.nt = tiles_to(p, s, i0 + 2 * p.tpt);
+      bd.w = tile_cost(p, s.n - i0);
+      bd.cut = tile_at(at.off, bd.w) > 0;
       bd.tok0 = s.lo + i0;
       bd.ntok = min(s.n - i0, 2 * p.tpt);
       bd.head = at.head;
@@ -335,19 +375,23 @@ __global__ void __launch_bounds__(THREADS, 1)
       u.head = -1;
       if (t < t1) {
         const int i0 = at.q * 2 * p.tpt, nt = tiles_to(p, s, i0 + 2 * p.tpt);
-        u.tok0 = s.lo + i0;
-        u.ntok = min(s.n - i0, 2 * p.tpt);
-        u.head = at.head;
-        u.b = at.b;
-        u.j0 = at.j;
-        u.j1 = (int)min((long long)nt, at.j + (t1 - t));
-        u.ja = tiles_to(p, s, i0 + p.tpt);
-        u.lim0 = p.causal ? s.len - s.n + i0 + 1 : s.len;
-        u.len = s.len;
-        u.slot = u.j0 > 0 ? 0 : (u.j1 < nt ? 1 : -1);
-        t += u.j1 - u.j0;
+        const int w = tile_cost(p, s.n - i0);
+        const long long cost = OVERHEAD + (long long)w * nt, end = at.off + (t1 - t);
+        u.j0 = tile_at(at.off, w);
+        u.j1 = end >= cost ? nt : tile_at(end, w);
+        if (u.j1 > u.j0) {  // else the run ends before the unit's first key tile
+          u.tok0 = s.lo + i0;
+          u.ntok = min(s.n - i0, 2 * p.tpt);
+          u.head = at.head;
+          u.b = at.b;
+          u.ja = tiles_to(p, s, i0 + p.tpt);
+          u.lim0 = p.causal ? s.len - s.n + i0 + 1 : s.len;
+          u.len = s.len;
+          u.slot = u.j0 > 0 ? 0 : (u.j1 < nt ? 1 : -1);
+        }
+        t += cost - at.off;
         // on to the next unit: of the head, the next head, the next sequence with new tokens
-        at.j = 0;
+        at.off = 0;
         if (t < t1 && ++at.q == units_of(p, s)) {
           at.q = 0;
           if (++at.head == p.Hkv) {
@@ -385,22 +429,20 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t q_bytes = (uint32_t)(p.G * p.tpt) * D * 2;
     while (ok && next_unit(k, u, SITE_PAGED_PROD)) {
       const bool two = u.ntok > p.tpt;
-      // this lane's page of key tile j: the pool's end, which reads as zeros, where the
+      // 32 entries of the table at a time, one a lane, the next 32 on their way and
+      // checked only when their turn comes; the pool's end, which reads as zeros, where the
       // sequence has no keys or the table names no page
       const int *table = p.s.table + u.b * p.s.table_stride;
-      auto page_of = [&](int j) {
-        const int at = (j * BN >> p.s.page_shift) + part;
-        int pg = (int)p.s.num_pages;
-        if (lane < boxes && j < u.j1 && (at << p.s.page_shift) < u.len) {
-          pg = __ldg(table + at);
-          if (pg < 0 || pg >= p.s.num_pages) {
-            atomicExch(&p.wc.status->reserved[0], 1);
-            pg = (int)p.s.num_pages;
-          }
-        }
-        return pg;
+      const int pool = (int)p.s.num_pages;
+      auto keys_at = [&](int at) { return ((long long)at << p.s.page_shift) < u.len; };
+      auto entry = [&](int at) { return keys_at(at) ? __ldg(table + at) : pool; };
+      auto checked = [&](int pg, int at) {
+        if (pg >= 0 && pg < pool) return pg;
+        if (keys_at(at)) atomicExch(&p.wc.status->reserved[0], 1);
+        return pool;
       };
-      int pg = page_of(u.j0);
+      int first = u.j0 * BN >> p.s.page_shift;
+      int pages = entry(first + lane), ahead = entry(first + 32 + lane);
       for (int t = 0; t < (two ? 2 : 1); ++t) {
         const int buf = two ? t : (int)qsel;
         if (q_uses[buf] > 0)
@@ -416,8 +458,16 @@ __global__ void __launch_bounds__(THREADS, 1)
         ++q_uses[buf];
       }
       if (!two) qsel ^= 1;
+      pages = checked(pages, first + lane);
       for (int j = u.j0; ok && j < u.j1; ++j) {
-        const int next = page_of(j + 1);
+        int e = (j * BN >> p.s.page_shift) - first;  // the tile's first entry
+        if (e >= 32) {
+          first += 32;
+          e -= 32;
+          pages = checked(ahead, first + lane);
+          ahead = entry(first + 32 + lane);
+        }
+        const int pg = __shfl_sync(0xffffffffu, pages, (e + part) & 31);
         const int at = page > BN ? (j * BN) & (page - 1) : 0;
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
@@ -432,7 +482,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                         kv ? &tmV : &tmK, &full[st], half * 64, at, u.head, pg);
           ++seq;
         }
-        pg = next;
       }
     }
     if (*abort_flag && lane == 0) {
@@ -657,12 +706,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         ++joins;
         continue;
       }
-      float w[2] = {1.0f, 0.0f};  // weights of the two streams' O
-      bool has[2] = {t == 0 ? n0 > 0 : false, t == 1 ? n1 > 0 : false};
-      if (t == 1) {
-        w[0] = 0.0f;
-        w[1] = 1.0f;
-      }
+      float w[2] = {t == 0 ? 1.0f : 0.0f, t == 1 ? 1.0f : 0.0f};  // weights of the two streams' O
+      bool has[2] = {t == 0 && n0 > 0, t == 1};
       if (!two) {
         ok = warp_wait(&joined[0], joins & 1, SITE_PAGED_EPI);
         if (!ok) break;
@@ -688,10 +733,13 @@ __global__ void __launch_bounds__(THREADS, 1)
           w[0] *= inv;
           w[1] *= inv;
         }
-        const int64_t qrow = (int64_t)u.tok0 + tok, qhead = (int64_t)u.head * p.G + rhead;
-        const int64_t prow = ((int64_t)blockIdx.x * 2 + u.slot) * (2 * BM) + t * BM + row;
+        const int64_t qhead = (int64_t)u.head * p.G + rhead;
+        __nv_bfloat16 *orow = p.O + ((int64_t)u.tok0 + tok) * p.o_stok + qhead * p.o_shead;
+        // a slot's O is [D / 4][2 BM][4], so that lanes, which hold rows, write side by side
+        const int64_t slot = (int64_t)blockIdx.x * 2 + u.slot;
+        float4 *prow = reinterpret_cast<float4 *>(p.part_o) + slot * (2 * BM * D / 4) + t * BM + row;
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
+        for (int c = 0; c < D / 32 && (has[0] || has[1]); ++c) {
           uint32_t x[32];
           float o[32];
 #pragma unroll
@@ -704,24 +752,25 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(x[e]), w[y], o[e]);
           }
-          if (valid && whole) {
-            uint4 *dst = reinterpret_cast<uint4 *>(p.O + qrow * p.o_stok + qhead * p.o_shead + c * 32);
+          if (whole) {
+            uint4 v[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              dst[e] = make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]), pack_bf16(o[8 * e + 2], o[8 * e + 3]),
-                                  pack_bf16(o[8 * e + 4], o[8 * e + 5]), pack_bf16(o[8 * e + 6], o[8 * e + 7]));
-          } else if (valid) {
-            float4 *dst = reinterpret_cast<float4 *>(p.part_o + prow * D + c * 32);
+              v[e] = make_uint4(pack_bf16(o[8 * e], o[8 * e + 1]), pack_bf16(o[8 * e + 2], o[8 * e + 3]),
+                                pack_bf16(o[8 * e + 4], o[8 * e + 5]), pack_bf16(o[8 * e + 6], o[8 * e + 7]));
+            store_rows(v, orow + c * 32, valid, lane);
+          } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            for (int e = 0; e < 8; ++e)
+              if (valid) prow[(c * 8 + e) * (2 * BM)] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
           __syncwarp();
         }
         if (valid) {
           if (whole)
-            p.LSE[qhead * p.lse_shead + qrow] = l > 0.0f ? (m + lg2(l)) * 0.69314718055994531f : -INFINITY;
+            p.LSE[qhead * p.lse_shead + u.tok0 + tok] = l > 0.0f ? (m + lg2(l)) * 0.69314718055994531f : -INFINITY;
           else
-            p.part_ml[prow] = make_float2(m, l);
+            p.part_ml[slot * (2 * BM) + t * BM + row] = make_float2(m, l);
         }
       }
       if (!two) {
@@ -753,49 +802,94 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 // Joins a unit that runs' ends cut into parts: block (c, y) the unit that
-// boundary c + 1 falls into, if that is the unit's first boundary.  A warp to
-// a row; parts in the order of the keys.
+// boundary c + 1 falls into, if that is the unit's first boundary.  A block takes 32
+// rows and a warp D / 8 columns of them, a lane to a row as in the parts, PB parts loaded
+// at once, in the order of the keys; the kernel is a few dependent loads long.
+// Rows go out through shared memory.
 template <int D>
 __global__ void __launch_bounds__(256) paged_combine_kernel(const Params p) {
-  constexpr int E = D / 32;
+  constexpr int Q = D / 32, PB = 4;  // float4 a lane, parts at once
+  __shared__ uint2 rows[32][D / 4 + 1];
   pdl_wait();  // the parts and boundaries
   const int c = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Boundary bd = p.bounds[c];
-  if (!bd.cut || run_start(bd.total, c - 1) > bd.u0) return;
-  // rows are numbered as in the unit's tiles
-  const int tiles = bd.ntok > p.tpt ? 2 : 1;
-  for (int r = warp * gridDim.y + blockIdx.y; r < tiles * BM; r += gridDim.y * 8) {
-    const int rt = (r % BM) / p.G, tok = (r / BM) * p.tpt + rt;
-    if (rt >= p.tpt || tok >= bd.ntok) continue;
-    float m = -INFINITY, l = 0.0f, o[E];
+  const int tiles = bd.ntok > p.tpt ? 2 : 1;  // rows are numbered as in the unit's query tiles
+  if (!bd.cut || (int)blockIdx.y >= tiles * BM / 32) return;
+  if (tile_at(run_start(bd.total, c - 1) - bd.u0, bd.w) > 0) return;
+  const int r = blockIdx.y * 32 + lane;
+  const int rt = (r % BM) / p.G, tok = (r / BM) * p.tpt + rt;
+  const bool valid = rt < p.tpt && tok < bd.ntok;
+  if (!__syncthreads_or(valid)) return;
+  float m = -INFINITY, l = 0.0f;
+  float4 o[Q];
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.0f;
-    for (int k = c - 1; k < CTAS; ++k) {
-      const long long t0 = run_start(bd.total, k);
-      if (t0 >= bd.u1) break;
-      if (k >= c && run_start(bd.total, k + 1) == t0) continue;  // an empty run
-      const int64_t prow = ((int64_t)k * 2 + (k < c ? 1 : 0)) * (2 * BM) + r;
-      const float2 x = p.part_ml[prow];
-      const float *po = p.part_o + prow * D + lane * E;
-      float v[E];
+  for (int q = 0; q < Q; ++q) o[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  // block c - 1 holds the first part, as its last unit; the next blocks the others, as
+  // their first, down to the one that holds the unit's last key tile
+  int j0 = 0;
+  for (int k0 = c - 1; j0 < bd.nt; k0 += PB) {
+    float2 x[PB];
+    float4 v[PB][Q];
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = po[e];
-      const float top = fmaxf(m, x.x);
-      if (top == -INFINITY) continue;
-      const float w0 = ex2(m - top), w1 = ex2(x.x - top);
-      m = top;
-      l = l * w0 + x.y * w1;
+    for (int i = 0; i < PB; ++i) {
+      const int k = k0 + i;
+      const int j1 = k + 1 < CTAS ? min(bd.nt, tile_at(run_start(bd.total, k + 1) - bd.u0, bd.w)) : bd.nt;
+      x[i] = make_float2(-INFINITY, 0.0f);
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = o[e] * w0 + v[e] * w1;
+      for (int q = 0; q < Q; ++q) v[i][q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (j1 > j0 && valid) {  // an empty run holds no part
+        const int64_t slot = (int64_t)k * 2 + (k < c ? 1 : 0);
+        const float4 *po = reinterpret_cast<const float4 *>(p.part_o) + slot * (2 * BM * D / 4) + r;
+        x[i] = p.part_ml[slot * (2 * BM) + r];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) v[i][q] = po[(warp * Q + q) * (2 * BM)];
+      }
+      j0 = max(j0, j1);
     }
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    const int64_t qrow = (int64_t)bd.tok0 + tok, qhead = (int64_t)bd.head * p.G + r % BM - rt * p.G;
-    __nv_bfloat16 *dst = p.O + qrow * p.o_stok + qhead * p.o_shead + lane * E;
+    float top = m;
 #pragma unroll
-    for (int e = 0; e < E; e += 2)
-      *reinterpret_cast<uint32_t *>(dst + e) = pack_bf16(o[e] * inv, o[e + 1] * inv);
-    if (lane == 0)
-      p.LSE[qhead * p.lse_shead + qrow] = l > 0.0f ? (m + lg2(l)) * 0.69314718055994531f : -INFINITY;
+    for (int i = 0; i < PB; ++i) top = fmaxf(top, x[i].x);
+    if (top == -INFINITY) continue;
+    const float w0 = ex2(m - top);
+    m = top;
+    l *= w0;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      o[q].x *= w0;
+      o[q].y *= w0;
+      o[q].z *= w0;
+      o[q].w *= w0;
+    }
+#pragma unroll
+    for (int i = 0; i < PB; ++i) {
+      const float w = ex2(x[i].x - top);
+      l = fmaf(w, x[i].y, l);
+      if (x[i].x == -INFINITY) continue;  // no visible key in this part: it may have no O
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        o[q].x = fmaf(w, v[i][q].x, o[q].x);
+        o[q].y = fmaf(w, v[i][q].y, o[q].y);
+        o[q].z = fmaf(w, v[i][q].z, o[q].z);
+        o[q].w = fmaf(w, v[i][q].w, o[q].w);
+      }
+    }
+  }
+  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+#pragma unroll
+  for (int q = 0; q < Q; ++q)
+    rows[lane][warp * Q + q] =
+        make_uint2(pack_bf16(o[q].x * inv, o[q].y * inv), pack_bf16(o[q].z * inv, o[q].w * inv));
+  if (warp == 0 && valid)
+    p.LSE[((int64_t)bd.head * p.G + r % BM - rt * p.G) * p.lse_shead + bd.tok0 + tok] =
+        l > 0.0f ? (m + lg2(l)) * 0.69314718055994531f : -INFINITY;
+  __syncthreads();
+  for (int i = warp; i < 32; i += 8) {
+    const int ri = blockIdx.y * 32 + i, ti = (ri % BM) / p.G, tk = (ri / BM) * p.tpt + ti;
+    if (ti >= p.tpt || tk >= bd.ntok) continue;
+    uint2 *dst = reinterpret_cast<uint2 *>(
+        p.O + ((int64_t)bd.tok0 + tk) * p.o_stok +
+        ((int64_t)bd.head * p.G + ri % BM - ti * p.G) * p.o_shead);
+    if (lane < D / 4) dst[lane] = rows[i][lane];
   }
 }
 
@@ -849,7 +943,7 @@ cudaError_t launch(const PagedAttnArgs &a, const WaitCfg &wc, cudaStream_t st) {
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   timing_mark(st, 1);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(CTAS - 1, 4);
+  cfg.gridDim = dim3(CTAS - 1, 2 * BM / 32);
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
