@@ -327,119 +327,77 @@ def chain_bwd_noalloc(dO, A, B, C, O, LSE, f, mask, scale, dA, dB, dC, stream=No
         "chain_bwd_noalloc")
 
 
-# Norm + rotation and the paged cache: these calls take bf16 and f32 by their
-# values, so a tensor of another type is refused here (desc() would pass an
-# f16 tensor's two-byte payload as bf16), as is one that is not on the current
-# device, where the kernels launch.
-_FLOATS = {torch.bfloat16: BF16, torch.float32: F32}
-_I64x4 = ctypes.c_int64 * 4
+# Norm + rotation and the paged cache: calls of a few microseconds on the GPU,
+# whose arguments the native module marshals.  It takes bf16 and f32 tensors by their
+# values (desc() would pass an f16 tensor's two-byte payload as bf16) and
+# refuses a tensor that is not on the current device, where the kernels launch.
+_calls = None
 
 
-def _fdesc(t):
-    dt = _FLOATS.get(t.dtype)
-    if dt is None:
-        raise TypeError(f"chain_gb300: bf16 or f32 tensors only, not {t.dtype}")
-    shape = t.shape
-    if not 1 <= len(shape) <= 4:
-        raise ValueError("chain_gb300: tensors must have 1 to 4 dimensions")
-    return ctypes.byref(TensorDesc(t.data_ptr(), dt, len(shape), _I64x4(*shape), _I64x4(*t.stride())))
+def _small():
+    """The native module, with the library loaded (and built, if missing)."""
+    global _calls
+    if _calls is None:
+        _load()
+        from . import _build
+        if not os.path.exists(_build.NATIVE):
+            build()
+        from . import _native
+        _native.setup(torch.bfloat16, torch.float32, torch.int32, ChainError)
+        _calls = _native
+    return _calls
 
 
-def _on_current_device(*ts):
+def _where(stream):
+    """The current device, and the handle of `stream` or of its current stream."""
     dev = torch.cuda.current_device()
-    for t in ts:
-        if t is not None and not (t.is_cuda and t.get_device() == dev):
-            raise ValueError(f"chain_gb300: tensors must be on the current device, cuda:{dev}")
+    if stream is None:
+        return dev, torch._C._cuda_getCurrentRawStream(dev)
+    return dev, _stream(stream).value or 0
 
 
-def _i32(t, what, ndim=1):
-    if t.dtype != torch.int32 or t.dim() != ndim:
-        raise ValueError(f"{what} must be a CUDA int32 tensor of {ndim} dimension{'s' * (ndim > 1)}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{what} must be contiguous")
-    return t.data_ptr()
-
-
-def _positions(positions, tokens):
-    if positions is None:
-        return None
-    if not positions.is_contiguous():
-        raise ValueError("positions must be contiguous")
-    if positions.numel() != tokens:
-        raise ValueError("positions must hold one position for each token")
-    return _i32(positions, "positions", positions.dim())
-
-
-def _paged(cu_seqlens, kv_lens, page_table):
-    """The C ABI's arguments from cu_seqlens to max_pages."""
-    batch = kv_lens.shape[0] if kv_lens.dim() == 1 else -1
-    cu, lens = _i32(cu_seqlens, "cu_seqlens"), _i32(kv_lens, "kv_lens")
-    table = _i32(page_table, "page_table", 2)
-    if cu_seqlens.shape[0] != batch + 1 or page_table.shape[0] != batch:
-        raise ValueError("cu_seqlens [batch + 1], kv_lens [batch] and page_table [batch][max_pages] "
-                         "must agree on the batch")
-    return cu, lens, table, page_table.stride(0) if batch > 1 else page_table.shape[1], batch, \
-        page_table.shape[1]
+def _bytes(t):
+    return t.numel() * t.element_size()
 
 
 def chain_qk_norm_rope(Q, K, gq, gk, inv_freq, positions, eps, pairs, Qo, Ko, stream=None):
     """Per-head RMS norm and rotary embedding of Q and K; see include/chain.h."""
-    _on_current_device(Q, K, gq, gk, inv_freq, positions, Qo, Ko)
-    _ok(_load().chain_qk_norm_rope(_fdesc(Q), _fdesc(K), _fdesc(gq), _fdesc(gk),
-                                   None if inv_freq is None else _fdesc(inv_freq),
-                                   _positions(positions, Q.numel() // max(1, Q.shape[-1] * Q.shape[-2])),
-                                   eps, pairs, _fdesc(Qo), _fdesc(Ko), _stream(stream)),
-        "chain_qk_norm_rope")
+    _small().qk_norm_rope(Q, K, gq, gk, inv_freq, positions, eps, pairs, Qo, Ko, *_where(stream))
 
 
 def chain_qk_norm_rope_bwd_workspace_size(Q) -> int:
-    return int(_load().chain_qk_norm_rope_bwd_workspace_size(_fdesc(Q)))
+    return int(_load().chain_qk_norm_rope_bwd_workspace_size(_ref(desc(Q))))
 
 
 def chain_qk_norm_rope_bwd(dQo, dKo, Q, K, gq, gk, inv_freq, positions, eps, pairs, dQ, dK, dgq, dgk,
                            workspace, stream=None):
     """Gradients of chain_qk_norm_rope; see include/chain.h."""
-    _on_current_device(dQo, dKo, Q, K, gq, gk, inv_freq, positions, dQ, dK, dgq, dgk, workspace)
-    _ok(_load().chain_qk_norm_rope_bwd(_fdesc(dQo), _fdesc(dKo), _fdesc(Q), _fdesc(K), _fdesc(gq),
-                                       _fdesc(gk), None if inv_freq is None else _fdesc(inv_freq),
-                                       _positions(positions,
-                                                  Q.numel() // max(1, Q.shape[-1] * Q.shape[-2])),
-                                       eps, pairs, _fdesc(dQ), _fdesc(dK), _fdesc(dgq), _fdesc(dgk),
-                                       workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                       _stream(stream)), "chain_qk_norm_rope_bwd")
+    _small().qk_norm_rope_bwd(dQo, dKo, Q, K, gq, gk, inv_freq, positions, eps, pairs, dQ, dK, dgq, dgk,
+                              workspace, _bytes(workspace), *_where(stream))
 
 
 def chain_paged_append(K, V, cu_seqlens, kv_lens, page_table, Kc, Vc, stream=None):
     """Writes the new tokens' K and V into their pages; see include/chain.h."""
-    _on_current_device(K, V, cu_seqlens, kv_lens, page_table, Kc, Vc)
-    _ok(_load().chain_paged_append(_fdesc(K), _fdesc(V), *_paged(cu_seqlens, kv_lens, page_table),
-                                   _fdesc(Kc), _fdesc(Vc), _stream(stream)), "chain_paged_append")
+    _small().paged_append(K, V, cu_seqlens, kv_lens, page_table, Kc, Vc, *_where(stream))
 
 
 def chain_qk_norm_rope_append(Q, K, V, gq, gk, inv_freq, eps, pairs, cu_seqlens, kv_lens, page_table, Kc,
                               Vc, Qo, stream=None):
     """chain_qk_norm_rope at the tokens' cache positions with K and V written
     into their pages; see include/chain.h."""
-    _on_current_device(Q, K, V, gq, gk, inv_freq, cu_seqlens, kv_lens, page_table, Kc, Vc, Qo)
-    _ok(_load().chain_qk_norm_rope_append(_fdesc(Q), _fdesc(K), _fdesc(V), _fdesc(gq), _fdesc(gk),
-                                          None if inv_freq is None else _fdesc(inv_freq), eps, pairs,
-                                          *_paged(cu_seqlens, kv_lens, page_table), _fdesc(Kc), _fdesc(Vc),
-                                          _fdesc(Qo), _stream(stream)), "chain_qk_norm_rope_append")
+    _small().qk_norm_rope_append(Q, K, V, gq, gk, inv_freq, eps, pairs, cu_seqlens, kv_lens, page_table,
+                                 Kc, Vc, Qo, *_where(stream))
 
 
 def chain_fwd_paged_workspace_size(Q, Kc) -> int:
-    return int(_load().chain_fwd_paged_workspace_size(_fdesc(Q), _fdesc(Kc)))
+    return int(_load().chain_fwd_paged_workspace_size(_ref(desc(Q)), _ref(desc(Kc))))
 
 
 def chain_fwd_paged(Q, Kc, Vc, cu_seqlens, kv_lens, page_table, mask, scale, O, LSE, workspace,
                     stream=None):
     """Attention of a chunk of new tokens over a paged cache; see include/chain.h."""
-    _on_current_device(Q, Kc, Vc, cu_seqlens, kv_lens, page_table, O, LSE, workspace)
-    _ok(_load().chain_fwd_paged(_fdesc(Q), _fdesc(Kc), _fdesc(Vc),
-                                *_paged(cu_seqlens, kv_lens, page_table), mask, scale, _fdesc(O),
-                                _fdesc(LSE), workspace.data_ptr(),
-                                workspace.numel() * workspace.element_size(), _stream(stream)),
-        "chain_fwd_paged")
+    _small().fwd_paged(Q, Kc, Vc, cu_seqlens, kv_lens, page_table, mask, scale, O, LSE, workspace,
+                       _bytes(workspace), *_where(stream))
 
 
 def sp_relayout(shards, p, head_group, out, stream=None):

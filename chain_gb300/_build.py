@@ -2,7 +2,9 @@
 
 Each translation unit under csrc/ compiles in parallel to an object file in
 chain_gb300/_build/, then nvcc links the shared library beside this file.
-Rebuilds only what changed (sources or the shared headers).
+Rebuilds only what changed (sources or the shared headers).  binding.c, the
+CPython entry to the library's small calls, is compiled with gcc into
+chain_gb300/_native and linked to the library beside it.
 """
 from __future__ import annotations
 
@@ -11,12 +13,14 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libchain_gb300.so")
+NATIVE = os.path.join(HERE, "_native" + sysconfig.get_config_var("EXT_SUFFIX"))
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
@@ -50,7 +54,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"compilation failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         if verbose and (r.stdout or r.stderr):
             print(r.stdout + r.stderr)
 
@@ -61,8 +65,14 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
              os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs))
     if force or stale:
         tmp = LIB + f".tmp{os.getpid()}"
-        run([nvcc, *ARCH, "-shared", "-o", tmp, *objs])
+        run([nvcc, *ARCH, "-shared", "-Xlinker", "-soname=" + os.path.basename(LIB), "-o", tmp, *objs])
         os.replace(tmp, LIB)
+    src = os.path.join(CSRC, "binding.c")
+    if force or not os.path.exists(NATIVE) or os.path.getmtime(NATIVE) < max(os.path.getmtime(src), hdr_t):
+        tmp = NATIVE + f".tmp{os.getpid()}"
+        run(["gcc", "-O2", "-std=c11", "-Wall", "-fPIC", "-shared", "-I", sysconfig.get_paths()["include"], src,
+             "-o", tmp, "-L" + HERE, "-lchain_gb300", "-Wl,-rpath,$ORIGIN"])
+        os.replace(tmp, NATIVE)
     return LIB
 
 
