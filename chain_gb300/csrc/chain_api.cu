@@ -918,8 +918,8 @@ static int heads_view(const chain_tensor_t *t, int max_nd, NormRopeSide *s, int6
     if (t->shape[i] > 1 && (t->stride[i] <= 0 || (t->stride[i] * es) % 16 ||
                             t->stride[i] > (int64_t(1) << 40)))
       return CHAIN_ERR_ARG;
-  if (nd == 4 && *batch > 1) s->s_batch = t->stride[0];
   if (*n > 1) s->s_tok = t->stride[nd - 3];
+  s->s_batch = nd == 4 && *batch > 1 ? t->stride[0] : *n * s->s_tok;  // one entry: as if tokens went on
   if (*heads > 1) s->s_head = t->stride[nd - 2];
   return CHAIN_OK;
 }

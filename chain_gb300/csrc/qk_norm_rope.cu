@@ -17,16 +17,19 @@
 // is slow here, so angles are kept in turns as 64-bit fixed point: w_i / 2 pi
 // is formed once per block as an integer U_i = w_i / (2 pi) 2^64 (mod 2^64,
 // exact to one unit), and p U_i mod 2^64 is the angle of position p: exact
-// modular arithmetic whose error is |p| 2^-64 turns.  Its top 32 bits go to
-// sincospif.
+// modular arithmetic whose error is |p| 2^-64 turns.
+#include <algorithm>
+
 #include "internal.h"
 
 namespace chain {
 namespace {
 
-constexpr int THREADS = 256;
+constexpr int THREADS = 128;
 constexpr int WARPS = THREADS / 32;
 constexpr int MAX_FREQ = 64;  // rot / 2 at d = 128
+constexpr int SMS = 152;
+using std::min;
 
 // 1 / (2 pi) = 0.159154943... as a 128-bit binary fraction
 constexpr unsigned long long INV_2PI_HI = 0x28be60db9391054aull;
@@ -52,125 +55,203 @@ __device__ __forceinline__ unsigned long long turns_per_position(float w) {
   return (b >> 31) ? 0ull - u : u;
 }
 
-// (cos, sin) of position p and frequency U
+// (cos, sin) of position p and frequency U.  The angle's nearest quarter turn
+// comes off exactly, in integers; what is left, |x| <= pi/4, goes through the Taylor
+// series (to x^9 and x^8: their next terms are below 2^-25).  CUDA's sincospif in
+// their place made up a fifth of the forward's instructions.
 __device__ __forceinline__ float2 angle(int p, unsigned long long u) {
   const unsigned long long a = u * (unsigned long long)(long long)p;
-  const float t = (float)(int)(a >> 32) * 0x1p-31f;  // twice the turns, in [-1, 1]
-  float2 cs;
-  sincospif(t, &cs.y, &cs.x);
-  return cs;
+  const uint32_t t = (uint32_t)(a >> 32);         // turns in units of 2^-32
+  const uint32_t q = (t + 0x20000000u) >> 30;     // quarter turns, mod 4
+  const float x = (float)(int)(t - (q << 30)) * 1.46291807926715969e-9f;  // 2 pi 2^-32
+  const float z = x * x;
+  float s = fmaf(z, 2.75573192e-6f, -1.98412698e-4f);  // 1/9!, -1/7!
+  s = fmaf(z, s, 8.33333333e-3f);                      // 1/5!
+  s = fmaf(z, s, -1.66666667e-1f);                     // -1/3!
+  s = fmaf(x * z, s, x);
+  float c = fmaf(z, 2.48015873e-5f, -1.38888889e-3f);  // 1/8!, -1/6!
+  c = fmaf(z, c, 4.16666667e-2f);                      // 1/4!
+  c = fmaf(z, c, -0.5f);
+  c = fmaf(z, c, 1.0f);
+  if (q & 1) {
+    const float w = s;
+    s = c;
+    c = -w;
+  }
+  return q & 2 ? make_float2(-c, -s) : make_float2(c, s);
 }
 
-// ------------------------------------------------------- eight elements a lane
+// ------------------------------------------------------ sixteen elements a lane
+// A lane holds sixteen elements of a row as two groups of eight: eight pairs, the
+// firsts and the seconds.  Pairs (i, i + rot/2): the firsts from the first half
+// of the rotated elements and the seconds from the second, so that a rotation
+// needs no other lane; pairs (2i, 2i + 1), and elements that do not rotate: sixteen
+// in a row.  (With eight elements a lane, the reduction, the addressing and the loop
+// cost twice as much for each element, and the instruction issue bounded the kernels.)
+constexpr int EPL = 16;
+struct Lane {
+  int a, b;  // first elements of its groups of eight, as they lie in memory
+  int f;     // its first frequency
+  bool on;   // its elements rotate
+};
+template <int D, bool NEIGHBOUR>
+__device__ __forceinline__ Lane lane_of(int lane, int rot) {
+  const int l = lane % (D / EPL);
+  Lane r;
+  r.on = l * 16 < rot;
+  r.f = l * 8;
+  const bool split = r.on && !NEIGHBOUR;
+  r.a = split ? l * 8 : l * 16;
+  r.b = split ? rot / 2 + l * 8 : l * 16 + 8;
+  return r;
+}
+
+// Asynchronous copy of 16 bytes into shared memory
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void commit_async() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_async() {  // all but the newest N groups have arrived
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A lane's sixteen elements, as they lie in memory; get() gives the pairs' firsts in
+// f[0..7] and their seconds in f[8..15].  In a ring slot each 16-byte part of a
+// warp's lanes lies side by side, 512 bytes a part.
 template <typename T>
-struct Row8;
+struct Row;
 template <>
-struct Row8<__nv_bfloat16> {
-  uint4 v;
-  __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
-    v = *reinterpret_cast<const uint4 *>(p);
+struct Row<__nv_bfloat16> {
+  uint4 a, b;
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p, const Lane &ln) {
+    a = *reinterpret_cast<const uint4 *>(p + ln.a);
+    b = *reinterpret_cast<const uint4 *>(p + ln.b);
   }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  static __device__ __forceinline__ void fetch(uint32_t slot, const __nv_bfloat16 *p, const Lane &ln) {
+    copy_async(slot, p + ln.a);
+    copy_async(slot + 512, p + ln.b);
+  }
+  __device__ __forceinline__ void take(const uint8_t *slot) {
+    a = *reinterpret_cast<const uint4 *>(slot);
+    b = *reinterpret_cast<const uint4 *>(slot + 512);
+  }
+  static __device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
+  static __device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+  template <bool NEIGHBOUR>
+  __device__ __forceinline__ void get(float (&f)[16]) const {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      f[2 * k] = __uint_as_float(w[k] << 16);
-      f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    for (int k = 0; k < 8; ++k) {
+      f[NEIGHBOUR ? k : 2 * k] = lo(w[k]);
+      f[NEIGHBOUR ? 8 + k : 2 * k + 1] = hi(w[k]);
     }
   }
-  static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&f)[8]) {
-    *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
-                                               pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+  template <bool NEIGHBOUR>
+  static __device__ __forceinline__ void store(__nv_bfloat16 *p, const Lane &ln, const float (&f)[16]) {
+    uint32_t w[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      w[k] = NEIGHBOUR ? pack_bf16(f[k], f[8 + k]) : pack_bf16(f[2 * k], f[2 * k + 1]);
+    *reinterpret_cast<uint4 *>(p + ln.a) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4 *>(p + ln.b) = make_uint4(w[4], w[5], w[6], w[7]);
   }
 };
 template <>
-struct Row8<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float *p) {
-    a = reinterpret_cast<const float4 *>(p)[0];
-    b = reinterpret_cast<const float4 *>(p)[1];
+struct Row<float> {
+  float4 v[4];
+  __device__ __forceinline__ void load(const float *p, const Lane &ln) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = reinterpret_cast<const float4 *>(p + (k < 2 ? ln.a : ln.b))[k & 1];
   }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  static __device__ __forceinline__ void fetch(uint32_t slot, const float *p, const Lane &ln) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) copy_async(slot + 512 * k, p + (k < 2 ? ln.a : ln.b) + 4 * (k & 1));
   }
-  static __device__ __forceinline__ void store(float *p, const float (&f)[8]) {
-    reinterpret_cast<float4 *>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+  __device__ __forceinline__ void take(const uint8_t *slot) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const float4 *>(slot + 512 * k);
+  }
+  template <bool NEIGHBOUR>
+  __device__ __forceinline__ void get(float (&f)[16]) const {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float m[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[NEIGHBOUR ? 2 * k + e / 2 + 8 * (e & 1) : 4 * k + e] = m[e];
+    }
+  }
+  template <bool NEIGHBOUR>
+  static __device__ __forceinline__ void store(float *p, const Lane &ln, const float (&f)[16]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      reinterpret_cast<float4 *>(p + (k < 2 ? ln.a : ln.b))[k & 1] =
+          NEIGHBOUR ? make_float4(f[2 * k], f[8 + 2 * k], f[2 * k + 1], f[9 + 2 * k])
+                    : make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
   }
 };
 
-__device__ __forceinline__ void load_weight(const NormRopeWeight &g, int e0, float (&f)[8]) {
+template <bool NEIGHBOUR>
+__device__ __forceinline__ void load_weight(const NormRopeWeight &g, const Lane &ln, float (&f)[16]) {
   if (g.bf16) {
-    Row8<__nv_bfloat16> r;
-    r.load(static_cast<const __nv_bfloat16 *>(g.ptr) + e0);
-    r.get(f);
+    Row<__nv_bfloat16> r;
+    r.load(static_cast<const __nv_bfloat16 *>(g.ptr), ln);
+    r.get<NEIGHBOUR>(f);
   } else {
-    Row8<float> r;
-    r.load(static_cast<const float *>(g.ptr) + e0);
-    r.get(f);
+    Row<float> r;
+    r.load(static_cast<const float *>(g.ptr), ln);
+    r.get<NEIGHBOUR>(f);
   }
 }
 
-// What a lane knows of the rotation of its eight elements at one token.
-// Pairs (i, i + rot/2): all eight lie in one half and their partners in
-// lane `src`; pairs (2i, 2i + 1) lie within the lane.
-struct LaneRope {
+// Cosines and sines of a lane's eight pairs at one token
+struct Angles {
   float c[8], s[8];
-  int src;     // partner lane (pairs of halves)
-  bool on;     // the elements rotate
-  bool second; // they are the second of their pairs (pairs of halves)
 };
 
-template <int D>
-__device__ __forceinline__ void lane_rope_setup(LaneRope &lr, int lane, int rot, int neighbour) {
-  constexpr int LPR = D / 8;  // lanes a row
-  const int l = lane % LPR;
-  lr.on = l * 8 < rot;
-  lr.second = !neighbour && l * 16 >= rot;
-  const int half = rot / 16;  // lanes of half the rotated elements
-  lr.src = neighbour || !lr.on ? lane : (lr.second ? lane - half : lane + half);
-}
-
-// The token's (cos, sin) of each frequency into the warp's table, then the
-// lane's own into registers.  Elements that do not rotate get (1, 0).
-template <int D>
-__device__ __forceinline__ void lane_rope_token(LaneRope &lr, int lane, int rot, int neighbour, int p,
-                                                const unsigned long long *turns, float2 *table) {
-  constexpr int LPR = D / 8;
-  const int l = lane % LPR;
+// Every frequency's (cos, sin) at position p into the warp's table, each
+// computed once.
+__device__ __forceinline__ void put_angles(int lane, int rot, int p, const unsigned long long *turns,
+                                           float2 *table) {
   __syncwarp();  // the table's last readers are done
   for (int f = lane; f < rot / 2; f += 32) table[f] = angle(p, turns[f]);
   __syncwarp();
+}
+// The lane's own out of it; elements that do not rotate get (1, 0).
+__device__ __forceinline__ void take_angles(Angles &an, const Lane &ln, const float2 *table) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    float2 cs = make_float2(1.0f, 0.0f);
-    if (lr.on) {
-      const int e = l * 8 + k;
-      cs = table[neighbour ? e / 2 : (lr.second ? e - rot / 2 : e)];
-    }
-    lr.c[k] = cs.x;
-    lr.s[k] = cs.y;
+  for (int k = 0; k < 4; ++k) {
+    float4 cs = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
+    if (ln.on) cs = *reinterpret_cast<const float4 *>(table + ln.f + 2 * k);
+    an.c[2 * k] = cs.x;
+    an.s[2 * k] = cs.y;
+    an.c[2 * k + 1] = cs.z;
+    an.s[2 * k + 1] = cs.w;
   }
 }
 
-// y = R u (SIGN = 1) or R^T u (SIGN = -1).  Every lane of the warp calls it.
-template <int SIGN>
-__device__ __forceinline__ void rotate(const LaneRope &lr, int neighbour, float (&u)[8]) {
-  if (neighbour) {
+// R^T u: u[0..7] the firsts, u[8..15] the seconds of the pairs
+__device__ __forceinline__ void rotate_back(const Angles &an, float (&u)[16]) {
 #pragma unroll
-    for (int k = 0; k < 8; k += 2) {
-      const float a = u[k], b = u[k + 1], s = SIGN * lr.s[k];
-      u[k] = a * lr.c[k] - b * s;
-      u[k + 1] = a * s + b * lr.c[k];
-    }
-  } else {
-    const float sg = lr.second ? (float)SIGN : -(float)SIGN;
+  for (int k = 0; k < 8; ++k) {
+    const float x = u[k], y = u[8 + k];
+    u[k] = fmaf(y, an.s[k], x * an.c[k]);
+    u[8 + k] = fmaf(-x, an.s[k], y * an.c[k]);
+  }
+}
+
+// Norm weight and rotation in one matrix for each pair: R(p) diag(g).  The row's
+// 1 / rms, a scalar, is multiplied in afterwards.
+struct Turn {
+  float xx[8], xy[8], yx[8], yy[8];
+};
+__device__ __forceinline__ void turn_of(Turn &t, const Angles &an, const float (&g)[16]) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float o = __shfl_sync(0xffffffffu, u[k], lr.src);
-      u[k] = u[k] * lr.c[k] + o * (sg * lr.s[k]);
-    }
+  for (int k = 0; k < 8; ++k) {
+    t.xx[k] = an.c[k] * g[k];
+    t.xy[k] = -an.s[k] * g[8 + k];
+    t.yx[k] = an.s[k] * g[k];
+    t.yy[k] = an.c[k] * g[8 + k];
   }
 }
 
@@ -182,187 +263,354 @@ __device__ __forceinline__ float row_sum(float v) {
 }
 
 // Offset in elements of token t: t = b n + i of [B][n][H][d].
-__device__ __forceinline__ int64_t token_off(const NormRopeSide &x, int64_t t, int64_t n) {
+__device__ __forceinline__ int64_t token_off(const NormRopeSide &x, int t, int n) {
   if (x.s_batch == n * x.s_tok) return t * x.s_tok;
-  const int64_t b = t / n;
+  const int b = t / n;
   return b * x.s_batch + (t - b * n) * x.s_tok;
 }
 
-// Rows [h0, h1) of one token: norm, rotation, store.
-template <typename T, int D>
-__device__ __forceinline__ void fwd_rows(const T *src, int64_t s_head, T *dst, int64_t d_head, int h0,
-                                         int h1, const float (&g)[8], float eps, int neighbour,
-                                         const LaneRope &lr, int lane) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR, U = 4;
-  const int sub = lane / LPR, e0 = (lane % LPR) * 8;
-  for (int h = h0 + sub; h - sub < h1; h += RPW * U) {
-    Row8<T> x[U];
+template <int D>
+__device__ __forceinline__ void fwd_row(float (&f)[16], float eps, const Turn &t) {
+  float q[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int hh = h + u * RPW;
-      if (hh < h1) x[u].load(src + hh * s_head + e0);
-    }
+  for (int k = 0; k < 16; ++k) q[k & 3] = fmaf(f[k], f[k], q[k & 3]);
+  const float r = rsqrtf(row_sum<D / EPL>((q[0] + q[1]) + (q[2] + q[3])) * (1.0f / D) + eps);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int hh = h + u * RPW;
-      if (hh - sub >= h1) break;  // warp-uniform
-      float f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      if (hh < h1) x[u].get(f);
-      float q = 0.0f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) q = fmaf(f[k], f[k], q);
-      const float r = rsqrtf(row_sum<LPR>(q) * (1.0f / D) + eps);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] = f[k] * r * g[k];
-      rotate<1>(lr, neighbour, f);
-      if (hh < h1) Row8<T>::store(dst + hh * d_head + e0, f);
-    }
+  for (int k = 0; k < 8; ++k) {
+    const float x = f[k] * r, y = f[8 + k] * r;
+    f[k] = fmaf(y, t.xy[k], x * t.xx[k]);
+    f[8 + k] = fmaf(x, t.yx[k], y * t.yy[k]);
   }
 }
 
-// Heads [c per, (c + 1) per) of `heads`, clipped
-__device__ __forceinline__ void clip(int lo, int hi, int from, int heads, int &h0, int &h1) {
-  h0 = max(lo - from, 0);
-  h1 = min(hi - from, heads);
+// ------------------------------------------------------------ walk and ring
+// A warp takes the rows of a token in batches of U passes (32 / (D / 16) heads a
+// pass), queries' batches first, then keys', then (cache writes) values'; `run`
+// batches in a row are one warp's, all of the token's where there are tokens
+// enough.
+//
+// The rows of the next STAGES - 1 batches are on their way, by asynchronous
+// copies into shared memory, while a batch is worked on.  Every lane copies
+// the very bytes that it will read, so nothing but its own copies is waited for.
+constexpr int STAGES = 3;
+
+template <typename T>
+constexpr int fwd_passes() { return sizeof(T) == 2 ? 2 : 1; }  // U: 2 KB a batch
+template <typename T>
+constexpr int bwd_passes() { return 1; }  // of x and of dy
+template <typename T>
+constexpr int bwd_stages() { return sizeof(T) == 2 ? 4 : 2; }
+template <typename T>
+constexpr int pass_bytes() { return 32 * EPL * (int)sizeof(T); }
+template <int D>
+constexpr int rows_per_pass() { return 32 / (D / EPL); }
+
+struct Plan {
+  int batches;      // of a token
+  int run, chunks;  // batches a warp takes in a row; of a token, how many such runs
+  int bq, bk;       // batches of queries, of keys
+};
+
+struct Walk {
+  uint32_t c;    // run: tokens times runs of a token stay below 2^31
+  int t, j, j1;  // token (-1: done), its batch, end of the run
+};
+__device__ __forceinline__ void walk_to(Walk &w, const Plan &pl, uint32_t tokens, uint32_t c) {
+  w.c = c;
+  w.t = -1;
+  if (pl.chunks == 1) {
+    if (c < tokens) w.t = (int)c;
+    w.j = 0;
+    w.j1 = pl.batches;
+  } else if (c < tokens * pl.chunks) {
+    w.t = (int)(c / (uint32_t)pl.chunks);
+    w.j = (int)(c - (uint32_t)w.t * pl.chunks) * pl.run;
+    w.j1 = min(w.j + pl.run, pl.batches);
+  }
+}
+__device__ __forceinline__ void walk_on(Walk &w, const Plan &pl, uint32_t tokens) {
+  if (++w.j == w.j1) walk_to(w, pl, tokens, w.c + gridDim.x * WARPS);
 }
 
+__device__ __forceinline__ uint32_t walk_start() { return blockIdx.x * WARPS + (threadIdx.x >> 5); }
+
+// A lane's place in the batches of one side at one token; set at a change of token
+// or side, moved on from batch to batch in between (the 64-bit arithmetic of a
+// place made up half of the instructions when every batch computed its own).
+template <typename T>
+struct Cursor {
+  T *p;          // the lane's row of the next pass
+  int64_t pass;  // elements to the next pass
+  int left;      // rows below the side's last, from the lane's on
+  int batches;   // of this side, from here to the end of the run
+};
 template <typename T, int D>
-__global__ void __launch_bounds__(THREADS) norm_rope_kernel(const NormRopeArgs a, int per) {
+__device__ __forceinline__ void aim(Cursor<T> &c, const NormRopeSide &x, int64_t off, int heads, int j, int batches,
+                                    int passes, int lane) {
+  constexpr int RPW = rows_per_pass<D>();
+  const int h = j * passes * RPW + lane / (D / EPL);
+  c.p = static_cast<T *>(x.ptr) + off + h * x.s_head;
+  c.pass = RPW * x.s_head;
+  c.left = heads - h;
+  c.batches = batches;
+}
+
+// Starts the copies of the next batch into a ring slot.
+template <typename T, int D, int U>
+__device__ __forceinline__ void fetch_rows(uint32_t slot, Cursor<T> &c, const Lane &ln, int lane) {
+  constexpr int RPW = rows_per_pass<D>();
+#pragma unroll
+  for (int u = 0; u < U; ++u, c.p += c.pass)
+    if (c.left > u * RPW) Row<T>::fetch(slot + u * pass_bytes<T>() + lane * 16, c.p, ln);
+  c.left -= U * RPW;
+}
+
+// The batch's rows: norm, rotation, store.
+template <typename T, int D, bool NEIGHBOUR, int U>
+__device__ __forceinline__ void fwd_batch(const uint8_t *slot, Cursor<T> &c, float eps, const Turn &turn,
+                                          const Lane &ln, int lane) {
+  constexpr int RPW = rows_per_pass<D>();
+  const int first = c.left + lane / (D / EPL);  // of the warp's first row
+#pragma unroll
+  for (int u = 0; u < U; ++u, c.p += c.pass) {
+    if (first <= u * RPW) break;  // warp-uniform: no row of this pass is there
+    // a lane beyond the last head works on what its slot holds and stores nothing: sums stay within a row
+    Row<T> x;
+    x.take(slot + u * pass_bytes<T>() + lane * 16);
+    float f[16];
+    x.template get<NEIGHBOUR>(f);
+    fwd_row<D>(f, eps, turn);
+    if (c.left > u * RPW) Row<T>::template store<NEIGHBOUR>(c.p, ln, f);
+  }
+  c.left -= U * RPW;
+}
+
+// The queries' and the keys' weights as a lane's pairs; kept in shared memory, a
+// lane's part of it read at each change of side.
+struct Weights {
+  float g[2][16][8];  // [side][k][lane of a row]
+};
+template <int D, bool NEIGHBOUR>
+__device__ __forceinline__ void put_weights(Weights &w, const NormRopeWeight &gq, const NormRopeWeight &gk, int rot) {
+  constexpr int LPR = D / EPL;
+  if ((int)threadIdx.x < 2 * LPR) {
+    const int side = threadIdx.x / LPR, l = threadIdx.x % LPR;
+    float g[16];
+    load_weight<NEIGHBOUR>(side ? gk : gq, lane_of<D, NEIGHBOUR>(l, rot), g);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) w.g[side][k][l] = g[k];
+  }
+}
+template <int D>
+__device__ __forceinline__ void turn_for(Turn &t, const Weights &w, int side, const Lane &ln, const float2 *table,
+                                         int lane) {
+  Angles an;
+  take_angles(an, ln, table);
+  float g[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) g[k] = w.g[side][k][lane % (D / EPL)];
+  turn_of(t, an, g);
+}
+
+template <typename T, int D, bool NEIGHBOUR>
+__global__ void __launch_bounds__(THREADS, 5) norm_rope_kernel(const NormRopeArgs a, const Plan pl) {
+  constexpr int U = fwd_passes<T>(), B = U * rows_per_pass<D>(), BYTES = U * pass_bytes<T>();
   __shared__ unsigned long long turns[MAX_FREQ];
-  __shared__ float2 table[WARPS][MAX_FREQ];
-  for (int f = threadIdx.x; f < a.rot / 2; f += THREADS) turns[f] = turns_per_position(__ldg(a.inv_freq + f));
-  __syncthreads();
+  __shared__ __align__(16) float2 table[WARPS][MAX_FREQ];
+  __shared__ Weights weights;
+  __shared__ __align__(16) uint8_t ring[WARPS][STAGES][BYTES];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  LaneRope lr;
-  lane_rope_setup<D>(lr, lane, a.rot, a.neighbour);
-  float gq[8], gk[8];
-  load_weight(a.gq, (lane % (D / 8)) * 8, gq);
-  load_weight(a.gk, (lane % (D / 8)) * 8, gk);
-  const int heads = a.H + a.Hkv, chunks = (heads + per - 1) / per;
-  const int64_t items = a.tokens * chunks, step = (int64_t)gridDim.x * WARPS;
-  for (int64_t it = blockIdx.x * (int64_t)WARPS + warp; it < items; it += step) {
-    const int64_t t = it / chunks;
-    const int lo = (int)(it - t * chunks) * per, hi = min(lo + per, heads);
-    const int p = a.positions ? __ldg(a.positions + t) : (int)(t % a.n);
-    lane_rope_token<D>(lr, lane, a.rot, a.neighbour, p, turns, table[warp]);
-    int h0, h1;
-    clip(lo, hi, 0, a.H, h0, h1);
-    fwd_rows<T, D>(static_cast<const T *>(a.q.ptr) + token_off(a.q, t, a.n), a.q.s_head,
-                   static_cast<T *>(a.qo.ptr) + token_off(a.qo, t, a.n), a.qo.s_head, h0, h1, gq, a.eps,
-                   a.neighbour, lr, lane);
-    clip(lo, hi, a.H, a.Hkv, h0, h1);
-    fwd_rows<T, D>(static_cast<const T *>(a.k.ptr) + token_off(a.k, t, a.n), a.k.s_head,
-                   static_cast<T *>(a.ko.ptr) + token_off(a.ko, t, a.n), a.ko.s_head, h0, h1, gk, a.eps,
-                   a.neighbour, lr, lane);
+  const Lane ln = lane_of<D, NEIGHBOUR>(lane, a.rot);
+  Walk ahead, now;
+  walk_to(ahead, pl, (uint32_t)a.tokens, walk_start());
+  now = ahead;
+  int put = 0, got = 0;
+  // a side's cursor at batch w.j of token w.t
+  auto aim_at = [&](Cursor<T> &c, const Walk &w, const NormRopeSide &q, const NormRopeSide &k) {
+    const bool key = w.j >= pl.bq;
+    const NormRopeSide &x = key ? k : q;
+    aim<T, D>(c, x, token_off(x, w.t, (int)a.n), key ? a.Hkv : a.H, key ? w.j - pl.bq : w.j,
+              (key ? w.j1 : min(w.j1, pl.bq)) - w.j, U, lane);
+  };
+  Cursor<T> in, out;
+  in.batches = out.batches = 0;
+  auto fetch = [&]() {
+    if (ahead.t >= 0) {
+      if (in.batches == 0) aim_at(in, ahead, a.q, a.k);
+      --in.batches;
+      fetch_rows<T, D, U>(smem_u32(ring[warp][put]), in, ln, lane);
+      walk_on(ahead, pl, (uint32_t)a.tokens);
+      put = put + 1 == STAGES ? 0 : put + 1;
+    }
+    commit_async();
+  };
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i) fetch();
+  for (int f = threadIdx.x; f < a.rot / 2; f += THREADS) turns[f] = turns_per_position(__ldg(a.inv_freq + f));
+  put_weights<D, NEIGHBOUR>(weights, a.gq, a.gk, a.rot);
+  __syncthreads();
+  Turn turn;
+  int of = -1;  // the token of `table`
+  while (now.t >= 0) {
+    fetch();
+    if (out.batches == 0) {
+      aim_at(out, now, a.qo, a.ko);
+      if (now.t != of) {
+        const int p = a.positions ? __ldg(a.positions + now.t) : now.t % (int)a.n;
+        put_angles(lane, a.rot, p, turns, table[warp]);
+        of = now.t;
+      }
+      turn_for<D>(turn, weights, now.j >= pl.bq, ln, table[warp], lane);
+    }
+    --out.batches;
+    wait_async<STAGES - 1>();
+    fwd_batch<T, D, NEIGHBOUR, U>(ring[warp][got], out, a.eps, turn, ln, lane);
+    walk_on(now, pl, (uint32_t)a.tokens);
+    got = got + 1 == STAGES ? 0 : got + 1;
   }
 }
 
 // ------------------------------------------------------------------ backward
-template <typename T, int D>
-__device__ __forceinline__ void bwd_rows(const T *src, int64_t s_head, const T *dsrc, int64_t g_head,
-                                         T *dst, int64_t d_head, int h0, int h1, const float (&g)[8],
-                                         float (&dg)[8], float eps, int neighbour, const LaneRope &lr,
-                                         int lane) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR, U = 2;
-  const int sub = lane / LPR, e0 = (lane % LPR) * 8;
-  for (int h = h0 + sub; h - sub < h1; h += RPW * U) {
-    Row8<T> x[U], dy[U];
+// f = x in, dx out; v = dy
+template <int D>
+__device__ __forceinline__ void bwd_row(float (&f)[16], float (&v)[16], const float (&g)[16], float (&dg)[16],
+                                        float eps, const Angles &an) {
+  rotate_back(an, v);
+  float q[2] = {0.0f, 0.0f}, w[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int hh = h + u * RPW;
-      if (hh < h1) {
-        x[u].load(src + hh * s_head + e0);
-        dy[u].load(dsrc + hh * g_head + e0);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int hh = h + u * RPW;
-      if (hh - sub >= h1) break;  // warp-uniform
-      float f[8] = {0, 0, 0, 0, 0, 0, 0, 0}, v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      if (hh < h1) {
-        x[u].get(f);
-        dy[u].get(v);
-      }
-      rotate<-1>(lr, neighbour, v);
-      float q = 0.0f, w = 0.0f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        q = fmaf(f[k], f[k], q);
-        w = fmaf(v[k] * g[k], f[k], w);
-      }
-      q = row_sum<LPR>(q);
-      w = row_sum<LPR>(w);
-      const float r = rsqrtf(q * (1.0f / D) + eps);
-      const float c = w * (1.0f / D) * r * r;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        dg[k] = fmaf(v[k] * f[k], r, dg[k]);
-        f[k] = r * (v[k] * g[k] - f[k] * c);
-      }
-      if (hh < h1) Row8<T>::store(dst + hh * d_head + e0, f);
-    }
+  for (int k = 0; k < 16; ++k) {
+    q[k & 1] = fmaf(f[k], f[k], q[k & 1]);
+    w[k & 1] = fmaf(v[k] * g[k], f[k], w[k & 1]);
   }
+  const float sq = row_sum<D / EPL>(q[0] + q[1]), sw = row_sum<D / EPL>(w[0] + w[1]);
+  const float r = rsqrtf(sq * (1.0f / D) + eps);
+  const float c = -(sw * (1.0f / D)) * r * r * r;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const float a = v[k] * r;
+    dg[k] = fmaf(a, f[k], dg[k]);
+    f[k] = fmaf(a, g[k], f[k] * c);
+  }
+}
+
+// One side (queries or keys) of the backward: `heads` heads of every token;
+// the block's sum of a x r into part[D].
+template <typename T, int D, bool NEIGHBOUR>
+__device__ __forceinline__ void bwd_side(const NormRopeArgs &a, const NormRopeSide &x, const NormRopeSide &dy,
+                                         const NormRopeSide &dx, const NormRopeWeight &weight, int heads,
+                                         const Plan &pl, const unsigned long long *turns, float2 *table,
+                                         uint8_t *ring, float (*sums)[D], float *part) {
+  constexpr int LPR = D / EPL, RPW = rows_per_pass<D>();
+  constexpr int STAGES = bwd_stages<T>(), U = bwd_passes<T>(), BYTES = U * pass_bytes<T>();  // of x, and of dy
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / LPR;
+  const Lane ln = lane_of<D, NEIGHBOUR>(lane, a.rot);
+  Walk ahead, now;
+  walk_to(ahead, pl, (uint32_t)a.tokens, walk_start());
+  now = ahead;
+  int put = 0, got = 0;
+  Cursor<T> in_x, in_dy, out;
+  in_x.batches = in_dy.batches = out.batches = 0;
+  auto aim_at = [&](Cursor<T> &c, const Walk &w, const NormRopeSide &s) {
+    aim<T, D>(c, s, token_off(s, w.t, (int)a.n), heads, w.j, w.j1 - w.j, U, lane);
+  };
+  auto fetch = [&]() {
+    if (ahead.t >= 0) {
+      if (in_x.batches == 0) {
+        aim_at(in_x, ahead, x);
+        aim_at(in_dy, ahead, dy);
+      }
+      --in_x.batches;
+      const uint32_t slot = smem_u32(ring) + put * 2 * BYTES;
+      fetch_rows<T, D, U>(slot, in_x, ln, lane);
+      fetch_rows<T, D, U>(slot + BYTES, in_dy, ln, lane);
+      walk_on(ahead, pl, (uint32_t)a.tokens);
+      put = put + 1 == STAGES ? 0 : put + 1;
+    }
+    commit_async();
+  };
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i) fetch();
+  float g[16], dg[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) dg[k] = 0.0f;
+  load_weight<NEIGHBOUR>(weight, ln, g);
+  Angles an;
+  int of = -1;  // the token of `an`
+  while (now.t >= 0) {
+    fetch();
+    if (out.batches == 0) {
+      aim_at(out, now, dx);
+      if (now.t != of) {
+        const int p = a.positions ? __ldg(a.positions + now.t) : now.t % (int)a.n;
+        put_angles(lane, a.rot, p, turns, table);
+        take_angles(an, ln, table);
+        of = now.t;
+      }
+    }
+    --out.batches;
+    wait_async<STAGES - 1>();
+    const uint8_t *slot = ring + got * 2 * BYTES + lane * 16;
+    const int first = out.left + sub;  // of the warp's first row
+#pragma unroll
+    for (int u = 0; u < U; ++u, out.p += out.pass) {
+      if (first <= u * RPW) break;  // warp-uniform
+      float f[16], v[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) f[k] = v[k] = 0.0f;
+      if (out.left > u * RPW) {  // a row that is not there adds nothing to dg
+        Row<T> r;
+        r.take(slot + u * pass_bytes<T>());
+        r.template get<NEIGHBOUR>(f);
+        r.take(slot + BYTES + u * pass_bytes<T>());
+        r.template get<NEIGHBOUR>(v);
+      }
+      bwd_row<D>(f, v, g, dg, a.eps, an);
+      if (out.left > u * RPW) Row<T>::template store<NEIGHBOUR>(out.p, ln, f);
+    }
+    out.left -= U * RPW;
+    walk_on(now, pl, (uint32_t)a.tokens);
+    got = got + 1 == STAGES ? 0 : got + 1;
+  }
+  wait_async<0>();
+  // rows of a warp, then warps of the block
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {  // firsts, then seconds
+    float v = dg[k];
+#pragma unroll
+    for (int o = LPR; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    const int i = NEIGHBOUR ? ln.a + 2 * (k % 8) + k / 8 : (k < 8 ? ln.a : ln.b - 8) + k;
+    if (lane < LPR) sums[warp][i] = v;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < D; i += THREADS) {
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) s += sums[w][i];
+    part[i] = s;
+  }
+  __syncthreads();
 }
 
 // part[block][2][D]: the block's sums of a x r over its query rows and its
 // key rows.  No atomics: rows are dealt to warps by their number and every
-// sum has one order.
-template <typename T, int D>
-__global__ void __launch_bounds__(THREADS) norm_rope_bwd_kernel(const NormRopeBwdArgs b, int per,
-                                                                float *__restrict__ part) {
+// sum has one order.  Queries first, then keys: a weight and its sums take 16
+// registers, and holding both sides' at once would cost a third of the warps.
+template <typename T, int D, bool NEIGHBOUR>
+__global__ void __launch_bounds__(THREADS, 4) norm_rope_bwd_kernel(const NormRopeBwdArgs b, const Plan plq,
+                                                                   const Plan plk, float *__restrict__ part) {
+  constexpr int BYTES = bwd_passes<T>() * pass_bytes<T>();
   __shared__ unsigned long long turns[MAX_FREQ];
-  __shared__ float2 table[WARPS][MAX_FREQ];
-  __shared__ float sums[WARPS][2][D];
+  __shared__ __align__(16) float2 table[WARPS][MAX_FREQ];
+  __shared__ float sums[WARPS][D];
+  __shared__ __align__(16) uint8_t ring[WARPS][bwd_stages<T>() * 2 * BYTES];
   const NormRopeArgs &a = b.fwd;
+  const int warp = threadIdx.x >> 5;
+  pdl_launch_dependents();  // the sums over blocks may be launched; they wait for this grid
   for (int f = threadIdx.x; f < a.rot / 2; f += THREADS) turns[f] = turns_per_position(__ldg(a.inv_freq + f));
   __syncthreads();
-  constexpr int LPR = D / 8;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  LaneRope lr;
-  lane_rope_setup<D>(lr, lane, a.rot, a.neighbour);
-  float gq[8], gk[8], dgq[8] = {0, 0, 0, 0, 0, 0, 0, 0}, dgk[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  load_weight(a.gq, (lane % LPR) * 8, gq);
-  load_weight(a.gk, (lane % LPR) * 8, gk);
-  const int heads = a.H + a.Hkv, chunks = (heads + per - 1) / per;
-  const int64_t items = a.tokens * chunks, step = (int64_t)gridDim.x * WARPS;
-  for (int64_t it = blockIdx.x * (int64_t)WARPS + warp; it < items; it += step) {
-    const int64_t t = it / chunks;
-    const int lo = (int)(it - t * chunks) * per, hi = min(lo + per, heads);
-    const int p = a.positions ? __ldg(a.positions + t) : (int)(t % a.n);
-    lane_rope_token<D>(lr, lane, a.rot, a.neighbour, p, turns, table[warp]);
-    int h0, h1;
-    clip(lo, hi, 0, a.H, h0, h1);
-    bwd_rows<T, D>(static_cast<const T *>(a.q.ptr) + token_off(a.q, t, a.n), a.q.s_head,
-                   static_cast<const T *>(b.dqo.ptr) + token_off(b.dqo, t, a.n), b.dqo.s_head,
-                   static_cast<T *>(a.qo.ptr) + token_off(a.qo, t, a.n), a.qo.s_head, h0, h1, gq, dgq,
-                   a.eps, a.neighbour, lr, lane);
-    clip(lo, hi, a.H, a.Hkv, h0, h1);
-    bwd_rows<T, D>(static_cast<const T *>(a.k.ptr) + token_off(a.k, t, a.n), a.k.s_head,
-                   static_cast<const T *>(b.dko.ptr) + token_off(b.dko, t, a.n), b.dko.s_head,
-                   static_cast<T *>(a.ko.ptr) + token_off(a.ko, t, a.n), a.ko.s_head, h0, h1, gk, dgk,
-                   a.eps, a.neighbour, lr, lane);
-  }
-  // rows of a warp, then warps of the block
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-#pragma unroll
-    for (int o = LPR; o < 32; o <<= 1) {
-      dgq[k] += __shfl_xor_sync(0xffffffffu, dgq[k], o);
-      dgk[k] += __shfl_xor_sync(0xffffffffu, dgk[k], o);
-    }
-    if (lane < LPR) {
-      sums[warp][0][lane * 8 + k] = dgq[k];
-      sums[warp][1][lane * 8 + k] = dgk[k];
-    }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 2 * D; i += THREADS) {
-    float s = 0.0f;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) s += sums[w][i / D][i % D];
-    part[(int64_t)blockIdx.x * 2 * D + i] = s;
-  }
+  part += (int64_t)blockIdx.x * 2 * D;
+  bwd_side<T, D, NEIGHBOUR>(a, a.q, b.dqo, a.qo, a.gq, a.H, plq, turns, table[warp], ring[warp], sums, part);
+  bwd_side<T, D, NEIGHBOUR>(a, a.k, b.dko, a.ko, a.gk, a.Hkv, plk, turns, table[warp], ring[warp], sums, part + D);
 }
 
 // dgq, dgk [D] from the blocks' sums: one block for 32 of the 2 D columns,
@@ -373,6 +621,8 @@ __global__ void __launch_bounds__(THREADS) norm_rope_dg_kernel(const float *__re
   __shared__ float sums[WARPS][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
   float s = 0.0f;
+  pdl_wait();
+#pragma unroll 8
   for (int i = warp; i < blocks; i += WARPS) s += part[(int64_t)i * 2 * d + col];
   sums[warp][lane] = s;
   __syncthreads();
@@ -387,168 +637,263 @@ __global__ void __launch_bounds__(THREADS) norm_rope_dg_kernel(const float *__re
 template <int D>
 __device__ __forceinline__ void copy_rows(const __nv_bfloat16 *src, int64_t s_head, __nv_bfloat16 *dst,
                                           int64_t d_head, int h0, int h1, int lane) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR;
+  constexpr int LPR = D / 8, RPW = 32 / LPR, U = 4;
   const int e0 = (lane % LPR) * 8;
-  for (int h = h0 + lane / LPR; h < h1; h += RPW)
-    *reinterpret_cast<uint4 *>(dst + h * d_head + e0) =
-        *reinterpret_cast<const uint4 *>(src + h * s_head + e0);
-}
-
-// NORM: Q normed, rotated and written to qo, K normed, rotated and written
-// into its page, V copied into its page.  Otherwise K and V copied.
-template <int D, bool NORM>
-__global__ void __launch_bounds__(THREADS) append_kernel(const AppendArgs a, int per) {
-  __shared__ unsigned long long turns[MAX_FREQ];
-  __shared__ float2 table[WARPS][MAX_FREQ];
-  using T = __nv_bfloat16;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  LaneRope lr;
-  float gq[8], gk[8];
-  if constexpr (NORM) {
-    for (int f = threadIdx.x; f < a.rot / 2; f += THREADS)
-      turns[f] = turns_per_position(__ldg(a.inv_freq + f));
-    __syncthreads();
-    lane_rope_setup<D>(lr, lane, a.rot, a.neighbour);
-    load_weight(a.gq, (lane % (D / 8)) * 8, gq);
-    load_weight(a.gk, (lane % (D / 8)) * 8, gk);
-  }
-  const PagedSeqs &s = a.seqs;
-  const int qh = NORM ? a.H : 0;
-  const int heads = qh + 2 * a.Hkv, chunks = (heads + per - 1) / per;
-  const int64_t items = a.tokens * chunks, step = (int64_t)gridDim.x * WARPS;
-  for (int64_t it = blockIdx.x * (int64_t)WARPS + warp; it < items; it += step) {
-    const int t = (int)(it / chunks);
-    const int lo = (int)(it - (int64_t)t * chunks) * per, hi = min(lo + per, heads);
-    // the sequence of token t: the last b with cu[b] <= t
-    int b = 0, e = s.batch;
-    while (e - b > 1) {
-      const int m = (b + e) >> 1;
-      if (__ldg(s.cu + m) <= t)
-        b = m;
-      else
-        e = m;
-    }
-    const int first = __ldg(s.cu + b), end = __ldg(s.cu + b + 1);
-    if (t < first || t >= end) continue;  // a row behind the last sequence
-    const int64_t len = __ldg(s.lens + b), pos = len - end + t;
-    // its place; out of the table's or the pool's range: reported, not written
-    int64_t page = -1;
-    int slot = 0;
-    if (pos >= 0 && pos < ((int64_t)s.max_pages << s.page_shift)) {
-      page = __ldg(s.table + b * s.table_stride + (pos >> s.page_shift));
-      slot = (int)(pos & ((1 << s.page_shift) - 1));
-    }
-    if (page < 0 || page >= s.num_pages) {
-      if (lane == 0) atomicExch(&a.status->reserved[0], 1);
-      page = -1;
-    }
-    int h0, h1;
-    if constexpr (NORM) {
-      lane_rope_token<D>(lr, lane, a.rot, a.neighbour, (int)pos, turns, table[warp]);
-      clip(lo, hi, 0, a.H, h0, h1);
-      fwd_rows<T, D>(static_cast<const T *>(a.q.ptr) + t * a.q.s_tok, a.q.s_head,
-                     static_cast<T *>(a.qo.ptr) + t * a.qo.s_tok, a.qo.s_head, h0, h1, gq, a.eps,
-                     a.neighbour, lr, lane);
-    }
-    if (page < 0) continue;
-    T *kd = static_cast<T *>(a.kc.ptr) + page * a.kc.s_page + slot * a.kc.s_slot;
-    T *vd = static_cast<T *>(a.vc.ptr) + page * a.vc.s_page + slot * a.vc.s_slot;
-    clip(lo, hi, qh, a.Hkv, h0, h1);
-    if constexpr (NORM)
-      fwd_rows<T, D>(static_cast<const T *>(a.k.ptr) + t * a.k.s_tok, a.k.s_head, kd, a.kc.s_head, h0, h1,
-                     gk, a.eps, a.neighbour, lr, lane);
-    else
-      copy_rows<D>(static_cast<const T *>(a.k.ptr) + t * a.k.s_tok, a.k.s_head, kd, a.kc.s_head, h0, h1,
-                   lane);
-    clip(lo, hi, qh + a.Hkv, a.Hkv, h0, h1);
-    copy_rows<D>(static_cast<const T *>(a.v.ptr) + t * a.v.s_tok, a.v.s_head, vd, a.vc.s_head, h0, h1,
-                 lane);
+  for (int h = h0 + lane / LPR; h < h1; h += RPW * U) {
+    uint4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (h + u * RPW < h1) v[u] = *reinterpret_cast<const uint4 *>(src + (h + u * RPW) * s_head + e0);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (h + u * RPW < h1) *reinterpret_cast<uint4 *>(dst + (h + u * RPW) * d_head + e0) = v[u];
   }
 }
 
-// Rows a warp takes at once, and blocks: one warp to a token once the tokens
-// fill the card by themselves, fewer heads to a warp below that.
-struct Split {
-  int per;
-  unsigned grid;
+// The sequence of token t, the last b with cu[b] <= t: 32 places at a time.
+__device__ __forceinline__ int sequence_of(const int *cu, int batch, int t, int lane) {
+  int b = 0, n = batch;  // it lies in [b, b + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32, at = lane * step;
+    const uint32_t below = __ballot_sync(0xffffffffu, at < n && __ldg(cu + b + at) <= t);
+    // cu is nondecreasing: the lanes below form a run from 0 (none: t lies before the first)
+    const int k = below ? 31 - __clz(below) : 0;
+    b += k * step;
+    n = min(step, n - k * step);
+  }
+  return b;
+}
+
+// Where token t goes: its position, and the element offsets of its row in the
+// pools' first head, or ok = 0 with what is out of range reported.
+struct Spot {
+  int64_t pos, k, v;
+  int in, ok;  // in: it belongs to a sequence
 };
-Split split(int64_t tokens, int heads, int rows_per_pass, int max_grid) {
-  int64_t chunks = 1;
-  const int most = (heads + rows_per_pass - 1) / rows_per_pass;
-  const int64_t want = (int64_t)152 * 16;  // warps that keep the memory busy
-  if (tokens < want) {
-    chunks = (want + tokens - 1) / tokens;
-    if (chunks > most) chunks = most;
+__device__ __forceinline__ Spot spot_of(const AppendArgs &a, int t, int lane) {
+  const PagedSeqs &s = a.seqs;
+  Spot sp = {0, 0, 0, 0, 0};
+  const int b = sequence_of(s.cu, s.batch, t, lane);
+  const int first = __ldg(s.cu + b), end = __ldg(s.cu + b + 1), len = __ldg(s.lens + b);
+  if (t < first || t >= end) return sp;  // a row behind the last sequence
+  sp.in = 1;
+  sp.pos = (int64_t)len - end + t;
+  int page = -1;
+  if (sp.pos >= 0 && sp.pos < ((int64_t)s.max_pages << s.page_shift))
+    page = __ldg(s.table + b * s.table_stride + (sp.pos >> s.page_shift));
+  if (page < 0 || page >= s.num_pages) {
+    if (lane == 0) atomicExch(&a.status->reserved[0], 1);
+    return sp;
   }
-  Split s;
-  s.per = (int)((heads + chunks - 1) / chunks);
-  s.per = (s.per + rows_per_pass - 1) / rows_per_pass * rows_per_pass;
-  const int64_t items = tokens * ((heads + s.per - 1) / s.per);
-  const int64_t blocks = (items + WARPS - 1) / WARPS;
-  s.grid = (unsigned)(blocks < max_grid ? blocks : max_grid);
-  return s;
+  const int64_t slot = sp.pos & ((1 << s.page_shift) - 1);
+  sp.k = page * a.kc.s_page + slot * a.kc.s_slot;
+  sp.v = page * a.vc.s_page + slot * a.vc.s_slot;
+  sp.ok = 1;
+  return sp;
 }
 
-template <typename T, int D>
+// Q normed, rotated and written to qo, K normed, rotated and written into its
+// page, V copied into its page.
+template <int D, bool NEIGHBOUR>
+__global__ void __launch_bounds__(THREADS, 4) norm_append_kernel(const AppendArgs a, const Plan pl) {
+  using T = __nv_bfloat16;
+  constexpr int RPW = rows_per_pass<D>(), U = fwd_passes<T>(), B = U * RPW, BYTES = U * pass_bytes<T>();
+  __shared__ unsigned long long turns[MAX_FREQ];
+  __shared__ __align__(16) float2 table[WARPS][MAX_FREQ];
+  __shared__ Weights weights;
+  __shared__ __align__(16) uint8_t ring[WARPS][STAGES][BYTES];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Lane ln = lane_of<D, NEIGHBOUR>(lane, a.rot);
+  Walk ahead, now;
+  walk_to(ahead, pl, (uint32_t)a.tokens, walk_start());
+  now = ahead;
+  int put = 0, got = 0;
+  // of batch w.j: its side (queries, keys, values), and the batches of the side before and up to it
+  auto side_of = [&](const Walk &w, int &from, int &to) {
+    const int side = w.j < pl.bq ? 0 : (w.j < pl.bq + pl.bk ? 1 : 2);
+    from = side == 0 ? 0 : (side == 1 ? pl.bq : pl.bq + pl.bk);
+    to = min(w.j1, side == 0 ? pl.bq : (side == 1 ? pl.bq + pl.bk : pl.batches));
+    return side;
+  };
+  Cursor<T> in, out;
+  in.batches = out.batches = 0;
+  auto fetch = [&]() {
+    if (ahead.t >= 0) {
+      if (in.batches == 0) {
+        int from, to;
+        const int side = side_of(ahead, from, to);
+        const NormRopeSide &x = side == 0 ? a.q : (side == 1 ? a.k : a.v);
+        aim<T, D>(in, x, ahead.t * x.s_tok, side ? a.Hkv : a.H, ahead.j - from, to - ahead.j, U, lane);
+      }
+      --in.batches;
+      fetch_rows<T, D, U>(smem_u32(ring[warp][put]), in, ln, lane);
+      walk_on(ahead, pl, (uint32_t)a.tokens);
+      put = put + 1 == STAGES ? 0 : put + 1;
+    }
+    commit_async();
+  };
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i) fetch();
+  for (int f = threadIdx.x; f < a.rot / 2; f += THREADS) turns[f] = turns_per_position(__ldg(a.inv_freq + f));
+  put_weights<D, NEIGHBOUR>(weights, a.gq, a.gk, a.rot);
+  __syncthreads();
+  Turn turn;
+  Spot sp = {0, 0, 0, 0, 0};
+  int of = -1, side = 0;  // the token of `table` and `sp`, the side of `out` and `turn`
+  while (now.t >= 0) {
+    fetch();
+    if (out.batches == 0) {
+      if (now.t != of) {
+        sp = spot_of(a, now.t, lane);
+        put_angles(lane, a.rot, (int)sp.pos, turns, table[warp]);
+        of = now.t;
+      }
+      int from, to;
+      side = side_of(now, from, to);
+      NormRopeSide y = a.qo;
+      int64_t off = now.t * y.s_tok;
+      if (side) {
+        y.ptr = side == 1 ? a.kc.ptr : a.vc.ptr;
+        y.s_head = side == 1 ? a.kc.s_head : a.vc.s_head;
+        off = side == 1 ? sp.k : sp.v;
+      }
+      aim<T, D>(out, y, off, (side ? sp.ok : sp.in) ? (side ? a.Hkv : a.H) : 0, now.j - from, to - now.j, U, lane);
+      if (side < 2) turn_for<D>(turn, weights, side, ln, table[warp], lane);
+    }
+    --out.batches;
+    wait_async<STAGES - 1>();
+    const uint8_t *slot = ring[warp][got];
+    if (side < 2) {
+      fwd_batch<T, D, NEIGHBOUR, U>(slot, out, a.eps, turn, ln, lane);
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u, out.p += out.pass)
+        if (out.left > u * RPW) {
+          Row<T> r;
+          r.take(slot + u * pass_bytes<T>() + lane * 16);
+          *reinterpret_cast<uint4 *>(out.p + ln.a) = r.a;
+          *reinterpret_cast<uint4 *>(out.p + ln.b) = r.b;
+        }
+      out.left -= U * RPW;
+    }
+    walk_on(now, pl, (uint32_t)a.tokens);
+    got = got + 1 == STAGES ? 0 : got + 1;
+  }
+}
+
+// K and V copied into their pages, a token to a warp.
+template <int D>
+__global__ void __launch_bounds__(THREADS) append_kernel(const AppendArgs a) {
+  using T = __nv_bfloat16;
+  const int lane = threadIdx.x & 31;
+  for (int64_t t = walk_start(); t < a.tokens; t += gridDim.x * WARPS) {
+    const Spot sp = spot_of(a, (int)t, lane);
+    if (!sp.ok) continue;
+    copy_rows<D>(static_cast<const T *>(a.k.ptr) + t * a.k.s_tok, a.k.s_head, static_cast<T *>(a.kc.ptr) + sp.k,
+                 a.kc.s_head, 0, a.Hkv, lane);
+    copy_rows<D>(static_cast<const T *>(a.v.ptr) + t * a.v.s_tok, a.v.s_head, static_cast<T *>(a.vc.ptr) + sp.v,
+                 a.vc.s_head, 0, a.Hkv, lane);
+  }
+}
+
+// Batches a warp takes in a row: all of a token's once the tokens give every
+// SM its warps, fewer below that.
+Plan plan(int64_t tokens, int bq, int bk, int bv) {
+  Plan pl;
+  pl.bq = bq;
+  pl.bk = bk;
+  pl.batches = bq + bk + bv;
+  const int64_t want = (int64_t)SMS * 24;
+  const int64_t runs = tokens >= want ? 1 : min((want + tokens - 1) / tokens, (int64_t)pl.batches);
+  pl.run = (int)((pl.batches + runs - 1) / runs);
+  pl.chunks = (pl.batches + pl.run - 1) / pl.run;
+  return pl;
+}
+unsigned blocks_for(int64_t tokens, const Plan &pl, int per_sm) {
+  return (unsigned)min((tokens * pl.chunks + WARPS - 1) / WARPS, (int64_t)SMS * per_sm);
+}
+int batches_of(int heads, int b) { return (heads + b - 1) / b; }
+
+template <typename T, int D, bool NEIGHBOUR>
 cudaError_t launch_fwd(const NormRopeArgs &a, cudaStream_t st) {
-  const Split s = split(a.tokens, a.H + a.Hkv, 32 / (D / 8), 152 * 8);
-  norm_rope_kernel<T, D><<<s.grid, THREADS, 0, st>>>(a, s.per);
+  constexpr int B = fwd_passes<T>() * rows_per_pass<D>();
+  const Plan pl = plan(a.tokens, batches_of(a.H, B), batches_of(a.Hkv, B), 0);
+  norm_rope_kernel<T, D, NEIGHBOUR><<<blocks_for(a.tokens, pl, 5), THREADS, 0, st>>>(a, pl);
   return cudaGetLastError();
 }
 
-template <typename T, int D>
+template <typename T, int D, bool NEIGHBOUR>
 cudaError_t launch_bwd(const NormRopeBwdArgs &b, cudaStream_t st) {
+  constexpr int B = bwd_passes<T>() * rows_per_pass<D>();
   float *part = static_cast<float *>(b.workspace);
   unsigned blocks = 0;  // no tokens: no sums, dg = 0
   if (b.fwd.tokens > 0) {
-    const Split s = split(b.fwd.tokens, b.fwd.H + b.fwd.Hkv, 32 / (D / 8), kNormRopeBwdMaxGrid);
-    blocks = s.grid;
-    norm_rope_bwd_kernel<T, D><<<blocks, THREADS, 0, st>>>(b, s.per, part);
+    const Plan plq = plan(b.fwd.tokens, batches_of(b.fwd.H, B), 0, 0);
+    const Plan plk = plan(b.fwd.tokens, batches_of(b.fwd.Hkv, B), 0, 0);
+    blocks = blocks_for(b.fwd.tokens, plq, kNormRopeBwdMaxGrid / SMS);
+    norm_rope_bwd_kernel<T, D, NEIGHBOUR><<<blocks, THREADS, 0, st>>>(b, plq, plk, part);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  norm_rope_dg_kernel<<<2 * D / 32, THREADS, 0, st>>>(part, (int)blocks, D, b.dgq, b.dgk);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * D / 32);
+  cfg.blockDim = dim3(THREADS);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = blocks > 0;  // behind this call's own kernel only
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, norm_rope_dg_kernel, (const float *)part, (int)blocks, D, b.dgq, b.dgk);
+}
+
+template <int D>
+cudaError_t launch_app(const AppendArgs &a, cudaStream_t st) {
+  constexpr int B = fwd_passes<__nv_bfloat16>() * rows_per_pass<D>();
+  const int kv = batches_of(a.Hkv, B);
+  const Plan pl = a.norm ? plan(a.tokens, batches_of(a.H, B), kv, kv) : plan(a.tokens, 1, 0, 0);
+  const unsigned blocks = blocks_for(a.tokens, pl, a.norm ? 4 : 16);
+  if (!a.norm)
+    append_kernel<D><<<blocks, THREADS, 0, st>>>(a);
+  else if (a.neighbour)
+    norm_append_kernel<D, true><<<blocks, THREADS, 0, st>>>(a, pl);
+  else
+    norm_append_kernel<D, false><<<blocks, THREADS, 0, st>>>(a, pl);
   return cudaGetLastError();
 }
 
-template <int D, bool NORM>
-cudaError_t launch_app(const AppendArgs &a, cudaStream_t st) {
-  const Split s = split(a.tokens, (NORM ? a.H : 0) + 2 * a.Hkv, 32 / (D / 8), 152 * 8);
-  append_kernel<D, NORM><<<s.grid, THREADS, 0, st>>>(a, s.per);
-  return cudaGetLastError();
+// kernel<type, d, pairs> of the arguments
+template <typename T>
+cudaError_t fwd_of(const NormRopeArgs &a, cudaStream_t st) {
+  if (a.d == 128) return a.neighbour ? launch_fwd<T, 128, true>(a, st) : launch_fwd<T, 128, false>(a, st);
+  return a.neighbour ? launch_fwd<T, 64, true>(a, st) : launch_fwd<T, 64, false>(a, st);
+}
+template <typename T>
+cudaError_t bwd_of(const NormRopeBwdArgs &b, cudaStream_t st) {
+  if (b.fwd.d == 128)
+    return b.fwd.neighbour ? launch_bwd<T, 128, true>(b, st) : launch_bwd<T, 128, false>(b, st);
+  return b.fwd.neighbour ? launch_bwd<T, 64, true>(b, st) : launch_bwd<T, 64, false>(b, st);
 }
 
 }  // namespace
 
 cudaError_t launch_norm_rope(const NormRopeArgs &a, cudaStream_t st) {
   timing_mark(st, 0);
-  cudaError_t e;
-  if (a.f32)
-    e = a.d == 128 ? launch_fwd<float, 128>(a, st) : launch_fwd<float, 64>(a, st);
-  else
-    e = a.d == 128 ? launch_fwd<__nv_bfloat16, 128>(a, st) : launch_fwd<__nv_bfloat16, 64>(a, st);
+  const cudaError_t e = a.f32 ? fwd_of<float>(a, st) : fwd_of<__nv_bfloat16>(a, st);
   timing_mark(st, 1);
   return e;
 }
 
 cudaError_t launch_norm_rope_bwd(const NormRopeBwdArgs &b, cudaStream_t st) {
   timing_mark(st, 0);
-  cudaError_t e;
-  if (b.fwd.f32)
-    e = b.fwd.d == 128 ? launch_bwd<float, 128>(b, st) : launch_bwd<float, 64>(b, st);
-  else
-    e = b.fwd.d == 128 ? launch_bwd<__nv_bfloat16, 128>(b, st) : launch_bwd<__nv_bfloat16, 64>(b, st);
+  const cudaError_t e = b.fwd.f32 ? bwd_of<float>(b, st) : bwd_of<__nv_bfloat16>(b, st);
   timing_mark(st, 1);
   return e;
 }
 
 cudaError_t launch_append(const AppendArgs &a, cudaStream_t st) {
   timing_mark(st, 0);
-  cudaError_t e;
-  if (a.norm)
-    e = a.d == 128 ? launch_app<128, true>(a, st) : launch_app<64, true>(a, st);
-  else
-    e = a.d == 128 ? launch_app<128, false>(a, st) : launch_app<64, false>(a, st);
+  const cudaError_t e = a.d == 128 ? launch_app<128>(a, st) : launch_app<64>(a, st);
   timing_mark(st, 1);
   return e;
 }
