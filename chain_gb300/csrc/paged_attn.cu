@@ -30,14 +30,13 @@
 //   warp 8     TMA producer: Q tiles, then K and V tiles through one ring of
 //              NS tile slots in the order K0 V0 K1 V1 ...; a tile of 128 keys is
 //              128 / page boxes, their pages looked up one tile ahead, one lane a box.
-//   warp 9     MMA issuer.
+//   warp 9     MMA issuer; at d = 64 of stream 0, and warp 11 of stream 1.
 //   warp 10    scheduler: finds the run's units and hands them to the other
 //              warps through a small ring.
 // Two streams share the tensor core, so that one multiplies while the other
 // exponentiates.  With more than TPT tokens the streams are the unit's two
 // query tiles over the same keys; with fewer (single tokens, short chunks) they are
 // its even and odd key tiles for one query tile, joined before the store.
-// Tensor memory: S0/P0 [0,128), S1/P1 [128,256), O0 [256,384), O1 [384,512).
 #include "internal.h"
 
 namespace chain {
@@ -48,7 +47,6 @@ constexpr int CTAS = 152;     // one block on each SM
 constexpr int THREADS = 384;
 constexpr int NU = 4;         // units in flight between the scheduler and the other warps
 constexpr int MAX_BATCH = 8192;
-constexpr int OVERHEAD = 2;   // cost of a unit's start and end, in key tiles
 constexpr uint32_t REGS_SOFTMAX = 184, REGS_CONTROL = 136;  // 256 x 184 + 128 x 136 = 384 x 168
 constexpr float RESCALE_THRESHOLD = 8.0f;                   // log2 units
 
@@ -85,13 +83,25 @@ struct Boundary {
 template <int D>
 struct Layout {
   static constexpr uint32_t TILE = BM * D * 2;  // a Q, K or V tile
-  static constexpr int NS = D == 128 ? 5 : 10;  // 160 KB of K and V in flight
+  static constexpr int NS = D == 128 ? 5 : 8;  // 160 or 128 KB of K and V in flight
+  static constexpr int ISSUERS = D == 128 ? 1 : 2;
+  static_assert(ISSUERS == 1 || NS % 4 == 0, "two issuers: a unit's slot stays with one stream");
+  // Costs, in quarters of a key tile against one query tile: fitted to the blocks' times over
+  // mixed batches (cycles at d = 128 / 64: tile 2,600 / 1,400 with one query tile,
+  // 3,300 / 2,200 with two; a unit's start and end 5,000 to 7,000).
+  static constexpr int COST1 = 4, COST2 = D == 128 ? 5 : 6, OVERHEAD = D == 128 ? 9 : 16;
+  // Tensor memory: S0 [0,128), S1 [128,256).  At d = 64 P has columns of its own, so that a
+  // stream's next S is computed while its softmax still runs; at d = 128 there is no
+  // room, and P overwrites S.
+  static constexpr bool OWN_P = D == 64;
+  static __host__ __device__ constexpr uint32_t p_col(int t) { return OWN_P ? 256 + 64 * t : BN * t; }
+  static __host__ __device__ constexpr uint32_t o_col(int t) { return OWN_P ? 384 + 64 * t : 256 + 128 * t; }
   static constexpr uint32_t OFF_Q = 0;
   static constexpr uint32_t OFF_RING = 2 * TILE;
   static constexpr uint32_t OFF_BAR = OFF_RING + NS * TILE;
   // q_full[2], q_empty[2], full[NS], empty[NS], s_full[2], p_ready[2],
-  // pv_done[2], u_full[NU], u_empty[NU], joined[2], drain
-  static constexpr uint32_t NBAR = 4 + 2 * NS + 6 + 2 * NU + 2 + 1;
+  // pv_done[2], s_free[2], u_full[NU], u_empty[NU], joined[2], drain[2]
+  static constexpr uint32_t NBAR = 4 + 2 * NS + 8 + 2 * NU + 2 + 2;
   static constexpr uint32_t OFF_UNITS = (OFF_BAR + NBAR * 8 + 15) & ~15u;
   static constexpr uint32_t OFF_ML = OFF_UNITS + NU * 48;
   static constexpr uint32_t OFF_MISC = OFF_ML + BM * 8;
@@ -104,6 +114,7 @@ struct Layout {
 struct Params {
   PagedSeqs s;
   int total, G, Hkv, tpt, causal;
+  int cost1, cost2, overhead;  // of a key tile against one and two query tiles, of a unit
   float scale_log2;
   __nv_bfloat16 *O;
   int64_t o_stok, o_shead;
@@ -186,16 +197,15 @@ __device__ __forceinline__ int units_of(const Params &p, const Seq &s) {
   return (s.n + 2 * p.tpt - 1) / (2 * p.tpt);
 }
 
-// Cost of a unit: its key tiles, a tile of two query tiles counting twice (it
-// has twice the products and exponentials), and OVERHEAD for its start and end.
-__device__ __forceinline__ int tile_cost(const Params &p, int ntok) { return ntok > p.tpt ? 2 : 1; }
+// Cost of a unit: its key tiles, and `overhead` for its start and end.
+__device__ __forceinline__ int tile_cost(const Params &p, int ntok) { return ntok > p.tpt ? p.cost2 : p.cost1; }
 __device__ __forceinline__ long long unit_cost(const Params &p, const Seq &s, int q) {
   const int i0 = q * 2 * p.tpt;
-  return OVERHEAD + (long long)tile_cost(p, s.n - i0) * tiles_to(p, s, i0 + 2 * p.tpt);
+  return p.overhead + (long long)tile_cost(p, s.n - i0) * tiles_to(p, s, i0 + 2 * p.tpt);
 }
 // Key tile at a cost offset into a unit.
-__device__ __forceinline__ int tile_at(long long off, int w) {
-  return off <= OVERHEAD ? 0 : (int)((off - OVERHEAD) / w);
+__device__ __forceinline__ int tile_at(const Params &p, long long off, int w) {
+  return off <= p.overhead ? 0 : (int)((off - p.overhead) / w);
 }
 
 // Cost of one K/V head of the sequence
@@ -278,12 +288,14 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t *s_full = empty + NS;                                       // [2]
   uint64_t *p_ready = s_full + 2;                                      // [2]
   uint64_t *pv_done = p_ready + 2;                                     // [2]
-  uint64_t *u_full = pv_done + 2;                                      // [NU]
+  uint64_t *s_free = pv_done + 2;                                      // [2]
+  uint64_t *u_full = s_free + 2;                                       // [NU]
   uint64_t *u_empty = u_full + NU;                                     // [NU]
   uint64_t *joined = u_empty + NU;                                     // [2]: stream 1's (m, l); O1 read
-  uint64_t *mma_drain = joined + 2;
+  uint64_t *mma_drain = joined + 2;                                    // [2]
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::OFF_MISC);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_MISC + 4);
+  volatile int *has_work = reinterpret_cast<volatile int *>(smem + L::OFF_MISC + 8);
   float2 *ml = reinterpret_cast<float2 *>(smem + L::OFF_ML);
   long long *sums = reinterpret_cast<long long *>(smem + L::OFF_RING);
 
@@ -291,21 +303,22 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
       mbar_init(&q_full[t], 1);
-      mbar_init(&q_empty[t], 1);
+      mbar_init(&q_empty[t], L::ISSUERS);
+      mbar_init(&mma_drain[t], 1);
       mbar_init(&s_full[t], 1);
       mbar_init(&p_ready[t], 128);
       mbar_init(&pv_done[t], 1);
+      mbar_init(&s_free[t], 128);
       mbar_init(&joined[t], 128);
     }
     for (int s = 0; s < NS; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], L::ISSUERS);
     }
     for (int s = 0; s < NU; ++s) {
       mbar_init(&u_full[s], 1);
-      mbar_init(&u_empty[s], 2 + 8);  // producer, MMA warp, eight softmax warps
+      mbar_init(&u_empty[s], 1 + L::ISSUERS + 8);  // producer, MMA warps, eight softmax warps
     }
-    mbar_init(mma_drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -327,6 +340,46 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t tmem = *tmem_slot;
   pdl_launch_dependents();  // the join may be launched; it waits for this grid
 
+  // The scheduler warp finds where the block's run begins.
+  long long t = 0, t1 = 0;  // the run
+  Place at = {0, 0, 0, 0};
+  Seq s = {0, 0, 0};
+  if (warp == 10) {
+    long long total = 0;
+    for (int b = lane; b < p.s.batch; b += 32) total += sums[b];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    total *= p.Hkv;
+    t = run_start(total, blockIdx.x);
+    t1 = run_start(total, blockIdx.x + 1);
+    Boundary bd = {0, total, 0, 1, 0, 0, 0, 0};
+    int work = 0;
+    if (t < total) {
+      at = locate(p, sums, t, lane);
+      s = seq_of(p, at.b, false);
+      const int i0 = at.q * 2 * p.tpt;
+      bd.u0 = t - at.off;
+      bd.nt = tiles_to(p, s, i0 + 2 * p.tpt);
+      bd.w = tile_cost(p, s.n - i0);
+      bd.cut = tile_at(p, at.off, bd.w) > 0;
+      bd.tok0 = s.lo + i0;
+      bd.ntok = min(s.n - i0, 2 * p.tpt);
+      bd.head = at.head;
+      // a run that ends before the first key tile that it reaches has nothing to do
+      const long long end = at.off + (t1 - t), cost = p.overhead + (long long)bd.w * bd.nt;
+      work = t < t1 && (end >= cost || tile_at(p, end, bd.w) > tile_at(p, at.off, bd.w));
+    }
+    if (lane == 0) {
+      p.bounds[blockIdx.x] = bd;
+      *has_work = work;
+    }
+  }
+  __syncthreads();
+  if (!*has_work) {
+    if (warp == 9) tmem_dealloc(tmem, 512);
+    return;
+  }
+
   // Every lane waits, and the warp goes on or gives up as one: what follows
   // holds warp-wide instructions.
   auto warp_wait = [&](uint64_t *bar, uint32_t parity, int site) -> bool {
@@ -340,34 +393,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     u = *reinterpret_cast<const Unit *>(smem + L::OFF_UNITS + s * 48);
     __syncwarp();
     if (lane == 0) mbar_arrive(&u_empty[s]);
+    __syncwarp();  // what follows elects a lane or reads tensor memory
     ++k;
     return u.head >= 0;
   };
 
   auto role_scheduler = [&]() {
-    long long total = 0;
-    for (int b = lane; b < p.s.batch; b += 32) total += sums[b];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    total *= p.Hkv;
-    long long t = run_start(total, blockIdx.x);
-    const long long t1 = run_start(total, blockIdx.x + 1);
-    Boundary bd = {0, total, 0, 1, 0, 0, 0, 0};
-    Place at = {0, 0, 0, 0};
-    Seq s = {0, 0, 0};
-    if (t < total) {
-      at = locate(p, sums, t, lane);
-      s = seq_of(p, at.b, false);
-      const int i0 = at.q * 2 * p.tpt;
-      bd.u0 = t - at.off;
-      bd.nt = tiles_to(p, s, i0 + 2 * p.tpt);
-      bd.w = tile_cost(p, s.n - i0);
-      bd.cut = tile_at(at.off, bd.w) > 0;
-      bd.tok0 = s.lo + i0;
-      bd.ntok = min(s.n - i0, 2 * p.tpt);
-      bd.head = at.head;
-    }
-    if (lane == 0) p.bounds[blockIdx.x] = bd;
     int k = 0;
     bool ok = true;
     while (true) {
@@ -376,9 +407,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (t < t1) {
         const int i0 = at.q * 2 * p.tpt, nt = tiles_to(p, s, i0 + 2 * p.tpt);
         const int w = tile_cost(p, s.n - i0);
-        const long long cost = OVERHEAD + (long long)w * nt, end = at.off + (t1 - t);
-        u.j0 = tile_at(at.off, w);
-        u.j1 = end >= cost ? nt : tile_at(end, w);
+        const long long cost = p.overhead + (long long)w * nt, end = at.off + (t1 - t);
+        u.j0 = tile_at(p, at.off, w);
+        u.j1 = end >= cost ? nt : tile_at(p, end, w);
         if (u.j1 > u.j0) {  // else the run ends before the unit's first key tile
           u.tok0 = s.lo + i0;
           u.ntok = min(s.n - i0, 2 * p.tpt);
@@ -494,7 +525,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncwarp();
   };
 
-  auto role_mma = [&]() {
+  // Issues the products of streams [first, end).  At d = 128 one warp issues both streams', whose
+  // order keeps them half a step apart: one multiplies while the other exponentiates.  (An
+  // issuer for each let them fall into step, and single tokens took 389 us that take 336.)  At
+  // d = 64, where S does not wait for P V and the products are half as long, the issuer's own
+  // waits, some 200 cycles each, bounded the step, and each stream has an issuer (a chunk
+  // over 32768 positions 681 us with one issuer and shared columns, 551 with two and P's own).
+  auto role_mma = [&](const int first, const int end) {
     const uint32_t idS = idesc_bf16_f32(BM, BN, 0, 0), idO = idesc_bf16_f32(BM, D, 0, 1);
     const SDesc dQ = sdesc_make(smem_u32(smem + L::OFF_Q), 16, 1024);
     const SDesc dK = sdesc_make(smem_u32(smem + L::OFF_RING), 16, 1024);
@@ -502,93 +539,120 @@ __global__ void __launch_bounds__(THREADS, 1)
     Unit u;
     int k = 0;
     uint32_t q_uses[2] = {0, 0}, qsel = 0;
-    uint32_t base = 0;            // ring number of the unit's first K tile
-    uint32_t steps[2] = {0, 0};   // P V products of each stream so far
+    uint32_t base = 0;             // ring number of the unit's first K tile
+    uint32_t steps[2] = {0, 0};    // P V products of each stream so far
+    uint32_t s_count[2] = {0, 0};  // S products of each stream so far
     bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+      return mbar_wait_warp(bar, parity, p.wc, abort_flag, SITE_PAGED_MMA);
+    };
     while (ok && next_unit(k, u, SITE_PAGED_MMA)) {
       const bool two = u.ntok > p.tpt;
       const int n = u.j1 - u.j0;
       int ns[2];
       ns[0] = two ? max(0, min(u.ja, u.j1) - u.j0) : (n + 1) / 2;
       ns[1] = two ? n : n / 2;
-      const int buf0 = two ? 0 : (int)qsel;
-      ok = mbar_wait_warp(&q_full[buf0], q_uses[buf0] & 1, p.wc, abort_flag, SITE_PAGED_MMA);
-      ++q_uses[buf0];
-      if (two) {
-        ok = ok && mbar_wait_warp(&q_full[1], q_uses[1] & 1, p.wc, abort_flag, SITE_PAGED_MMA);
-        ++q_uses[1];
-        if (ok && ns[0] == 0 && elect_one()) umma_commit(&q_empty[0]);
+      const int single = (int)qsel;  // the Q tile of a unit that has one
+      for (int b = 0; b < 2; ++b)
+        if (two ? b >= first && b < end : b == single) ok = ok && wait(&q_full[b], q_uses[b] & 1);
+      for (int b = 0; b < 2; ++b) q_uses[b] += two || b == single;
+      if (!two) qsel ^= 1;
+      // Frees a buffer.  With one issuer the last product that reads it does; with two, one
+      // arrival comes from each stream that reads it, both from a stream that reads it alone.
+      auto release = [&](uint64_t *bar, bool alone) {
+        umma_commit(bar);
+        if (L::ISSUERS == 2 && alone) umma_commit(bar);
+      };
+      // does stream t's step i read its K and V tiles alone, or (one issuer) last
+      auto last_reader = [&](int t, int i) {
+        return !two || (t == 1 && (L::ISSUERS == 1 || i >= ns[0]));
+      };
+      for (int t = first; t < end; ++t) {
+        if (ok && ns[t] == 0 && (two || L::ISSUERS == 2) && elect_one()) release(&q_empty[two ? t : single], two);
         __syncwarp();
-      } else {
-        qsel ^= 1;
       }
+      auto k_seq = [&](int t, int i) { return base + 2 * (two ? i : 2 * i + t); };
+      // Waits for a ring slot's tile.  Two issuers wait on the slots out of ring order, and a
+      // parity says only whether the phase before the last is over: at a slot's first use by the unit, that
+      // its previous tile has been freed is waited for too.  (Within a unit a slot goes to the same
+      // stream each time, or both wait on all of them.)
+      auto tile_wait = [&](uint32_t seq) {
+        const uint32_t st = seq % NS, turn = seq / NS;
+        if (L::ISSUERS == 2 && turn > 0 && seq - base < NS && !wait(&empty[st], (turn - 1) & 1)) return false;
+        return wait(&full[st], turn & 1);
+      };
       // S_t of step i into columns [128 t, 128 t + 128)
       auto issue_s = [&](int t, int i) -> bool {
-        const int x = two ? i : 2 * i + t;
-        const uint32_t seq = base + 2 * x, st = seq % NS;
-        if (!mbar_wait_warp(&full[st], (seq / NS) & 1, p.wc, abort_flag, SITE_PAGED_MMA)) return false;
+        const uint32_t seq = k_seq(t, i), st = seq % NS;
+        if (!tile_wait(seq)) return false;
+        // where P has its own columns, S may come as soon as the one before it has been read; where it
+        // has not, the P V product before it in the issue order has read them last
+        if (L::OWN_P && s_count[t] > 0 && !wait(&s_free[t], (s_count[t] - 1) & 1)) return false;
+        ++s_count[t];
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t qo = (uint32_t)(two ? t : buf0) * L::TILE, ko = st * L::TILE;
+          const uint32_t qo = (uint32_t)(two ? t : single) * L::TILE, ko = st * L::TILE;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = (kk >> 2) * (BM * 128) + (kk & 3) * 32;
             umma_f16_ss(tmem + t * BN, sdesc_at(dQ, qo + off), sdesc_at(dK, ko + off), idS, kk > 0);
           }
           umma_commit(&s_full[t]);
-          if (!two || t == 1) umma_commit(&empty[st]);
-          if (two ? i == ns[t] - 1 : x == n - 1) umma_commit(&q_empty[two ? t : buf0]);
+          if (L::ISSUERS == 2 || last_reader(t, i)) release(&empty[st], last_reader(t, i));
+          if (two || L::ISSUERS == 2 ? i == ns[t] - 1 : 2 * i + t == n - 1)
+            release(&q_empty[two ? t : single], two);
         }
         __syncwarp();
         return true;
       };
-      for (int t = 0; ok && t < 2; ++t)
-        if (ns[t] > 0) ok = issue_s(t, 0);
-      const int most = max(ns[0], ns[1]);
-      for (int i = 0; ok && i < most; ++i) {
-        for (int t = 0; ok && t < 2; ++t) {
-          if (i >= ns[t]) continue;
-          const int x = two ? i : 2 * i + t;
-          const uint32_t seq = base + 2 * x + 1, st = seq % NS;
-          ok = mbar_wait_warp(&full[st], (seq / NS) & 1, p.wc, abort_flag, SITE_PAGED_MMA);
-          if (!ok) break;
-          // The last page may hold anything behind the sequence's end, and 0 times a
-          // NaN is not 0: those rows of V become zeros.
-          const int valid = u.len - (u.j0 + x) * BN;
-          if (valid > 0 && valid < BN && (!two || t == 0 || i >= ns[0])) {
-            const int page = 1 << p.s.page_shift;
-            const int end = min(BN, (valid + page - 1) & ~(page - 1));
-            for (int c = lane; c < (end - valid) * (D / 8); c += 32) {
-              const int r = valid + c / (D / 8), q = c % (D / 8);
-              st_shared_v4(smem_u32(smem + L::OFF_RING + st * L::TILE + (q >> 3) * (BN * 128) + r * 128 + (q & 7) * 16),
-                           0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
+      // O_t += P_t V of step i
+      auto issue_pv = [&](int t, int i) -> bool {
+        const uint32_t seq = k_seq(t, i) + 1, st = seq % NS;
+        if (!tile_wait(seq)) return false;
+        // The last page may hold anything behind the sequence's end, and 0 times a NaN
+        // is not 0: those rows of V become zeros (twice, where two issuers' streams read them).
+        const int valid = u.len - (u.j0 + (two ? i : 2 * i + t)) * BN;
+        if (valid > 0 && valid < BN) {
+          const int page = 1 << p.s.page_shift;
+          const int upto = min(BN, (valid + page - 1) & ~(page - 1));
+          for (int c = lane; c < (upto - valid) * (D / 8); c += 32) {
+            const int r = valid + c / (D / 8), q = c % (D / 8);
+            st_shared_v4(smem_u32(smem + L::OFF_RING + st * L::TILE + (q >> 3) * (BN * 128) + r * 128 + (q & 7) * 16),
+                         0, 0, 0, 0);
           }
-          ok = mbar_wait_warp(&p_ready[t], steps[t] & 1, p.wc, abort_flag, SITE_PAGED_MMA);
-          if (!ok) break;
-          ++steps[t];
-          tc_fence_after();
-          if (elect_one()) {
-            const uint32_t vo = st * L::TILE;
-#pragma unroll
-            for (int kk = 0; kk < BN / 16; ++kk)
-              umma_f16_ts(tmem + 256 + t * 128, tmem + t * BN + kk * 8, sdesc_at(dV, vo + kk * 2048), idO,
-                          i > 0 || kk > 0);
-            umma_commit(&pv_done[t]);
-            if (!two || t == 1) umma_commit(&empty[st]);
-          }
+          fence_proxy_async_smem();
           __syncwarp();
-          if (i + 1 < ns[t]) ok = issue_s(t, i + 1);
         }
-      }
+        if (!wait(&p_ready[t], steps[t] & 1)) return false;
+        ++steps[t];
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t vo = st * L::TILE;
+#pragma unroll
+          for (int kk = 0; kk < BN / 16; ++kk)
+            umma_f16_ts(tmem + L::o_col(t), tmem + L::p_col(t) + kk * 8, sdesc_at(dV, vo + kk * 2048), idO,
+                        i > 0 || kk > 0);
+          umma_commit(&pv_done[t]);
+          if (L::ISSUERS == 2 || last_reader(t, i)) release(&empty[st], last_reader(t, i));
+        }
+        __syncwarp();
+        return true;
+      };
+      for (int t = first; ok && t < end; ++t)
+        if (ns[t] > 0) ok = issue_s(t, 0);
+      for (int i = 0; ok && i < max(ns[0], ns[1]); ++i)
+        for (int t = first; ok && t < end; ++t) {
+          if (L::OWN_P && i + 1 < ns[t]) ok = issue_s(t, i + 1);
+          if (ok && i < ns[t]) ok = issue_pv(t, i);
+          if (!L::OWN_P && ok && i + 1 < ns[t]) ok = issue_s(t, i + 1);
+        }
       base += 2 * n;
     }
     // no MMA may still be running when tensor memory is released
-    if (elect_one()) umma_commit(mma_drain);
     __syncwarp();
-    if (lane == 0) drain_wait(mma_drain, 0, p.wc);
+    if (elect_one()) umma_commit(&mma_drain[first]);
+    __syncwarp();
+    if (lane == 0) drain_wait(&mma_drain[first], 0, p.wc);
     __syncwarp();
   };
 
@@ -596,7 +660,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int t = warp >> 2;
     const int row = threadIdx.x & 127;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lane_off + t * BN;
+    const uint32_t tS = tmem + lane_off + t * BN, tP = tmem + lane_off + L::p_col(t);
     const int rtok = row / p.G, rhead = row - rtok * p.G;  // token of the tile, head of the group
     Unit u;
     int k = 0;
@@ -624,11 +688,16 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int c = 0; c < BN / 32; ++c)
             tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[c * 32]));
           tmem_wait_ld();
+          if (L::OWN_P) {
+            tc_fence_before();
+            mbar_arrive(&s_free[t]);
+          }
           if (kv0 + BN > lim) {
 #pragma unroll
             for (int e = 0; e < BN; ++e)
               if (kv0 + e >= lim) s[e] = __float_as_uint(-INFINITY);
           }
+          __syncwarp();
           float mx4[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -649,6 +718,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             rescale = true;
           }
           const float mref = m == -INFINITY ? 0.0f : m;
+          if (L::OWN_P && i > 0) {  // the product before this one has read P, and O holds it
+            ok = warp_wait(&pv_done[t], (steps[t] + i - 1) & 1, SITE_PAGED_SOFTMAX);
+            if (!ok) break;
+            tc_fence_after();
+          }
           // P = 2^(s scale log2e - m): keys [32 g, 32 g + 32) to columns [16 g, 16 g + 16)
           const uint64_t sc2 = f32x2(p.scale_log2, p.scale_log2), nm2 = f32x2(-mref, -mref);
           uint64_t rs2[4] = {0, 0, 0, 0};
@@ -665,7 +739,7 @@ __global__ void __launch_bounds__(THREADS, 1)
               rs2[(e >> 1) & 3] = add_f32x2(rs2[(e >> 1) & 3], f32x2(p0, p1));
               pk[e >> 1] = pack_bf16(p0, p1);
             }
-            tmem_st16(tS + g * 16, pk);
+            tmem_st16(tP + g * 16, pk);
           }
           float rs = 0.0f;
 #pragma unroll
@@ -674,9 +748,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             f32x2_split(rs2[e], a0, a1);
             rs += a0 + a1;
           }
-          // S of this step was issued after the previous step's P V: O holds every earlier key
+          // the previous step's P V is done: O holds every earlier key
           if (__any_sync(0xffffffffu, rescale)) {
-            const uint32_t tO = tmem + lane_off + 256 + t * 128;
+            const uint32_t tO = tmem + lane_off + L::o_col(t);
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               uint32_t o[32];
@@ -689,6 +763,12 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           l = l * alpha + rs;
           tmem_wait_st();
+        } else if (L::OWN_P) {
+          // a warp without rows keeps step too: S of step i + 1 does not wait for P of step i, and an
+          // arrival of step i + 1 must not count for step i
+          mbar_arrive(&s_free[t]);
+          if (i > 0) ok = warp_wait(&pv_done[t], (steps[t] + i - 1) & 1, SITE_PAGED_SOFTMAX);
+          if (!ok) break;
         }
         tc_fence_before();
         mbar_arrive(&p_ready[t]);
@@ -747,7 +827,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
             if (!has[y]) continue;
-            tmem_ld32(tmem + lane_off + 256 + y * 128 + c * 32, x);
+            tmem_ld32(tmem + lane_off + L::o_col(y) + c * 32, x);
             tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(x[e]), w[y], o[e]);
@@ -781,14 +861,16 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   };
 
-  if (warp >= 8) {  // warp 11 only hands its registers over
+  if (warp >= 8) {  // with one issuer warp 11 only hands its registers over
     setmaxnreg_dec<REGS_CONTROL>();
     if (warp == 8)
       role_producer();
-    else if (warp == 9)
-      role_mma();
     else if (warp == 10)
       role_scheduler();
+    else if (L::ISSUERS == 2)
+      role_mma(warp == 9 ? 0 : 1, warp == 9 ? 1 : 2);
+    else if (warp == 9)
+      role_mma(0, 2);
   } else {
     setmaxnreg_inc<REGS_SOFTMAX>();
     role_softmax();
@@ -815,7 +897,7 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const Params p) {
   const Boundary bd = p.bounds[c];
   const int tiles = bd.ntok > p.tpt ? 2 : 1;  // rows are numbered as in the unit's query tiles
   if (!bd.cut || (int)blockIdx.y >= tiles * BM / 32) return;
-  if (tile_at(run_start(bd.total, c - 1) - bd.u0, bd.w) > 0) return;
+  if (tile_at(p, run_start(bd.total, c - 1) - bd.u0, bd.w) > 0) return;
   const int r = blockIdx.y * 32 + lane;
   const int rt = (r % BM) / p.G, tok = (r / BM) * p.tpt + rt;
   const bool valid = rt < p.tpt && tok < bd.ntok;
@@ -833,7 +915,7 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const Params p) {
 #pragma unroll
     for (int i = 0; i < PB; ++i) {
       const int k = k0 + i;
-      const int j1 = k + 1 < CTAS ? min(bd.nt, tile_at(run_start(bd.total, k + 1) - bd.u0, bd.w)) : bd.nt;
+      const int j1 = k + 1 < CTAS ? min(bd.nt, tile_at(p, run_start(bd.total, k + 1) - bd.u0, bd.w)) : bd.nt;
       x[i] = make_float2(-INFINITY, 0.0f);
 #pragma unroll
       for (int q = 0; q < Q; ++q) v[i][q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -906,6 +988,9 @@ cudaError_t launch(const PagedAttnArgs &a, const WaitCfg &wc, cudaStream_t st) {
   p.Hkv = a.Hkv;
   p.tpt = BM / p.G;
   p.causal = a.causal;
+  p.cost1 = L::COST1;
+  p.cost2 = L::COST2;
+  p.overhead = L::OVERHEAD;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.O = static_cast<__nv_bfloat16 *>(a.O);
   p.o_stok = a.o_stok;

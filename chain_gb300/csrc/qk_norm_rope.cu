@@ -614,21 +614,23 @@ __global__ void __launch_bounds__(THREADS, 4) norm_rope_bwd_kernel(const NormRop
 }
 
 // dgq, dgk [D] from the blocks' sums: one block for 32 of the 2 D columns,
-// warp w adding the blocks w, w + 8, ...
-__global__ void __launch_bounds__(THREADS) norm_rope_dg_kernel(const float *__restrict__ part, int blocks,
-                                                               int d, float *__restrict__ dgq,
-                                                               float *__restrict__ dgk) {
-  __shared__ float sums[WARPS][32];
+// warp w adding the blocks w, w + 32, ...  (With four warps its 150 dependent loads
+// took longer than the gradients of a short batch.)
+constexpr int DG_WARPS = 32;
+__global__ void __launch_bounds__(32 * DG_WARPS) norm_rope_dg_kernel(const float *__restrict__ part, int blocks,
+                                                                     int d, float *__restrict__ dgq,
+                                                                     float *__restrict__ dgk) {
+  __shared__ float sums[DG_WARPS][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
   float s = 0.0f;
   pdl_wait();
 #pragma unroll 8
-  for (int i = warp; i < blocks; i += WARPS) s += part[(int64_t)i * 2 * d + col];
+  for (int i = warp; i < blocks; i += DG_WARPS) s += part[(int64_t)i * 2 * d + col];
   sums[warp][lane] = s;
   __syncthreads();
   if (warp == 0) {
 #pragma unroll
-    for (int w = 1; w < WARPS; ++w) s += sums[w][lane];
+    for (int w = 1; w < DG_WARPS; ++w) s += sums[w][lane];
     (col < d ? dgq : dgk - d)[col] = s;
   }
 }
@@ -837,7 +839,7 @@ cudaError_t launch_bwd(const NormRopeBwdArgs &b, cudaStream_t st) {
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * D / 32);
-  cfg.blockDim = dim3(THREADS);
+  cfg.blockDim = dim3(32 * DG_WARPS);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
