@@ -83,7 +83,7 @@ struct Boundary {
 template <int D>
 struct Layout {
   static constexpr uint32_t TILE = BM * D * 2;  // a Q, K or V tile
-  static constexpr int NS = D == 128 ? 5 : 8;  // 160 or 128 KB of K and V in flight
+  static constexpr int NS = D == 128 ? 5 : 12;  // 160 or 192 KB of K and V in flight
   static constexpr int ISSUERS = D == 128 ? 1 : 2;
   static_assert(ISSUERS == 1 || NS % 4 == 0, "two issuers: a unit's slot stays with one stream");
   // Costs, in quarters of a key tile against one query tile: fitted to the blocks' times over
@@ -546,6 +546,19 @@ __global__ void __launch_bounds__(THREADS, 1)
     auto wait = [&](uint64_t *bar, uint32_t parity) {
       return mbar_wait_warp(bar, parity, p.wc, abort_flag, SITE_PAGED_MMA);
     };
+    // Two barriers in one go, and whether a third is there already: lane 0 polls, as in
+    // mbar_wait_warp, and one exchange tells the others.  Returns bit 0: both over, bit 1: the third.
+    auto wait_pair = [&](uint64_t *b0, uint32_t p0, uint64_t *b1, uint32_t p1, uint64_t *b2, uint32_t p2) -> int {
+      int r = 0;
+      if (lane == 0) {
+        const uint32_t a0 = smem_u32(b0), a1 = smem_u32(b1);
+        const bool r0 = mbar_try_wait(a0, p0), r1 = mbar_try_wait(a1, p1);
+        r = (r0 || mbar_wait(b0, p0, p.wc, abort_flag, SITE_PAGED_MMA)) &&
+            (r1 || mbar_wait(b1, p1, p.wc, abort_flag, SITE_PAGED_MMA));
+        if (r && b2 && mbar_try_wait(smem_u32(b2), p2)) r |= 2;
+      }
+      return __shfl_sync(0xffffffffu, r, 0);
+    };
     while (ok && next_unit(k, u, SITE_PAGED_MMA)) {
       const bool two = u.ntok > p.tpt;
       const int n = u.j1 - u.j0;
@@ -572,45 +585,56 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
       }
       auto k_seq = [&](int t, int i) { return base + 2 * (two ? i : 2 * i + t); };
-      // Waits for a ring slot's tile.  Two issuers wait on the slots out of ring order, and a
-      // parity says only whether the phase before the last is over: at a slot's first use by the unit, that
-      // its previous tile has been freed is waited for too.  (Within a unit a slot goes to the same
-      // stream each time, or both wait on all of them.)
-      auto tile_wait = [&](uint32_t seq) {
-        const uint32_t st = seq % NS, turn = seq / NS;
-        if (L::ISSUERS == 2 && turn > 0 && seq - base < NS && !wait(&empty[st], (turn - 1) & 1)) return false;
-        return wait(&full[st], turn & 1);
+      // Two issuers wait on the ring's slots out of ring order, and a parity says only whether
+      // the phase before the last is over: at a slot's first use by the unit, that its previous
+      // tile has been freed is waited for first.  (Within a unit a slot goes to the same stream
+      // each time, or both wait on all of them.)
+      auto fresh = [&](uint32_t seq) {
+        const uint32_t turn = seq / NS;
+        if (L::ISSUERS == 2 && turn > 0 && seq - base < NS) return wait(&empty[seq % NS], (turn - 1) & 1);
+        return true;
       };
-      // S_t of step i into columns [128 t, 128 t + 128)
+      // S of step i into columns [128 t, 128 t + 128), by the elected lane
+      auto put_s = [&](int t, int i) {
+        const uint32_t st = k_seq(t, i) % NS, qo = (uint32_t)(two ? t : single) * L::TILE, ko = st * L::TILE;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * (BM * 128) + (kk & 3) * 32;
+          umma_f16_ss(tmem + t * BN, sdesc_at(dQ, qo + off), sdesc_at(dK, ko + off), idS, kk > 0);
+        }
+        umma_commit(&s_full[t]);
+        if (L::ISSUERS == 2 || last_reader(t, i)) release(&empty[st], last_reader(t, i));
+        if (two || L::ISSUERS == 2 ? i == ns[t] - 1 : 2 * i + t == n - 1)
+          release(&q_empty[two ? t : single], two);
+      };
       auto issue_s = [&](int t, int i) -> bool {
-        const uint32_t seq = k_seq(t, i), st = seq % NS;
-        if (!tile_wait(seq)) return false;
+        const uint32_t seq = k_seq(t, i), st = seq % NS, turn = seq / NS;
+        if (!fresh(seq)) return false;
         // where P has its own columns, S may come as soon as the one before it has been read; where it
         // has not, the P V product before it in the issue order has read them last
-        if (L::OWN_P && s_count[t] > 0 && !wait(&s_free[t], (s_count[t] - 1) & 1)) return false;
+        if (L::OWN_P && s_count[t] > 0) {
+          if (!wait_pair(&full[st], turn & 1, &s_free[t], (s_count[t] - 1) & 1, nullptr, 0)) return false;
+        } else if (!wait(&full[st], turn & 1)) {
+          return false;
+        }
         ++s_count[t];
         tc_fence_after();
-        if (elect_one()) {
-          const uint32_t qo = (uint32_t)(two ? t : single) * L::TILE, ko = st * L::TILE;
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * (BM * 128) + (kk & 3) * 32;
-            umma_f16_ss(tmem + t * BN, sdesc_at(dQ, qo + off), sdesc_at(dK, ko + off), idS, kk > 0);
-          }
-          umma_commit(&s_full[t]);
-          if (L::ISSUERS == 2 || last_reader(t, i)) release(&empty[st], last_reader(t, i));
-          if (two || L::ISSUERS == 2 ? i == ns[t] - 1 : 2 * i + t == n - 1)
-            release(&q_empty[two ? t : single], two);
-        }
+        if (elect_one()) put_s(t, i);
         __syncwarp();
         return true;
       };
-      // O_t += P_t V of step i
+      // O_t += P_t V of step i; where P shares S's columns, with S of the stream's next step right
+      // behind it if its K tile is there
       auto issue_pv = [&](int t, int i) -> bool {
         const uint32_t seq = k_seq(t, i) + 1, st = seq % NS;
-        if (!tile_wait(seq)) return false;
+        const bool next_s = !L::OWN_P && i + 1 < ns[t];
+        const uint32_t nseq = k_seq(t, i + 1);
+        if (!fresh(seq)) return false;
+        const int got = wait_pair(&full[st], (seq / NS) & 1, &p_ready[t], steps[t] & 1,
+                                  next_s ? &full[nseq % NS] : nullptr, (nseq / NS) & 1);
+        if (!(got & 1)) return false;
         // The last page may hold anything behind the sequence's end, and 0 times a NaN
-        // is not 0: those rows of V become zeros (twice, where two issuers' streams read them).
+        // is not 0: those rows of V become zeros (twice, where both streams read them).
         const int valid = u.len - (u.j0 + (two ? i : 2 * i + t)) * BN;
         if (valid > 0 && valid < BN) {
           const int page = 1 << p.s.page_shift;
@@ -623,7 +647,6 @@ __global__ void __launch_bounds__(THREADS, 1)
           fence_proxy_async_smem();
           __syncwarp();
         }
-        if (!wait(&p_ready[t], steps[t] & 1)) return false;
         ++steps[t];
         tc_fence_after();
         if (elect_one()) {
@@ -634,9 +657,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                         i > 0 || kk > 0);
           umma_commit(&pv_done[t]);
           if (L::ISSUERS == 2 || last_reader(t, i)) release(&empty[st], last_reader(t, i));
+          if (got & 2) put_s(t, i + 1);
         }
         __syncwarp();
-        return true;
+        return !next_s || (got & 2) || issue_s(t, i + 1);
       };
       for (int t = first; ok && t < end; ++t)
         if (ns[t] > 0) ok = issue_s(t, 0);
@@ -644,7 +668,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int t = first; ok && t < end; ++t) {
           if (L::OWN_P && i + 1 < ns[t]) ok = issue_s(t, i + 1);
           if (ok && i < ns[t]) ok = issue_pv(t, i);
-          if (!L::OWN_P && ok && i + 1 < ns[t]) ok = issue_s(t, i + 1);
         }
       base += 2 * n;
     }
