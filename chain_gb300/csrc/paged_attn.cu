@@ -203,9 +203,15 @@ __device__ __forceinline__ long long unit_cost(const Params &p, const Seq &s, in
   const int i0 = q * 2 * p.tpt;
   return p.overhead + (long long)tile_cost(p, s.n - i0) * tiles_to(p, s, i0 + 2 * p.tpt);
 }
+// 64-bit division takes hundreds of cycles and is hardly ever needed
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
 // Key tile at a cost offset into a unit.
 __device__ __forceinline__ int tile_at(const Params &p, long long off, int w) {
-  return off <= p.overhead ? 0 : (int)((off - p.overhead) / w);
+  return off <= p.overhead ? 0 : (int)quotient(off - p.overhead, w);
 }
 
 // Cost of one K/V head of the sequence
@@ -214,12 +220,6 @@ __device__ __forceinline__ long long head_cost(const Params &p, const Seq &s) {
   long long t = 0;
   for (int q = 0; q < nu; ++q) t += unit_cost(p, s, q);
   return t;
-}
-
-// 64-bit division takes hundreds of cycles and is hardly ever needed
-__device__ __forceinline__ long long quotient(long long a, long long b) {
-  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
-  return a / b;
 }
 
 struct Place {
@@ -907,49 +907,49 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 // Joins a unit that runs' ends cut into parts: block (c, y) the unit that
-// boundary c + 1 falls into, if that is the unit's first boundary.  A block takes 32
-// rows and a warp D / 8 columns of them, a lane to a row as in the parts, PB parts loaded
-// at once, in the order of the keys; the kernel is a few dependent loads long.
-// Rows go out through shared memory.
-template <int D>
-__global__ void __launch_bounds__(256) paged_combine_kernel(const Params p) {
-  constexpr int Q = D / 32, PB = 4;  // float4 a lane, parts at once
-  __shared__ uint2 rows[32][D / 4 + 1];
-  pdl_wait();  // the parts and boundaries
-  const int c = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Boundary bd = p.bounds[c];
-  const int tiles = bd.ntok > p.tpt ? 2 : 1;  // rows are numbered as in the unit's query tiles
-  if (!bd.cut || (int)blockIdx.y >= tiles * BM / 32) return;
-  if (tile_at(p, run_start(bd.total, c - 1) - bd.u0, bd.w) > 0) return;
-  const int r = blockIdx.y * 32 + lane;
+// boundary c + 1 falls into, if that is the unit's first boundary.  A block takes
+// `ROWS` rows and a warp D / 8 columns of them; a lane takes a row, as in the
+// parts, and every GROUPS-th part of it, PB loaded at once: the kernel is a
+// few dependent loads long.  Rows go out through shared memory.
+template <int D, int ROWS>
+__device__ __forceinline__ void combine_rows(const Params &p, const Boundary &bd, int c, int first_row,
+                                             uint2 (*rows)[D / 4 + 1]) {
+  constexpr int Q = D / 32, PB = 2, GROUPS = 32 / ROWS;  // Q: float4 a lane
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = lane / ROWS;
+  const int r = first_row + lane % ROWS;
   const int rt = (r % BM) / p.G, tok = (r / BM) * p.tpt + rt;
   const bool valid = rt < p.tpt && tok < bd.ntok;
-  if (!__syncthreads_or(valid)) return;
   float m = -INFINITY, l = 0.0f;
   float4 o[Q];
 #pragma unroll
   for (int q = 0; q < Q; ++q) o[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   // block c - 1 holds the first part, as its last unit; the next blocks the others, as
   // their first, down to the one that holds the unit's last key tile
-  int j0 = 0;
-  for (int k0 = c - 1; j0 < bd.nt; k0 += PB) {
+  const long long end = bd.u0 + p.overhead + (long long)bd.w * bd.nt;
+  // a run shorter than a key tile may hold none of it, and then no part
+  const bool tiny = bd.total < (long long)CTAS * (bd.w + 1);
+  auto has_part = [&](int k) {
+    if (k >= CTAS || run_start(bd.total, k) >= end) return false;
+    if (!tiny) return true;
+    const int j0 = tile_at(p, run_start(bd.total, k) - bd.u0, bd.w);
+    return run_start(bd.total, k + 1) >= end || tile_at(p, run_start(bd.total, k + 1) - bd.u0, bd.w) > j0;
+  };
+  for (int k0 = c - 1; k0 < CTAS && run_start(bd.total, k0) < end; k0 += PB * GROUPS) {
     float2 x[PB];
     float4 v[PB][Q];
 #pragma unroll
     for (int i = 0; i < PB; ++i) {
-      const int k = k0 + i;
-      const int j1 = k + 1 < CTAS ? min(bd.nt, tile_at(p, run_start(bd.total, k + 1) - bd.u0, bd.w)) : bd.nt;
+      const int k = k0 + i * GROUPS + group;
       x[i] = make_float2(-INFINITY, 0.0f);
 #pragma unroll
       for (int q = 0; q < Q; ++q) v[i][q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (j1 > j0 && valid) {  // an empty run holds no part
+      if (valid && has_part(k)) {
         const int64_t slot = (int64_t)k * 2 + (k < c ? 1 : 0);
         const float4 *po = reinterpret_cast<const float4 *>(p.part_o) + slot * (2 * BM * D / 4) + r;
         x[i] = p.part_ml[slot * (2 * BM) + r];
 #pragma unroll
         for (int q = 0; q < Q; ++q) v[i][q] = po[(warp * Q + q) * (2 * BM)];
       }
-      j0 = max(j0, j1);
     }
     float top = m;
 #pragma unroll
@@ -979,23 +979,60 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const Params p) {
       }
     }
   }
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  __syncwarp();
+  // the groups' shares of the row
 #pragma unroll
-  for (int q = 0; q < Q; ++q)
-    rows[lane][warp * Q + q] =
-        make_uint2(pack_bf16(o[q].x * inv, o[q].y * inv), pack_bf16(o[q].z * inv, o[q].w * inv));
-  if (warp == 0 && valid)
-    p.LSE[((int64_t)bd.head * p.G + r % BM - rt * p.G) * p.lse_shead + bd.tok0 + tok] =
-        l > 0.0f ? (m + lg2(l)) * 0.69314718055994531f : -INFINITY;
+  for (int step = ROWS; step < 32; step <<= 1) {
+    const float om = __shfl_xor_sync(0xffffffffu, m, step), top = fmaxf(m, om);
+    const float w0 = top == -INFINITY ? 0.0f : ex2(m - top), w1 = top == -INFINITY ? 0.0f : ex2(om - top);
+    m = top;
+    l = l * w0 + __shfl_xor_sync(0xffffffffu, l, step) * w1;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      o[q].x = o[q].x * w0 + __shfl_xor_sync(0xffffffffu, o[q].x, step) * w1;
+      o[q].y = o[q].y * w0 + __shfl_xor_sync(0xffffffffu, o[q].y, step) * w1;
+      o[q].z = o[q].z * w0 + __shfl_xor_sync(0xffffffffu, o[q].z, step) * w1;
+      o[q].w = o[q].w * w0 + __shfl_xor_sync(0xffffffffu, o[q].w, step) * w1;
+    }
+  }
+  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  if (group == 0) {
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+      rows[lane % ROWS][warp * Q + q] =
+          make_uint2(pack_bf16(o[q].x * inv, o[q].y * inv), pack_bf16(o[q].z * inv, o[q].w * inv));
+    if (warp == 0 && valid)
+      p.LSE[((int64_t)bd.head * p.G + r % BM - rt * p.G) * p.lse_shead + bd.tok0 + tok] =
+          l > 0.0f ? (m + lg2(l)) * 0.69314718055994531f : -INFINITY;
+  }
   __syncthreads();
-  for (int i = warp; i < 32; i += 8) {
-    const int ri = blockIdx.y * 32 + i, ti = (ri % BM) / p.G, tk = (ri / BM) * p.tpt + ti;
+  for (int i = warp; i < ROWS; i += 8) {
+    const int ri = first_row + i, ti = (ri % BM) / p.G, tk = (ri / BM) * p.tpt + ti;
     if (ti >= p.tpt || tk >= bd.ntok) continue;
     uint2 *dst = reinterpret_cast<uint2 *>(
         p.O + ((int64_t)bd.tok0 + tk) * p.o_stok +
         ((int64_t)bd.head * p.G + ri % BM - ti * p.G) * p.o_shead);
     if (lane < D / 4) dst[lane] = rows[i][lane];
   }
+}
+
+template <int D>
+__global__ void __launch_bounds__(256, 4) paged_combine_kernel(const Params p) {
+  __shared__ uint2 rows[32][D / 4 + 1];
+  pdl_wait();  // the parts and boundaries
+  const int c = blockIdx.x + 1, y = blockIdx.y;
+  const Boundary bd = p.bounds[c];
+  const int tiles = bd.ntok > p.tpt ? 2 : 1;  // rows are numbered as in the unit's query tiles
+  if (!bd.cut || y >= tiles * BM / 32) return;
+  // no row of this block: those of a tile's tokens lie together from its first row on
+  const int tok = bd.ntok - (y * 32 / BM) * p.tpt;
+  if ((y * 32) % BM >= min(tok, p.tpt) * p.G) return;
+  if (tile_at(p, run_start(bd.total, c - 1) - bd.u0, bd.w) > 0) return;
+  // a single token's few rows, over many blocks' parts: the parts are shared out among lanes
+  if (bd.ntok * p.G <= 8)
+    combine_rows<D, 8>(p, bd, c, 0, rows);
+  else
+    combine_rows<D, 32>(p, bd, c, y * 32, rows);
 }
 
 size_t part_bytes(int d) { return (size_t)CTAS * 2 * 2 * BM * d * sizeof(float); }
@@ -1050,6 +1087,8 @@ cudaError_t launch(const PagedAttnArgs &a, const WaitCfg &wc, cudaStream_t st) {
   paged_attn_kernel<D><<<CTAS, THREADS, L::ALLOC, st>>>(mq, mk, mv, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   timing_mark(st, 1);
+  // no sequence is longer than a key tile: no unit is cut
+  if (((int64_t)a.seqs.max_pages << a.seqs.page_shift) <= BN) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(CTAS - 1, 2 * BM / 32);
   cfg.blockDim = dim3(256);
