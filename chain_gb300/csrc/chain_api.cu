@@ -188,7 +188,8 @@ void timing_mark(cudaStream_t st, int k) {
 }
 
 cudaError_t make_tmap(CUtensorMap *map, CUtensorMapDataType dt, int rank, const void *base,
-                      const uint64_t *dims, const uint64_t *strides_bytes, const uint32_t *box) {
+                      const uint64_t *dims, const uint64_t *strides_bytes, const uint32_t *box,
+                      CUtensorMapL2promotion promote) {
   if (!g_encode) return cudaErrorInitializationError;
   cuuint64_t gd[5], gs[4];
   cuuint32_t bx[5], es[5];
@@ -200,7 +201,7 @@ cudaError_t make_tmap(CUtensorMap *map, CUtensorMapDataType dt, int rank, const 
   for (int i = 0; i + 1 < rank; ++i) gs[i] = strides_bytes[i];
   CUresult r = g_encode(map, dt, (cuuint32_t)rank, const_cast<void *>(base), gd, gs, bx, es,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                        promote, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 

@@ -12,8 +12,11 @@ namespace chain {
 // Encodes a 2-D/3-D bf16 or f32 tiled tensor map with 128-byte swizzle.
 // dims/strides are innermost first; strides (bytes) exclude the innermost.
 // Returns cudaSuccess or cudaErrorInvalidValue on encode failure.
+// promote is the least that a miss of the second-level cache fetches: 256 bytes where the
+// neighbouring bytes are read soon by the same block, 128 where they are not.
 cudaError_t make_tmap(CUtensorMap *map, CUtensorMapDataType dt, int rank, const void *base,
-                      const uint64_t *dims, const uint64_t *strides_bytes, const uint32_t *box);
+                      const uint64_t *dims, const uint64_t *strides_bytes, const uint32_t *box,
+                      CUtensorMapL2promotion promote = CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 
 struct AttnFwdArgs {
   const void *Q, *K, *V;  // [BH][n][d]

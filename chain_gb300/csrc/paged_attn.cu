@@ -87,9 +87,10 @@ struct Layout {
   static constexpr int ISSUERS = D == 128 ? 1 : 2;
   static_assert(ISSUERS == 1 || NS % 4 == 0, "two issuers: a unit's slot stays with one stream");
   // Costs, in quarters of a key tile against one query tile: fitted to the blocks' times over
-  // mixed batches (cycles at d = 128 / 64: tile 2,600 / 1,400 with one query tile,
-  // 3,300 / 2,200 with two; a unit's start and end 5,000 to 7,000).
-  static constexpr int COST1 = 4, COST2 = D == 128 ? 5 : 6, OVERHEAD = D == 128 ? 9 : 16;
+  // mixed batches (cycles at d = 128 / 64: tile 2,600 / 1,400 with one query tile, 3,300 / 2,200
+  // with two; a unit's start and end 5,000 to 7,000), the last then raised, as dearer units
+  // leave fewer of them cut and joined (24 mixed sequences at d = 128: 95 us with 9, 90 with 14).
+  static constexpr int COST1 = 4, COST2 = D == 128 ? 5 : 6, OVERHEAD = D == 128 ? 14 : 20;
   // Tensor memory: S0 [0,128), S1 [128,256).  At d = 64 P has columns of its own, so that a
   // stream's next S is computed while its softmax still runs; at d = 128 there is no
   // room, and P overwrites S.
@@ -1076,10 +1077,16 @@ cudaError_t launch(const PagedAttnArgs &a, const WaitCfg &wc, cudaStream_t st) {
   const uint64_t sk[3] = {(uint64_t)a.kc.s_slot * 2, (uint64_t)a.kc.s_head * 2, (uint64_t)a.kc.s_page * 2};
   const uint64_t sv[3] = {(uint64_t)a.vc.s_slot * 2, (uint64_t)a.vc.s_head * 2, (uint64_t)a.vc.s_page * 2};
   const uint32_t bk[4] = {64, (uint32_t)(page < BN ? page : BN), 1, 1};
+  // A token's row of one K/V head is 128 bytes at d = 64, and the bytes after it belong to
+  // another head, which another unit reads much later: fetched 256 at a time, half of the
+  // traffic is for nothing (64 sequences of 32,768 keys, 8 K/V heads: 885 us, against 637).
+  // At d = 128 the row is the 256 bytes (64 sequences of 8,192: 341 us, 343 with 128).
+  const CUtensorMapL2promotion promote =
+      D == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
   cudaError_t e;
   if ((e = make_tmap(&mq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.Q, dq, sq, bq)) != cudaSuccess ||
-      (e = make_tmap(&mk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, a.kc.ptr, dk, sk, bk)) != cudaSuccess ||
-      (e = make_tmap(&mv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, a.vc.ptr, dk, sv, bk)) != cudaSuccess)
+      (e = make_tmap(&mk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, a.kc.ptr, dk, sk, bk, promote)) != cudaSuccess ||
+      (e = make_tmap(&mv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, a.vc.ptr, dk, sv, bk, promote)) != cudaSuccess)
     return e;
   e = cudaFuncSetAttribute(paged_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC);
   if (e != cudaSuccess) return e;
