@@ -366,7 +366,7 @@ def chain_qk_norm_rope(Q, K, gq, gk, inv_freq, positions, eps, pairs, Qo, Ko, st
 
 
 def chain_qk_norm_rope_bwd_workspace_size(Q) -> int:
-    return int(_load().chain_qk_norm_rope_bwd_workspace_size(_ref(desc(Q))))
+    return _small().qk_norm_rope_bwd_workspace_size(Q)
 
 
 def chain_qk_norm_rope_bwd(dQo, dKo, Q, K, gq, gk, inv_freq, positions, eps, pairs, dQ, dK, dgq, dgk,
@@ -595,8 +595,8 @@ def relayout(shards, p: int, head_group: int, stream=None):
     return out
 
 
-def _dense_like(t):
-    return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+def _dense_like(t, **kw):
+    return torch.empty_like(t, memory_format=torch.contiguous_format, **kw)
 
 
 def qk_norm_rope(q, k, gq, gk, inv_freq, positions=None, eps: float = 1e-6, interleaved: bool = False,
@@ -612,11 +612,10 @@ def qk_norm_rope_bwd(dqo, dko, q, k, gq, gk, inv_freq, positions=None, eps: floa
                      interleaved: bool = False, workspace=None, stream=None):
     """Gradients of qk_norm_rope: returns (dq, dk, dgq, dgk), dgq and dgk f32."""
     dq, dk = _dense_like(q), _dense_like(k)
-    dg = torch.empty(2, q.shape[-1], dtype=torch.float32, device=q.device)
+    dgq, dgk = _dense_like(gq, dtype=torch.float32), _dense_like(gk, dtype=torch.float32)
     if workspace is None:
         workspace = torch.empty(max(chain_qk_norm_rope_bwd_workspace_size(q), 16), dtype=torch.uint8,
                                 device=q.device)
-    dgq, dgk = dg[0], dg[1]
     chain_qk_norm_rope_bwd(dqo, dko, q, k, gq, gk, inv_freq, positions, eps, int(interleaved), dq, dk,
                            dgq, dgk, workspace, stream)
     return dq, dk, dgq, dgk

@@ -45,13 +45,14 @@ static int read_sizes(PyObject *t, int64_t *out, int most) {
   return (int)n;
 }
 
+/* dev < 0: any. */
 static int on_device(PyObject *t, long dev) {
   PyObject *g = PyObject_CallMethodNoArgs(t, s_get_device);
   if (!g) return -1;
   const long d = PyLong_AsLong(g);
   Py_DECREF(g);
   if (d == -1 && PyErr_Occurred()) return -1;
-  if (d == dev) return 0;
+  if (d == dev || dev < 0) return 0;
   PyErr_Format(PyExc_ValueError, "chain_gb300: tensors must be on the current device, cuda:%ld", dev);
   return -1;
 }
@@ -247,6 +248,15 @@ static PyObject *qk_norm_rope_bwd(PyObject *self, PyObject *const *a, Py_ssize_t
               "chain_qk_norm_rope_bwd");
 }
 
+/* Sizes only: Q may lie on any device. */
+static PyObject *qk_norm_rope_bwd_workspace_size(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+  (void)self;
+  if (count(n, 1, "chain_qk_norm_rope_bwd_workspace_size")) return NULL;
+  chain_tensor_t q, *Q;
+  if (tensor(a[0], -1, 0, &q, &Q)) return NULL;
+  return PyLong_FromSize_t(chain_qk_norm_rope_bwd_workspace_size(Q));
+}
+
 static PyObject *paged_append(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   (void)self;
   if (count(n, 9, "chain_paged_append")) return NULL;
@@ -310,6 +320,7 @@ static PyObject *fwd_paged(PyObject *self, PyObject *const *a, Py_ssize_t n) {
 #define METHOD(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, NULL}
 static PyMethodDef methods[] = {METHOD(setup),        METHOD(qk_norm_rope),        METHOD(qk_norm_rope_bwd),
                                 METHOD(paged_append), METHOD(qk_norm_rope_append), METHOD(fwd_paged),
+                                METHOD(qk_norm_rope_bwd_workspace_size),
                                 {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", NULL, -1, methods, NULL, NULL, NULL, NULL};
 
