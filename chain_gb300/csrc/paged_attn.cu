@@ -927,15 +927,24 @@ __device__ __forceinline__ void combine_rows(const Params &p, const Boundary &bd
   // block c - 1 holds the first part, as its last unit; the next blocks the others, as
   // their first, down to the one that holds the unit's last key tile
   const long long end = bd.u0 + p.overhead + (long long)bd.w * bd.nt;
+  auto begins = [&](int k) { return k < CTAS && run_start(bd.total, k) < end; };
+  // Where a lane takes many parts, one after another, their end is found first (8 tokens over
+  // 4,096 keys: 26.3 us -> 22.6); a single token's lanes take one or two (17.3 us, 16.6 without).
+  int k1 = c - 1;
+  for (uint32_t in = ~0u; ROWS == 32 && in == ~0u;) {
+    in = __ballot_sync(0xffffffffu, begins(k1 + lane));
+    k1 += __popc(in);
+  }
+  auto in_unit = [&](int k) { return ROWS == 32 ? k < k1 : begins(k); };
   // a run shorter than a key tile may hold none of it, and then no part
   const bool tiny = bd.total < (long long)CTAS * (bd.w + 1);
   auto has_part = [&](int k) {
-    if (k >= CTAS || run_start(bd.total, k) >= end) return false;
+    if (!in_unit(k)) return false;
     if (!tiny) return true;
     const int j0 = tile_at(p, run_start(bd.total, k) - bd.u0, bd.w);
     return run_start(bd.total, k + 1) >= end || tile_at(p, run_start(bd.total, k + 1) - bd.u0, bd.w) > j0;
   };
-  for (int k0 = c - 1; k0 < CTAS && run_start(bd.total, k0) < end; k0 += PB * GROUPS) {
+  for (int k0 = c - 1; in_unit(k0); k0 += PB * GROUPS) {
     float2 x[PB];
     float4 v[PB][Q];
 #pragma unroll
