@@ -599,25 +599,38 @@ def _dense_like(t, **kw):
     return torch.empty_like(t, memory_format=torch.contiguous_format, **kw)
 
 
+def _current(stream):
+    """`stream` as the current one: what a call allocates then belongs to the stream that uses it."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
+
+
 def qk_norm_rope(q, k, gq, gk, inv_freq, positions=None, eps: float = 1e-6, interleaved: bool = False,
                  stream=None):
     """RMS norm and rotary embedding of q [T, H, d] and k [T, Hkv, d] (or
     [B, n, heads, d]), any head and token strides.  Returns dense (q, k)."""
+    if stream is not None:
+        with _current(stream):
+            return qk_norm_rope(q, k, gq, gk, inv_freq, positions, eps, interleaved)
     qo, ko = _dense_like(q), _dense_like(k)
-    chain_qk_norm_rope(q, k, gq, gk, inv_freq, positions, eps, int(interleaved), qo, ko, stream)
+    chain_qk_norm_rope(q, k, gq, gk, inv_freq, positions, eps, int(interleaved), qo, ko)
     return qo, ko
 
 
 def qk_norm_rope_bwd(dqo, dko, q, k, gq, gk, inv_freq, positions=None, eps: float = 1e-6,
                      interleaved: bool = False, workspace=None, stream=None):
     """Gradients of qk_norm_rope: returns (dq, dk, dgq, dgk), dgq and dgk f32."""
+    if stream is not None:
+        with _current(stream):
+            return qk_norm_rope_bwd(dqo, dko, q, k, gq, gk, inv_freq, positions, eps, interleaved, workspace)
     dq, dk = _dense_like(q), _dense_like(k)
     dgq, dgk = _dense_like(gq, dtype=torch.float32), _dense_like(gk, dtype=torch.float32)
     if workspace is None:
         workspace = torch.empty(max(chain_qk_norm_rope_bwd_workspace_size(q), 16), dtype=torch.uint8,
                                 device=q.device)
     chain_qk_norm_rope_bwd(dqo, dko, q, k, gq, gk, inv_freq, positions, eps, int(interleaved), dq, dk,
-                           dgq, dgk, workspace, stream)
+                           dgq, dgk, workspace)
     return dq, dk, dgq, dgk
 
 
@@ -627,9 +640,13 @@ def qk_norm_rope_append(q, k, v, gq, gk, inv_freq, k_cache, v_cache, cu_seqlens,
     at their cache positions; the rotated k and v go into their pages of
     k_cache, v_cache [pages, page, Hkv, d].  Returns the rotated q (rows behind
     the last sequence are not written)."""
+    if stream is not None:
+        with _current(stream):
+            return qk_norm_rope_append(q, k, v, gq, gk, inv_freq, k_cache, v_cache, cu_seqlens, kv_lens,
+                                       page_table, eps, interleaved)
     qo = _dense_like(q)
     chain_qk_norm_rope_append(q, k, v, gq, gk, inv_freq, eps, int(interleaved), cu_seqlens, kv_lens,
-                              page_table, k_cache, v_cache, qo, stream)
+                              page_table, k_cache, v_cache, qo)
     return qo
 
 
@@ -638,6 +655,10 @@ def attention_fwd_paged(q, k_cache, v_cache, cu_seqlens, kv_lens, page_table, ca
     """Packed new tokens q [total, H, d] over a paged cache that already holds
     them.  Returns (O [total, H, d], LSE [H, total]); rows behind the last
     sequence are not written."""
+    if stream is not None:
+        with _current(stream):
+            return attention_fwd_paged(q, k_cache, v_cache, cu_seqlens, kv_lens, page_table, causal, scale,
+                                       workspace)
     scale = q.shape[-1] ** -0.5 if scale is None else scale
     o = _dense_like(q)
     lse = torch.empty(q.shape[1], q.shape[0], dtype=torch.float32, device=q.device)
@@ -645,5 +666,5 @@ def attention_fwd_paged(q, k_cache, v_cache, cu_seqlens, kv_lens, page_table, ca
         workspace = torch.empty(max(chain_fwd_paged_workspace_size(q, k_cache), 16), dtype=torch.uint8,
                                 device=q.device)
     chain_fwd_paged(q, k_cache, v_cache, cu_seqlens, kv_lens, page_table,
-                    MASK_CAUSAL if causal else MASK_NONE, scale, o, lse, workspace, stream)
+                    MASK_CAUSAL if causal else MASK_NONE, scale, o, lse, workspace)
     return o, lse

@@ -916,8 +916,8 @@ static int heads_view(const chain_tensor_t *t, int max_nd, NormRopeSide *s, int6
   if (*batch == 0 || *n == 0) return CHAIN_OK;  // no tokens: the pointer may be null
   if (!t->ptr || !aligned16(t->ptr) || t->stride[nd - 1] != 1) return CHAIN_ERR_ARG;
   for (int i = 0; i + 1 < nd; ++i)
-    if (t->shape[i] > 1 && (t->stride[i] <= 0 || (t->stride[i] * es) % 16 ||
-                            t->stride[i] > (int64_t(1) << 40)))
+    if (t->shape[i] > 1 && (t->stride[i] <= 0 || t->stride[i] >= (int64_t(1) << 40) / es ||
+                            (t->stride[i] * es) % 16))
       return CHAIN_ERR_ARG;
   if (*n > 1) s->s_tok = t->stride[nd - 3];
   s->s_batch = nd == 4 && *batch > 1 ? t->stride[0] : *n * s->s_tok;  // one entry: as if tokens went on
@@ -1050,7 +1050,7 @@ static int pool_view(const chain_tensor_t *t, PagedSide *s, int64_t (&shape)[4])
   for (int i = 0; i < 3; ++i) {
     st[i] = t->stride[i];
     if (shape[i] == 1) st[i] = shape[3];  // any value is allowed there: a valid one for the tensor map
-    if (st[i] < shape[3] || (st[i] * 2) % 16 || st[i] * 2 >= (int64_t(1) << 40)) return CHAIN_ERR_ARG;
+    if (st[i] < shape[3] || st[i] >= (int64_t(1) << 39) || (st[i] * 2) % 16) return CHAIN_ERR_ARG;
   }
   s->ptr = t->ptr;
   s->s_page = st[0]; s->s_slot = st[1]; s->s_head = st[2];

@@ -676,7 +676,8 @@ __device__ __forceinline__ Spot spot_of(const AppendArgs &a, int t, int lane) {
   const PagedSeqs &s = a.seqs;
   Spot sp = {0, 0, 0, 0, 0};
   const int b = sequence_of(s.cu, s.batch, t, lane);
-  const int first = __ldg(s.cu + b), end = __ldg(s.cu + b + 1), len = __ldg(s.lens + b);
+  const int first = __ldg(s.cu + b), len = __ldg(s.lens + b);
+  const int end = min(__ldg(s.cu + b + 1), (int)a.tokens);
   if (t < first || t >= end) return sp;  // a row behind the last sequence
   sp.in = 1;
   sp.pos = (int64_t)len - end + t;

@@ -443,9 +443,9 @@ int chain_fwd_fp8(const chain_tensor_t *Q, const chain_tensor_t *K,
  * are not rotated.
  *   Q, Qo      [T][H][d], K, Ko [T][Hkv][d]; or 4-D [B][n][heads][d].  All of one
  *              type, bf16 or f32; d = 64 or 128, contiguous; each tensor has
- *              its own other strides, multiples of 16 bytes and positive, so views
- *              of one fused projection are taken, and head-major tensors
- *              through their transposed view.  Qo, Ko may be Q, K themselves
+ *              its own other strides, multiples of 16 bytes, positive and below
+ *              2^40 bytes, and begins on 16 bytes: views of one fused projection
+ *              are taken, and head-major tensors through their transposed view.  Qo, Ko may be Q, K themselves
  *              (same pointer and strides); otherwise no tensor written may
  *              overlap another.
  *   gq, gk     [d] weights, bf16 or f32, contiguous, 16-byte aligned.

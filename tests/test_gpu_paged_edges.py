@@ -1,0 +1,214 @@
+"""GPU: the norm + rotation and paged-cache calls where they could go wrong --
+other streams and two calls at once, captured graphs, offsets past 32 bits,
+the largest batch, shared pages and rows behind what is packed.  Attention is
+checked against the definition in 64 bits with the tolerances of
+test_gpu_paged; the rest bit for bit against the same call made plainly."""
+import pytest
+import torch
+
+import chain_synth as cs
+from test_gpu_paged import Cache, cg, check  # noqa: F401  (cg: the fixture)
+from test_gpu_qk_norm_rope import EPS, freqs
+
+pytestmark = pytest.mark.gpu
+
+
+def calls(cg, d=128):
+    """Each call on inputs of its own, as f(stream) -> outputs."""
+    c = Cache([300, 1, 77], [130, 1, 5], 2, d, 32, 31).fill().cuda()
+    q, k, v = (cs.normal((c.total, h, d), 60 + h).cuda() for h in (8, 2, 2))
+    g, w = (1 + 0.1 * cs.normal((d,), 64, dtype=torch.float32)).cuda(), freqs(d).cuda()
+    return {
+        "forward": lambda s: cg.qk_norm_rope(q, k, g, g, w, stream=s),
+        "backward": lambda s: cg.qk_norm_rope_bwd(q, k, q, v, g, g, w, stream=s),
+        "append": lambda s: (cg.qk_norm_rope_append(q, k, v, g, g, w, c.kcd.clone(), c.vcd.clone(), *c.args,
+                                                    stream=s),),
+        "attention": lambda s: cg.attention_fwd_paged(q, c.kcd, c.vcd, *c.args, causal=True, stream=s),
+    }
+
+
+@pytest.mark.parametrize("name", ["forward", "backward", "append", "attention"])
+def test_outputs_belong_to_the_stream_given(cg, name):
+    # memory that the current stream has freed but still writes must not become another stream's output
+    f = calls(cg)[name]
+    ref = [x.clone() for x in f(None)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for s in (side, side.cuda_stream):
+        torch.cuda._sleep(200_000_000)
+        junk = [torch.empty_like(x) for x in ref for _ in range(2)]
+        for x in junk:
+            x.fill_(7)
+        del junk
+        out = f(s)
+        side.synchronize()
+        torch.cuda.synchronize()
+        for a, b in zip(out, ref):
+            assert torch.equal(a, b)
+
+
+def test_two_calls_at_once(cg):
+    # two streams, their launches interleaved: every result as alone
+    H, d = 16, 64
+    cases = [Cache(lens, news, 2, d, 16, 80 + i).fill().cuda()
+             for i, (lens, news) in enumerate([([3000, 20, 700], [1, 1, 90]), ([1900, 1900], [1, 1])])]
+    qs = [cs.normal((c.total, H, d), 85 + i).cuda() for i, c in enumerate(cases)]
+    ws = [torch.empty(cg.chain_fwd_paged_workspace_size(q, c.kcd), dtype=torch.uint8, device="cuda")
+          for q, c in zip(qs, cases)]
+    g, w = torch.ones(d, device="cuda"), freqs(d).cuda()
+    both = lambda i, s: (*cg.attention_fwd_paged(qs[i], cases[i].kcd, cases[i].vcd, *cases[i].args, causal=True,
+                                                 workspace=ws[i], stream=s),
+                         *cg.qk_norm_rope_bwd(qs[i], qs[i], qs[i], qs[i], g, g, w, stream=s))
+    ref = [[x.clone() for x in both(i, None)] for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[], []]
+    for _ in range(10):
+        for i in range(2):
+            outs[i].append(both(i, streams[i]))
+    torch.cuda.synchronize()
+    assert cg.chain_check()[0] == 0
+    for i in range(2):
+        for out in outs[i]:
+            assert all(torch.equal(a, b) for a, b in zip(out, ref[i]))
+
+
+def test_a_layer_captured(cg):
+    # append, attention, norm forward and backward in one graph: replays give the eager bits
+    H, Hkv, d = 8, 2, 128
+    c = Cache([260, 40, 1], [4, 40, 1], Hkv, d, 16, 90).fill().cuda()
+    q, k, v = (cs.normal((c.total, h, d), 91 + h).cuda() for h in (H, Hkv, Hkv))
+    g, w = torch.ones(d, device="cuda"), freqs(d).cuda()
+    ws = torch.empty(cg.chain_fwd_paged_workspace_size(q, c.kcd), dtype=torch.uint8, device="cuda")
+
+    def layer():
+        qo = cg.qk_norm_rope_append(q, k, v, g, g, w, c.kcd, c.vcd, *c.args, eps=EPS)
+        o, lse = cg.attention_fwd_paged(qo, c.kcd, c.vcd, *c.args, causal=True, workspace=ws)
+        return (qo, o, lse, *cg.qk_norm_rope(q, k, g, g, w, eps=EPS), *cg.qk_norm_rope_bwd(o, v, q, k, g, g, w, eps=EPS))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        ref = [x.clone() for x in layer()]
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = layer()
+    for _ in range(3):
+        for x in out:
+            x.zero_()
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(out, ref))
+    assert cg.chain_check()[0] == 0
+
+
+def test_offsets_past_32_bits(cg):
+    # pages, tokens and heads further apart than 2^31 elements
+    far, d, page, Hkv, H = 2 ** 31 + 512, 128, 16, 1, 2
+    store = torch.empty(2 * far + 2 ** 20, dtype=torch.bfloat16, device="cuda")
+    pool = lambda at: store.as_strided((3, page, Hkv, d), (far, d, d, 1), at)
+    kc, vc = pool(0), pool(4096)
+    table = torch.tensor([[2, 0, 1]], dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([40], dtype=torch.int32, device="cuda")
+    old = cs.normal((2, 37, Hkv, d), 95)
+    q, k, v = cs.normal((3, H, d), 96), cs.normal((3, Hkv, d), 97), cs.normal((3, Hkv, d), 98)
+    qf = store.as_strided((3, H, d), (far, d, 1), 2 ** 17)
+    kf = store.as_strided((3, Hkv, d), (far, d, 1), 2 ** 18)
+    vf = store.as_strided((3, Hkv, d), (far, d, 1), 2 ** 18 + 512)
+    for x, y in ((qf, q), (kf, k), (vf, v)):
+        x.copy_(y)
+    first = torch.tensor([0, 37], dtype=torch.int32, device="cuda")
+    cg.chain_paged_append(old[0].cuda(), old[1].cuda(), first, torch.tensor([37], dtype=torch.int32, device="cuda"),
+                          table, kc, vc)
+    cg.chain_paged_append(kf, vf, cu, lens, table, kc, vc)
+    assert cg.chain_check()[0] == 0
+    keys, vals = torch.cat((old[0], k)), torch.cat((old[1], v))
+    for i, p in enumerate((2, 0, 1)):
+        n = min(page, 40 - i * page)
+        assert torch.equal(kc[p, :n].cpu(), keys[i * page:i * page + n])
+        assert torch.equal(vc[p, :n].cpu(), vals[i * page:i * page + n])
+    o, lse = cg.attention_fwd_paged(qf, kc, vc, cu, lens, table, causal=True)
+    c = Cache([40], [3], Hkv, d, page, 99)
+    c.k, c.v = [keys], [vals]
+    check(c, q, o, lse, True, d ** -0.5)
+    g, w = torch.ones(d, device="cuda"), freqs(d).cuda()
+    pos = torch.tensor([5, 6, 7], dtype=torch.int32, device="cuda")
+    ref = cg.qk_norm_rope(q.cuda(), k.cuda(), g, g, w, pos)
+    bwd = cg.qk_norm_rope_bwd(q.cuda(), k.cuda(), q.cuda(), k.cuda(), g, g, w, pos)
+    assert all(torch.equal(a, b) for a, b in zip(cg.qk_norm_rope(qf, kf, g, g, w, pos), ref))
+    assert all(torch.equal(a, b) for a, b in zip(cg.qk_norm_rope_bwd(qf, kf, qf, kf, g, g, w, pos), bwd))
+    cg.chain_qk_norm_rope(qf, kf, g, g, w, pos, 1e-6, 0, qf, kf)
+    assert torch.equal(qf, ref[0]) and torch.equal(kf, ref[1])
+
+
+def test_rows_beyond_the_packed_ones(cg):
+    # cu_seqlens past the packed rows counts only those: the writes and the attention agree on the positions
+    d, Hkv, H = 64, 2, 4
+    c = Cache([50], [8], Hkv, d, 16, 101).cuda()
+    k, v, q = cs.normal((8, Hkv, d), 102).cuda(), cs.normal((8, Hkv, d), 103).cuda(), cs.normal((8, H, d), 104).cuda()
+    g, w = torch.ones(d, device="cuda"), freqs(d).cuda()
+    over = torch.tensor([0, 11], dtype=torch.int32, device="cuda")
+    pools = [[c.kc.cuda(), c.vc.cuda()] for _ in range(2)]
+    for p, cu in zip(pools, (c.cud, over)):
+        cg.chain_paged_append(k, v, cu, c.lensd, c.tabled, *p)
+        p.append(cg.qk_norm_rope_append(q, k, v, g, g, w, *(x.clone() for x in p), cu, c.lensd, c.tabled))
+    for a, b in zip(*pools):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+    c.fill().cuda()
+    for a, b in zip(*(cg.attention_fwd_paged(q, c.kcd, c.vcd, cu, c.lensd, c.tabled, causal=True)
+                      for cu in (c.cud, over))):
+        assert torch.equal(a, b)
+    assert cg.chain_check()[0] == 0
+
+
+def test_largest_batch(cg):
+    B = 8192
+    lens = [(13 * i) % 45 + 1 for i in range(B)]
+    c = Cache(lens, [1] * B, 1, 64, 16, 105).fill().cuda()
+    q = cs.normal((B, 2, 64), 106)
+    o, lse = cg.attention_fwd_paged(q.cuda(), c.kcd, c.vcd, *c.args, causal=True)
+    assert cg.chain_check()[0] == 0
+    some = list(range(0, B, 37)) + [B - 1]
+    s = Cache([lens[i] for i in some], [1] * len(some), 1, 64, 16, 107)
+    s.k, s.v = [c.k[i] for i in some], [c.v[i] for i in some]
+    check(s, q[some], o[some], lse[:, some], True, 64 ** -0.5)
+
+
+def test_shared_pages_and_pools_of_two_layouts(cg):
+    # two sequences that share a prefix's pages, K token-major and V head-major, rows of the table further apart
+    Hkv, d, page = 2, 128, 16
+    c = Cache([48, 70], [1, 20], Hkv, d, page, 108)
+    c.table[1, :3] = c.table[0, :3]
+    c.k[1][:48], c.v[1][:48] = c.k[0], c.v[0]
+    c.fill()
+    wide = torch.full((2, c.table.shape[1] + 5), -3, dtype=torch.int32)
+    wide[:, :c.table.shape[1]] = c.table
+    vc = c.vc.transpose(1, 2).contiguous().cuda().transpose(1, 2)
+    c.cuda()
+    q = cs.normal((c.total, 6, d), 109)
+    o, lse = cg.attention_fwd_paged(q.cuda(), c.kcd, vc, c.cud, c.lensd, wide.cuda()[:, :c.table.shape[1]], causal=True)
+    assert cg.chain_check()[0] == 0
+    check(c, q, o, lse, True, d ** -0.5)
+
+
+# many units to a block, many key tiles to a unit: both forms of a unit, cut and whole
+LONG = {
+    "tokens, d 128": ([4000 - 61 * i for i in range(40)], [1] * 40, 16, 8, 128, 64),
+    "tokens, d 64": ([4000 - 61 * i for i in range(40)], [1] * 40, 16, 8, 64, 16),
+    "chunks, d 128": ([3100, 2500, 1700], [700, 129, 64], 16, 4, 128, 128),
+    "chunks, d 64": ([3100, 2500, 1700], [700, 129, 64], 16, 4, 64, 32),
+    "mixed, d 64": ([2900 - 83 * i for i in range(30)], [1 if i % 3 else 40 + 7 * i for i in range(30)], 8, 2, 64, 16),
+    "mixed, d 128": ([2900 - 83 * i for i in range(30)], [1 if i % 3 else 40 + 7 * i for i in range(30)], 8, 2, 128, 16),
+}
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("name", LONG)
+def test_long(cg, name, causal):
+    lens, news, H, Hkv, d, page = LONG[name]
+    c = Cache(lens, news, Hkv, d, page, 120 + len(name)).fill().cuda()
+    q = cs.normal((c.total, H, d), 121)
+    o, lse = cg.attention_fwd_paged(q.cuda(), c.kcd, c.vcd, *c.args, causal=causal)
+    assert cg.chain_check()[0] == 0
+    check(c, q, o, lse, causal, d ** -0.5)

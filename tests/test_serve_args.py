@@ -158,3 +158,11 @@ def test_attention_only(cg):
     # no tokens: done without a device
     e, l = D(cg, (0, 4, 128), ptr=0), D(cg, (4, 0), cg.F32, ptr=0)
     assert paged(cg, "attn", Q=e, O=e, L=l) == cg.OK
+
+
+def test_strides_out_of_reach(cg):
+    # no tensor spans 2^40 bytes: refused before a copy is described with such a stride
+    for far in (2 ** 39, 2 ** 61, 2 ** 63 - 8):
+        assert rope(cg, Q=D(cg, (10, 4, 128), strides=(far, 128, 1))) == cg.ERR_ARG
+        assert paged(cg, "attn", Q=D(cg, (10, 4, 128), strides=(far, 128, 1))) == cg.ERR_ARG
+        assert paged(cg, "append", Kc=D(cg, (20, 16, 2, 128), strides=(far, 256, 128, 1))) == cg.ERR_ARG
