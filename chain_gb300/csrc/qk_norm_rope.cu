@@ -82,28 +82,36 @@ __device__ __forceinline__ float2 angle(int p, unsigned long long u) {
 }
 
 // ------------------------------------------------------ sixteen elements a lane
-// A lane holds sixteen elements of a row as two groups of eight: eight pairs, the
-// firsts and the seconds.  Pairs (i, i + rot/2): the firsts from the first half
-// of the rotated elements and the seconds from the second, so that a rotation
-// needs no other lane; pairs (2i, 2i + 1), and elements that do not rotate: sixteen
-// in a row.  (With eight elements a lane, the reduction, the addressing and the loop
-// cost twice as much for each element, and the instruction issue bounded the kernels.)
+// A lane holds sixteen elements of a row as eight pairs, in parts of 16 bytes (eight bf16,
+// four f32), and the lanes' parts lie side by side: with n lanes, lane l's part j is the
+// (j n + l)th, so that a warp's access covers whole sectors.  (Sixteen elements in a row a
+// lane, forward of 40 heads of d = 128: pairs (2i, 2i + 1) of 32,768 tokens in bf16 150 us,
+// 118 so; 16,384 tokens in f32 149 us, 110 so; the backward gains as much again.)  The lanes
+// of the rotated elements and those of the others are dealt apart; pairs (i, i + rot/2)
+// then lie in one lane, as pairs (2i, 2i + 1) do, and a rotation needs no other lane.  (With
+// eight elements a lane, the reduction, the addressing and the loop cost twice as much for
+// each element, and the instruction issue bounded the kernels.)
 constexpr int EPL = 16;
+template <typename T>
+constexpr int part_of() { return 16 / (int)sizeof(T); }  // elements
 struct Lane {
-  int a, b;  // first elements of its groups of eight, as they lie in memory
-  int f;     // its first frequency
-  bool on;   // its elements rotate
+  int at, step;  // its first part, from one part to the next; its elements rotate if at < rot
 };
-template <int D, bool NEIGHBOUR>
+template <typename T, int D>
 __device__ __forceinline__ Lane lane_of(int lane, int rot) {
-  const int l = lane % (D / EPL);
+  constexpr int W = part_of<T>();
+  const int l = lane % (D / EPL), n = rot / EPL;
   Lane r;
-  r.on = l * 16 < rot;
-  r.f = l * 8;
-  const bool split = r.on && !NEIGHBOUR;
-  r.a = split ? l * 8 : l * 16;
-  r.b = split ? rot / 2 + l * 8 : l * 16 + 8;
+  r.at = l < n ? l * W : rot + (l - n) * W;
+  r.step = (l < n ? n : D / EPL - n) * W;
   return r;
+}
+// Where a lane's element k lies in the row: k < 8 the firsts of the pairs, from 8 on their seconds
+template <typename T, bool NEIGHBOUR>
+__device__ __forceinline__ int element(const Lane &ln, int k) {
+  constexpr int W = part_of<T>();
+  const int i = NEIGHBOUR ? 2 * (k % 8) + k / 8 : k;
+  return ln.at + i / W * ln.step + i % W;
 }
 
 // Asynchronous copy of 16 bytes into shared memory
@@ -116,7 +124,7 @@ __device__ __forceinline__ void wait_async() {  // all but the newest N groups h
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A lane's sixteen elements, as they lie in memory; get() gives the pairs' firsts in
+// A lane's sixteen elements, as its parts lie in memory; get() gives the pairs' firsts in
 // f[0..7] and their seconds in f[8..15].  In a ring slot each 16-byte part of a
 // warp's lanes lies side by side, 512 bytes a part.
 template <typename T>
@@ -124,13 +132,9 @@ struct Row;
 template <>
 struct Row<__nv_bfloat16> {
   uint4 a, b;
-  __device__ __forceinline__ void load(const __nv_bfloat16 *p, const Lane &ln) {
-    a = *reinterpret_cast<const uint4 *>(p + ln.a);
-    b = *reinterpret_cast<const uint4 *>(p + ln.b);
-  }
-  static __device__ __forceinline__ void fetch(uint32_t slot, const __nv_bfloat16 *p, const Lane &ln) {
-    copy_async(slot, p + ln.a);
-    copy_async(slot + 512, p + ln.b);
+  static __device__ __forceinline__ void fetch(uint32_t slot, const __nv_bfloat16 *p, int step) {
+    copy_async(slot, p);
+    copy_async(slot + 512, p + step);
   }
   __device__ __forceinline__ void take(const uint8_t *slot) {
     a = *reinterpret_cast<const uint4 *>(slot);
@@ -148,25 +152,21 @@ struct Row<__nv_bfloat16> {
     }
   }
   template <bool NEIGHBOUR>
-  static __device__ __forceinline__ void store(__nv_bfloat16 *p, const Lane &ln, const float (&f)[16]) {
+  static __device__ __forceinline__ void store(__nv_bfloat16 *p, int step, const float (&f)[16]) {
     uint32_t w[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k)
       w[k] = NEIGHBOUR ? pack_bf16(f[k], f[8 + k]) : pack_bf16(f[2 * k], f[2 * k + 1]);
-    *reinterpret_cast<uint4 *>(p + ln.a) = make_uint4(w[0], w[1], w[2], w[3]);
-    *reinterpret_cast<uint4 *>(p + ln.b) = make_uint4(w[4], w[5], w[6], w[7]);
+    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4 *>(p + step) = make_uint4(w[4], w[5], w[6], w[7]);
   }
 };
 template <>
 struct Row<float> {
   float4 v[4];
-  __device__ __forceinline__ void load(const float *p, const Lane &ln) {
+  static __device__ __forceinline__ void fetch(uint32_t slot, const float *p, int step) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = reinterpret_cast<const float4 *>(p + (k < 2 ? ln.a : ln.b))[k & 1];
-  }
-  static __device__ __forceinline__ void fetch(uint32_t slot, const float *p, const Lane &ln) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) copy_async(slot + 512 * k, p + (k < 2 ? ln.a : ln.b) + 4 * (k & 1));
+    for (int k = 0; k < 4; ++k) copy_async(slot + 512 * k, p + k * step);
   }
   __device__ __forceinline__ void take(const uint8_t *slot) {
 #pragma unroll
@@ -182,25 +182,21 @@ struct Row<float> {
     }
   }
   template <bool NEIGHBOUR>
-  static __device__ __forceinline__ void store(float *p, const Lane &ln, const float (&f)[16]) {
+  static __device__ __forceinline__ void store(float *p, int step, const float (&f)[16]) {
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      reinterpret_cast<float4 *>(p + (k < 2 ? ln.a : ln.b))[k & 1] =
+      *reinterpret_cast<float4 *>(p + k * step) =
           NEIGHBOUR ? make_float4(f[2 * k], f[8 + 2 * k], f[2 * k + 1], f[9 + 2 * k])
                     : make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
   }
 };
 
-template <bool NEIGHBOUR>
+template <typename T, bool NEIGHBOUR>
 __device__ __forceinline__ void load_weight(const NormRopeWeight &g, const Lane &ln, float (&f)[16]) {
-  if (g.bf16) {
-    Row<__nv_bfloat16> r;
-    r.load(static_cast<const __nv_bfloat16 *>(g.ptr), ln);
-    r.get<NEIGHBOUR>(f);
-  } else {
-    Row<float> r;
-    r.load(static_cast<const float *>(g.ptr), ln);
-    r.get<NEIGHBOUR>(f);
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const int e = element<T, NEIGHBOUR>(ln, k);
+    f[k] = g.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(g.ptr)[e]) : static_cast<const float *>(g.ptr)[e];
   }
 }
 
@@ -218,11 +214,13 @@ __device__ __forceinline__ void put_angles(int lane, int rot, int p, const unsig
   __syncwarp();
 }
 // The lane's own out of it; elements that do not rotate get (1, 0).
-__device__ __forceinline__ void take_angles(Angles &an, const Lane &ln, const float2 *table) {
+template <typename T, bool NEIGHBOUR>
+__device__ __forceinline__ void take_angles(Angles &an, const Lane &ln, int rot, const float2 *table) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     float4 cs = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
-    if (ln.on) cs = *reinterpret_cast<const float4 *>(table + ln.f + 2 * k);
+    const int e = element<T, NEIGHBOUR>(ln, 2 * k);  // pairs 2k and 2k + 1 have frequencies side by side
+    if (ln.at < rot) cs = *reinterpret_cast<const float4 *>(table + (NEIGHBOUR ? e / 2 : e));
     an.c[2 * k] = cs.x;
     an.s[2 * k] = cs.y;
     an.c[2 * k + 1] = cs.z;
@@ -339,17 +337,17 @@ __device__ __forceinline__ uint32_t walk_start() { return blockIdx.x * WARPS + (
 // place made up half of the instructions when every batch computed its own).
 template <typename T>
 struct Cursor {
-  T *p;          // the lane's row of the next pass
+  T *p;          // the lane's first part in its row of the next pass
   int64_t pass;  // elements to the next pass
   int left;      // rows below the side's last, from the lane's on
   int batches;   // of this side, from here to the end of the run
 };
 template <typename T, int D>
 __device__ __forceinline__ void aim(Cursor<T> &c, const NormRopeSide &x, int64_t off, int heads, int j, int batches,
-                                    int passes, int lane) {
+                                    int passes, const Lane &ln, int lane) {
   constexpr int RPW = rows_per_pass<D>();
   const int h = j * passes * RPW + lane / (D / EPL);
-  c.p = static_cast<T *>(x.ptr) + off + h * x.s_head;
+  c.p = static_cast<T *>(x.ptr) + off + h * x.s_head + ln.at;
   c.pass = RPW * x.s_head;
   c.left = heads - h;
   c.batches = batches;
@@ -361,7 +359,7 @@ __device__ __forceinline__ void fetch_rows(uint32_t slot, Cursor<T> &c, const La
   constexpr int RPW = rows_per_pass<D>();
 #pragma unroll
   for (int u = 0; u < U; ++u, c.p += c.pass)
-    if (c.left > u * RPW) Row<T>::fetch(slot + u * pass_bytes<T>() + lane * 16, c.p, ln);
+    if (c.left > u * RPW) Row<T>::fetch(slot + u * pass_bytes<T>() + lane * 16, c.p, ln.step);
   c.left -= U * RPW;
 }
 
@@ -380,7 +378,7 @@ __device__ __forceinline__ void fwd_batch(const uint8_t *slot, Cursor<T> &c, flo
     float f[16];
     x.template get<NEIGHBOUR>(f);
     fwd_row<D>(f, eps, turn);
-    if (c.left > u * RPW) Row<T>::template store<NEIGHBOUR>(c.p, ln, f);
+    if (c.left > u * RPW) Row<T>::template store<NEIGHBOUR>(c.p, ln.step, f);
   }
   c.left -= U * RPW;
 }
@@ -390,22 +388,22 @@ __device__ __forceinline__ void fwd_batch(const uint8_t *slot, Cursor<T> &c, flo
 struct Weights {
   float g[2][16][8];  // [side][k][lane of a row]
 };
-template <int D, bool NEIGHBOUR>
+template <typename T, int D, bool NEIGHBOUR>
 __device__ __forceinline__ void put_weights(Weights &w, const NormRopeWeight &gq, const NormRopeWeight &gk, int rot) {
   constexpr int LPR = D / EPL;
   if ((int)threadIdx.x < 2 * LPR) {
     const int side = threadIdx.x / LPR, l = threadIdx.x % LPR;
     float g[16];
-    load_weight<NEIGHBOUR>(side ? gk : gq, lane_of<D, NEIGHBOUR>(l, rot), g);
+    load_weight<T, NEIGHBOUR>(side ? gk : gq, lane_of<T, D>(l, rot), g);
 #pragma unroll
     for (int k = 0; k < 16; ++k) w.g[side][k][l] = g[k];
   }
 }
-template <int D>
-__device__ __forceinline__ void turn_for(Turn &t, const Weights &w, int side, const Lane &ln, const float2 *table,
+template <typename T, int D, bool NEIGHBOUR>
+__device__ __forceinline__ void turn_for(Turn &t, const Weights &w, int side, const Lane &ln, int rot, const float2 *table,
                                          int lane) {
   Angles an;
-  take_angles(an, ln, table);
+  take_angles<T, NEIGHBOUR>(an, ln, rot, table);
   float g[16];
 #pragma unroll
   for (int k = 0; k < 16; ++k) g[k] = w.g[side][k][lane % (D / EPL)];
@@ -420,7 +418,7 @@ __global__ void __launch_bounds__(THREADS, 5) norm_rope_kernel(const NormRopeArg
   __shared__ Weights weights;
   __shared__ __align__(16) uint8_t ring[WARPS][STAGES][BYTES];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const Lane ln = lane_of<D, NEIGHBOUR>(lane, a.rot);
+  const Lane ln = lane_of<T, D>(lane, a.rot);
   Walk ahead, now;
   walk_to(ahead, pl, (uint32_t)a.tokens, walk_start());
   now = ahead;
@@ -430,7 +428,7 @@ __global__ void __launch_bounds__(THREADS, 5) norm_rope_kernel(const NormRopeArg
     const bool key = w.j >= pl.bq;
     const NormRopeSide &x = key ? k : q;
     aim<T, D>(c, x, token_off(x, w.t, (int)a.n), key ? a.Hkv : a.H, key ? w.j - pl.bq : w.j,
-              (key ? w.j1 : min(w.j1, pl.bq)) - w.j, U, lane);
+              (key ? w.j1 : min(w.j1, pl.bq)) - w.j, U, ln, lane);
   };
   Cursor<T> in, out;
   in.batches = out.batches = 0;
@@ -447,7 +445,7 @@ __global__ void __launch_bounds__(THREADS, 5) norm_rope_kernel(const NormRopeArg
 #pragma unroll
   for (int i = 0; i < STAGES - 1; ++i) fetch();
   for (int f = threadIdx.x; f < a.rot / 2; f += THREADS) turns[f] = turns_per_position(__ldg(a.inv_freq + f));
-  put_weights<D, NEIGHBOUR>(weights, a.gq, a.gk, a.rot);
+  put_weights<T, D, NEIGHBOUR>(weights, a.gq, a.gk, a.rot);
   __syncthreads();
   Turn turn;
   int of = -1;  // the token of `table`
@@ -460,7 +458,7 @@ __global__ void __launch_bounds__(THREADS, 5) norm_rope_kernel(const NormRopeArg
         put_angles(lane, a.rot, p, turns, table[warp]);
         of = now.t;
       }
-      turn_for<D>(turn, weights, now.j >= pl.bq, ln, table[warp], lane);
+      turn_for<T, D, NEIGHBOUR>(turn, weights, now.j >= pl.bq, ln, a.rot, table[warp], lane);
     }
     --out.batches;
     wait_async<STAGES - 1>();
@@ -503,7 +501,7 @@ __device__ __forceinline__ void bwd_side(const NormRopeArgs &a, const NormRopeSi
   constexpr int LPR = D / EPL, RPW = rows_per_pass<D>();
   constexpr int STAGES = bwd_stages<T>(), U = bwd_passes<T>(), BYTES = U * pass_bytes<T>();  // of x, and of dy
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / LPR;
-  const Lane ln = lane_of<D, NEIGHBOUR>(lane, a.rot);
+  const Lane ln = lane_of<T, D>(lane, a.rot);
   Walk ahead, now;
   walk_to(ahead, pl, (uint32_t)a.tokens, walk_start());
   now = ahead;
@@ -511,7 +509,7 @@ __device__ __forceinline__ void bwd_side(const NormRopeArgs &a, const NormRopeSi
   Cursor<T> in_x, in_dy, out;
   in_x.batches = in_dy.batches = out.batches = 0;
   auto aim_at = [&](Cursor<T> &c, const Walk &w, const NormRopeSide &s) {
-    aim<T, D>(c, s, token_off(s, w.t, (int)a.n), heads, w.j, w.j1 - w.j, U, lane);
+    aim<T, D>(c, s, token_off(s, w.t, (int)a.n), heads, w.j, w.j1 - w.j, U, ln, lane);
   };
   auto fetch = [&]() {
     if (ahead.t >= 0) {
@@ -521,6 +519,7 @@ __device__ __forceinline__ void bwd_side(const NormRopeArgs &a, const NormRopeSi
       }
       --in_x.batches;
       const uint32_t slot = smem_u32(ring) + put * 2 * BYTES;
+      in_dy.left = in_x.left;  // one register for both
       fetch_rows<T, D, U>(slot, in_x, ln, lane);
       fetch_rows<T, D, U>(slot + BYTES, in_dy, ln, lane);
       walk_on(ahead, pl, (uint32_t)a.tokens);
@@ -533,7 +532,7 @@ __device__ __forceinline__ void bwd_side(const NormRopeArgs &a, const NormRopeSi
   float g[16], dg[16];
 #pragma unroll
   for (int k = 0; k < 16; ++k) dg[k] = 0.0f;
-  load_weight<NEIGHBOUR>(weight, ln, g);
+  load_weight<T, NEIGHBOUR>(weight, ln, g);
   Angles an;
   int of = -1;  // the token of `an`
   while (now.t >= 0) {
@@ -543,7 +542,7 @@ __device__ __forceinline__ void bwd_side(const NormRopeArgs &a, const NormRopeSi
       if (now.t != of) {
         const int p = a.positions ? __ldg(a.positions + now.t) : now.t % (int)a.n;
         put_angles(lane, a.rot, p, turns, table);
-        take_angles(an, ln, table);
+        take_angles<T, NEIGHBOUR>(an, ln, a.rot, table);
         of = now.t;
       }
     }
@@ -565,7 +564,7 @@ __device__ __forceinline__ void bwd_side(const NormRopeArgs &a, const NormRopeSi
         r.template get<NEIGHBOUR>(v);
       }
       bwd_row<D>(f, v, g, dg, a.eps, an);
-      if (out.left > u * RPW) Row<T>::template store<NEIGHBOUR>(out.p, ln, f);
+      if (out.left > u * RPW) Row<T>::template store<NEIGHBOUR>(out.p, ln.step, f);
     }
     out.left -= U * RPW;
     walk_on(now, pl, (uint32_t)a.tokens);
@@ -578,8 +577,7 @@ __device__ __forceinline__ void bwd_side(const NormRopeArgs &a, const NormRopeSi
     float v = dg[k];
 #pragma unroll
     for (int o = LPR; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    const int i = NEIGHBOUR ? ln.a + 2 * (k % 8) + k / 8 : (k < 8 ? ln.a : ln.b - 8) + k;
-    if (lane < LPR) sums[warp][i] = v;
+    if (lane < LPR) sums[warp][element<T, NEIGHBOUR>(ln, k)] = v;
   }
   __syncthreads();
   for (int i = threadIdx.x; i < D; i += THREADS) {
@@ -706,7 +704,7 @@ __global__ void __launch_bounds__(THREADS, 4) norm_append_kernel(const AppendArg
   __shared__ Weights weights;
   __shared__ __align__(16) uint8_t ring[WARPS][STAGES][BYTES];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const Lane ln = lane_of<D, NEIGHBOUR>(lane, a.rot);
+  const Lane ln = lane_of<T, D>(lane, a.rot);
   Walk ahead, now;
   walk_to(ahead, pl, (uint32_t)a.tokens, walk_start());
   now = ahead;
@@ -726,7 +724,7 @@ __global__ void __launch_bounds__(THREADS, 4) norm_append_kernel(const AppendArg
         int from, to;
         const int side = side_of(ahead, from, to);
         const NormRopeSide &x = side == 0 ? a.q : (side == 1 ? a.k : a.v);
-        aim<T, D>(in, x, ahead.t * x.s_tok, side ? a.Hkv : a.H, ahead.j - from, to - ahead.j, U, lane);
+        aim<T, D>(in, x, ahead.t * x.s_tok, side ? a.Hkv : a.H, ahead.j - from, to - ahead.j, U, ln, lane);
       }
       --in.batches;
       fetch_rows<T, D, U>(smem_u32(ring[warp][put]), in, ln, lane);
@@ -738,7 +736,7 @@ __global__ void __launch_bounds__(THREADS, 4) norm_append_kernel(const AppendArg
 #pragma unroll
   for (int i = 0; i < STAGES - 1; ++i) fetch();
   for (int f = threadIdx.x; f < a.rot / 2; f += THREADS) turns[f] = turns_per_position(__ldg(a.inv_freq + f));
-  put_weights<D, NEIGHBOUR>(weights, a.gq, a.gk, a.rot);
+  put_weights<T, D, NEIGHBOUR>(weights, a.gq, a.gk, a.rot);
   __syncthreads();
   Turn turn;
   Spot sp = {0, 0, 0, 0, 0};
@@ -760,8 +758,8 @@ __global__ void __launch_bounds__(THREADS, 4) norm_append_kernel(const AppendArg
         y.s_head = side == 1 ? a.kc.s_head : a.vc.s_head;
         off = side == 1 ? sp.k : sp.v;
       }
-      aim<T, D>(out, y, off, (side ? sp.ok : sp.in) ? (side ? a.Hkv : a.H) : 0, now.j - from, to - now.j, U, lane);
-      if (side < 2) turn_for<D>(turn, weights, side, ln, table[warp], lane);
+      aim<T, D>(out, y, off, (side ? sp.ok : sp.in) ? (side ? a.Hkv : a.H) : 0, now.j - from, to - now.j, U, ln, lane);
+      if (side < 2) turn_for<T, D, NEIGHBOUR>(turn, weights, side, ln, a.rot, table[warp], lane);
     }
     --out.batches;
     wait_async<STAGES - 1>();
@@ -774,8 +772,8 @@ __global__ void __launch_bounds__(THREADS, 4) norm_append_kernel(const AppendArg
         if (out.left > u * RPW) {
           Row<T> r;
           r.take(slot + u * pass_bytes<T>() + lane * 16);
-          *reinterpret_cast<uint4 *>(out.p + ln.a) = r.a;
-          *reinterpret_cast<uint4 *>(out.p + ln.b) = r.b;
+          *reinterpret_cast<uint4 *>(out.p) = r.a;
+          *reinterpret_cast<uint4 *>(out.p + ln.step) = r.b;
         }
       out.left -= U * RPW;
     }
