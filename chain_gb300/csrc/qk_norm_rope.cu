@@ -132,6 +132,10 @@ struct Row;
 template <>
 struct Row<__nv_bfloat16> {
   uint4 a, b;
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p, int step) {
+    a = *reinterpret_cast<const uint4 *>(p);
+    b = *reinterpret_cast<const uint4 *>(p + step);
+  }
   static __device__ __forceinline__ void fetch(uint32_t slot, const __nv_bfloat16 *p, int step) {
     copy_async(slot, p);
     copy_async(slot + 512, p + step);
@@ -164,6 +168,10 @@ struct Row<__nv_bfloat16> {
 template <>
 struct Row<float> {
   float4 v[4];
+  __device__ __forceinline__ void load(const float *p, int step) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const float4 *>(p + k * step);
+  }
   static __device__ __forceinline__ void fetch(uint32_t slot, const float *p, int step) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) copy_async(slot + 512 * k, p + k * step);
@@ -193,6 +201,12 @@ struct Row<float> {
 
 template <typename T, bool NEIGHBOUR>
 __device__ __forceinline__ void load_weight(const NormRopeWeight &g, const Lane &ln, float (&f)[16]) {
+  if ((g.bf16 != 0) == (sizeof(T) == 2)) {  // of the heads' type: part by part
+    Row<T> r;
+    r.load(static_cast<const T *>(g.ptr) + ln.at, ln.step);
+    r.template get<NEIGHBOUR>(f);
+    return;
+  }
 #pragma unroll
   for (int k = 0; k < 16; ++k) {
     const int e = element<T, NEIGHBOUR>(ln, k);
