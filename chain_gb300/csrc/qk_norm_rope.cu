@@ -304,14 +304,18 @@ __device__ __forceinline__ void fwd_row(float (&f)[16], float eps, const Turn &t
 // The rows of the next STAGES - 1 batches are on their way, by asynchronous
 // copies into shared memory, while a batch is worked on.  Every lane copies
 // the very bytes that it will read, so nothing but its own copies is waited for.
-constexpr int STAGES = 3;
+// No more bytes in flight than hide the latency: beyond that the memory serves them worse.
+// At d = 128, bf16, a warp's one pass of 1 KB with five blocks an SM makes 20 KB an SM (40 heads
+// x 32,768 tokens, forward: 105 us; four blocks 112, six 109; two passes or a third stage 120).
+// At d = 64 a token's angles serve half as many bytes, and two passes hide that
+// arithmetic better (60,011 tokens of 32 heads: 86 us, 92 with one).
+constexpr int STAGES = 2;
+constexpr int FWD_BLOCKS = 5, BWD_BLOCKS = kNormRopeBwdMaxGrid / SMS;  // an SM
 
-template <typename T>
-constexpr int fwd_passes() { return sizeof(T) == 2 ? 2 : 1; }  // U: 2 KB a batch
+template <typename T, int D>
+constexpr int fwd_passes() { return sizeof(T) == 2 && D == 64 ? 2 : 1; }  // U
 template <typename T>
 constexpr int bwd_passes() { return 1; }  // of x and of dy
-template <typename T>
-constexpr int bwd_stages() { return sizeof(T) == 2 ? 4 : 2; }
 template <typename T>
 constexpr int pass_bytes() { return 32 * EPL * (int)sizeof(T); }
 template <int D>
@@ -425,8 +429,8 @@ __device__ __forceinline__ void turn_for(Turn &t, const Weights &w, int side, co
 }
 
 template <typename T, int D, bool NEIGHBOUR>
-__global__ void __launch_bounds__(THREADS, 5) norm_rope_kernel(const NormRopeArgs a, const Plan pl) {
-  constexpr int U = fwd_passes<T>(), B = U * rows_per_pass<D>(), BYTES = U * pass_bytes<T>();
+__global__ void __launch_bounds__(THREADS, FWD_BLOCKS) norm_rope_kernel(const NormRopeArgs a, const Plan pl) {
+  constexpr int U = fwd_passes<T, D>(), BYTES = U * pass_bytes<T>();
   __shared__ unsigned long long turns[MAX_FREQ];
   __shared__ __align__(16) float2 table[WARPS][MAX_FREQ];
   __shared__ Weights weights;
@@ -513,7 +517,7 @@ __device__ __forceinline__ void bwd_side(const NormRopeArgs &a, const NormRopeSi
                                          const Plan &pl, const unsigned long long *turns, float2 *table,
                                          uint8_t *ring, float (*sums)[D], float *part) {
   constexpr int LPR = D / EPL, RPW = rows_per_pass<D>();
-  constexpr int STAGES = bwd_stages<T>(), U = bwd_passes<T>(), BYTES = U * pass_bytes<T>();  // of x, and of dy
+  constexpr int U = bwd_passes<T>(), BYTES = U * pass_bytes<T>();  // of x, and of dy
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / LPR;
   const Lane ln = lane_of<T, D>(lane, a.rot);
   Walk ahead, now;
@@ -608,13 +612,13 @@ __device__ __forceinline__ void bwd_side(const NormRopeArgs &a, const NormRopeSi
 // sum has one order.  Queries first, then keys: a weight and its sums take 16
 // registers, and holding both sides' at once would cost a third of the warps.
 template <typename T, int D, bool NEIGHBOUR>
-__global__ void __launch_bounds__(THREADS, 4) norm_rope_bwd_kernel(const NormRopeBwdArgs b, const Plan plq,
+__global__ void __launch_bounds__(THREADS, BWD_BLOCKS) norm_rope_bwd_kernel(const NormRopeBwdArgs b, const Plan plq,
                                                                    const Plan plk, float *__restrict__ part) {
   constexpr int BYTES = bwd_passes<T>() * pass_bytes<T>();
   __shared__ unsigned long long turns[MAX_FREQ];
   __shared__ __align__(16) float2 table[WARPS][MAX_FREQ];
   __shared__ float sums[WARPS][D];
-  __shared__ __align__(16) uint8_t ring[WARPS][bwd_stages<T>() * 2 * BYTES];
+  __shared__ __align__(16) uint8_t ring[WARPS][STAGES * 2 * BYTES];
   const NormRopeArgs &a = b.fwd;
   const int warp = threadIdx.x >> 5;
   pdl_launch_dependents();  // the sums over blocks may be launched; they wait for this grid
@@ -710,9 +714,9 @@ __device__ __forceinline__ Spot spot_of(const AppendArgs &a, int t, int lane) {
 // Q normed, rotated and written to qo, K normed, rotated and written into its
 // page, V copied into its page.
 template <int D, bool NEIGHBOUR>
-__global__ void __launch_bounds__(THREADS, 4) norm_append_kernel(const AppendArgs a, const Plan pl) {
+__global__ void __launch_bounds__(THREADS, FWD_BLOCKS) norm_append_kernel(const AppendArgs a, const Plan pl) {
   using T = __nv_bfloat16;
-  constexpr int RPW = rows_per_pass<D>(), U = fwd_passes<T>(), B = U * RPW, BYTES = U * pass_bytes<T>();
+  constexpr int RPW = rows_per_pass<D>(), U = fwd_passes<T, D>(), BYTES = U * pass_bytes<T>();
   __shared__ unsigned long long turns[MAX_FREQ];
   __shared__ __align__(16) float2 table[WARPS][MAX_FREQ];
   __shared__ Weights weights;
@@ -831,9 +835,9 @@ int batches_of(int heads, int b) { return (heads + b - 1) / b; }
 
 template <typename T, int D, bool NEIGHBOUR>
 cudaError_t launch_fwd(const NormRopeArgs &a, cudaStream_t st) {
-  constexpr int B = fwd_passes<T>() * rows_per_pass<D>();
+  constexpr int B = fwd_passes<T, D>() * rows_per_pass<D>();
   const Plan pl = plan(a.tokens, batches_of(a.H, B), batches_of(a.Hkv, B), 0);
-  norm_rope_kernel<T, D, NEIGHBOUR><<<blocks_for(a.tokens, pl, 5), THREADS, 0, st>>>(a, pl);
+  norm_rope_kernel<T, D, NEIGHBOUR><<<blocks_for(a.tokens, pl, FWD_BLOCKS), THREADS, 0, st>>>(a, pl);
   return cudaGetLastError();
 }
 
@@ -845,7 +849,7 @@ cudaError_t launch_bwd(const NormRopeBwdArgs &b, cudaStream_t st) {
   if (b.fwd.tokens > 0) {
     const Plan plq = plan(b.fwd.tokens, batches_of(b.fwd.H, B), 0, 0);
     const Plan plk = plan(b.fwd.tokens, batches_of(b.fwd.Hkv, B), 0, 0);
-    blocks = blocks_for(b.fwd.tokens, plq, kNormRopeBwdMaxGrid / SMS);
+    blocks = blocks_for(b.fwd.tokens, plq, BWD_BLOCKS);
     norm_rope_bwd_kernel<T, D, NEIGHBOUR><<<blocks, THREADS, 0, st>>>(b, plq, plk, part);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
@@ -864,10 +868,10 @@ cudaError_t launch_bwd(const NormRopeBwdArgs &b, cudaStream_t st) {
 
 template <int D>
 cudaError_t launch_app(const AppendArgs &a, cudaStream_t st) {
-  constexpr int B = fwd_passes<__nv_bfloat16>() * rows_per_pass<D>();
+  constexpr int B = fwd_passes<__nv_bfloat16, D>() * rows_per_pass<D>();
   const int kv = batches_of(a.Hkv, B);
   const Plan pl = a.norm ? plan(a.tokens, batches_of(a.H, B), kv, kv) : plan(a.tokens, 1, 0, 0);
-  const unsigned blocks = blocks_for(a.tokens, pl, a.norm ? 4 : 16);
+  const unsigned blocks = blocks_for(a.tokens, pl, a.norm ? FWD_BLOCKS : 16);
   if (!a.norm)
     append_kernel<D><<<blocks, THREADS, 0, st>>>(a);
   else if (a.neighbour)
