@@ -629,25 +629,37 @@ __global__ void __launch_bounds__(THREADS, BWD_BLOCKS) norm_rope_bwd_kernel(cons
   bwd_side<T, D, NEIGHBOUR>(a, a.k, b.dko, a.ko, a.gk, a.Hkv, plk, turns, table[warp], ring[warp], sums, part + D);
 }
 
-// dgq, dgk [D] from the blocks' sums: one block for 32 of the 2 D columns,
-// warp w adding the blocks w, w + 32, ...  (With four warps its 150 dependent loads
-// took longer than the gradients of a short batch.)
-constexpr int DG_WARPS = 32;
+// dgq, dgk [D] from the blocks' sums: a block for 8 of the 2 D columns, its warps
+// four blocks' sums each at a time, all loaded at once.  (A block for 32 columns, a warp a
+// row, read them in rounds of dependent loads.)
+constexpr int DG_WARPS = 32, DG_COLS = 8, DG_ROWS = 32 / DG_COLS * DG_WARPS;
 __global__ void __launch_bounds__(32 * DG_WARPS) norm_rope_dg_kernel(const float *__restrict__ part, int blocks,
                                                                      int d, float *__restrict__ dgq,
                                                                      float *__restrict__ dgk) {
-  __shared__ float sums[DG_WARPS][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
-  float s = 0.0f;
+  constexpr int LOADS = (kNormRopeBwdMaxGrid + DG_ROWS - 1) / DG_ROWS;
+  __shared__ float sums[DG_WARPS][DG_COLS];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = warp * (32 / DG_COLS) + lane / DG_COLS, col = blockIdx.x * DG_COLS + lane % DG_COLS;
   pdl_wait();
-#pragma unroll 8
-  for (int i = warp; i < blocks; i += DG_WARPS) s += part[(int64_t)i * 2 * d + col];
-  sums[warp][lane] = s;
+  float v[LOADS], s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < LOADS; ++i) {
+    const int r = row + i * DG_ROWS;
+    v[i] = r < blocks ? part[(int64_t)r * 2 * d + col] : 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < LOADS; ++i) s += v[i];
+#pragma unroll
+  for (int o = DG_COLS; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane < DG_COLS) sums[warp][lane] = s;
   __syncthreads();
   if (warp == 0) {
+    s = 0.0f;
 #pragma unroll
-    for (int w = 1; w < DG_WARPS; ++w) s += sums[w][lane];
-    (col < d ? dgq : dgk - d)[col] = s;
+    for (int w = 0; w < DG_WARPS; w += 32 / DG_COLS) s += sums[w + lane / DG_COLS][lane % DG_COLS];
+#pragma unroll
+    for (int o = DG_COLS; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane < DG_COLS) (col < d ? dgq : dgk - d)[col] = s;
   }
 }
 
@@ -855,7 +867,7 @@ cudaError_t launch_bwd(const NormRopeBwdArgs &b, cudaStream_t st) {
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * D / 32);
+  cfg.gridDim = dim3(2 * D / DG_COLS);
   cfg.blockDim = dim3(32 * DG_WARPS);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
