@@ -127,7 +127,8 @@ struct Layout {
 
 struct Params {
   PagedSeqs s;
-  int total, G, Hkv, tpt, causal;
+  int total, G, Hkv, causal;
+  int tpt, utok;               // tokens of a query tile, of a unit
   int cost1, cost2, overhead;  // of a key tile against one and two query tiles, of a unit
   float scale_log2;
   __nv_bfloat16 *O;
@@ -137,6 +138,10 @@ struct Params {
   float *part_o;   // [CTAS][2][D / 4][2 BM][4]
   float2 *part_ml; // [CTAS][2][2 BM]
   Boundary *bounds;
+  // for the kernel of few rows, which makes its own copies
+  const __nv_bfloat16 *Q;
+  int64_t q_stok, q_shead;
+  PagedSide kc, vc;
   WaitCfg wc;
 };
 
@@ -208,14 +213,14 @@ __device__ __forceinline__ int tiles_to(const Params &p, const Seq &s, int end) 
 }
 
 __device__ __forceinline__ int units_of(const Params &p, const Seq &s) {
-  return (s.n + 2 * p.tpt - 1) / (2 * p.tpt);
+  return (s.n + p.utok - 1) / p.utok;
 }
 
 // Cost of a unit: its key tiles, and `overhead` for its start and end.
 __device__ __forceinline__ int tile_cost(const Params &p, int ntok) { return ntok > p.tpt ? p.cost2 : p.cost1; }
 __device__ __forceinline__ long long unit_cost(const Params &p, const Seq &s, int q) {
-  const int i0 = q * 2 * p.tpt;
-  return p.overhead + (long long)tile_cost(p, s.n - i0) * tiles_to(p, s, i0 + 2 * p.tpt);
+  const int i0 = q * p.utok;
+  return p.overhead + (long long)tile_cost(p, s.n - i0) * tiles_to(p, s, i0 + p.utok);
 }
 // 64-bit division takes hundreds of cycles and is hardly ever needed
 __device__ __forceinline__ long long quotient(long long a, long long b) {
@@ -283,7 +288,87 @@ __device__ __forceinline__ Place locate(const Params &p, const long long *sums, 
   return at;
 }
 
-__device__ __forceinline__ long long run_start(long long total, int cta) { return total * cta / CTAS; }
+template <int RUNS>
+__device__ __forceinline__ long long run_start(long long total, int cta) {
+  return total * cta / RUNS;
+}
+
+// A block's run: what is left of it, and where it goes on.
+struct Run {
+  long long t, t1;  // cost offsets into all of the work
+  Place at;
+  Seq s;
+};
+
+// A warp finds where the block's run begins, writes its boundary, and says whether
+// there is anything in it.
+template <int RUNS>
+__device__ __forceinline__ bool begin_run(const Params &p, const long long *sums, Run &r, int lane) {
+  long long total = 0;
+  for (int b = lane; b < p.s.batch; b += 32) total += sums[b];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  total *= p.Hkv;
+  r.t = run_start<RUNS>(total, blockIdx.x);
+  r.t1 = run_start<RUNS>(total, blockIdx.x + 1);
+  r.at = Place{0, 0, 0, 0};
+  r.s = Seq{0, 0, 0};
+  Boundary bd = {0, total, 0, 1, 0, 0, 0, 0};
+  bool work = false;
+  if (r.t < total) {
+    r.at = locate(p, sums, r.t, lane);
+    r.s = seq_of(p, r.at.b, false);
+    const int i0 = r.at.q * p.utok;
+    bd.u0 = r.t - r.at.off;
+    bd.nt = tiles_to(p, r.s, i0 + p.utok);
+    bd.w = tile_cost(p, r.s.n - i0);
+    bd.cut = tile_at(p, r.at.off, bd.w) > 0;
+    bd.tok0 = r.s.lo + i0;
+    bd.ntok = min(r.s.n - i0, p.utok);
+    bd.head = r.at.head;
+    // a run that ends before the first key tile that it reaches has nothing to do
+    const long long end = r.at.off + (r.t1 - r.t), cost = p.overhead + (long long)bd.w * bd.nt;
+    work = r.t < r.t1 && (end >= cost || tile_at(p, end, bd.w) > tile_at(p, r.at.off, bd.w));
+  }
+  if (lane == 0) p.bounds[blockIdx.x] = bd;
+  return work;
+}
+
+// The run's next unit; head = -1 at its end.
+__device__ __forceinline__ Unit next_of(const Params &p, Run &r) {
+  Unit u = {};
+  u.head = -1;
+  if (r.t < r.t1) {
+    const int i0 = r.at.q * p.utok, nt = tiles_to(p, r.s, i0 + p.utok);
+    const int w = tile_cost(p, r.s.n - i0);
+    const long long cost = p.overhead + (long long)w * nt, end = r.at.off + (r.t1 - r.t);
+    u.j0 = tile_at(p, r.at.off, w);
+    u.j1 = end >= cost ? nt : tile_at(p, end, w);
+    if (u.j1 > u.j0) {  // else the run ends before the unit's first key tile
+      u.tok0 = r.s.lo + i0;
+      u.ntok = min(r.s.n - i0, p.utok);
+      u.head = r.at.head;
+      u.b = r.at.b;
+      u.ja = tiles_to(p, r.s, i0 + p.tpt);
+      u.lim0 = p.causal ? r.s.len - r.s.n + i0 + 1 : r.s.len;
+      u.len = r.s.len;
+      u.slot = u.j0 > 0 ? 0 : (u.j1 < nt ? 1 : -1);
+    }
+    r.t += cost - r.at.off;
+    // on to the next unit: of the head, the next head, the next sequence with new tokens
+    r.at.off = 0;
+    if (r.t < r.t1 && ++r.at.q == units_of(p, r.s)) {
+      r.at.q = 0;
+      if (++r.at.head == p.Hkv) {
+        r.at.head = 0;
+        do {
+          r.s = seq_of(p, ++r.at.b, false);
+        } while (r.s.n == 0 && r.at.b + 1 < p.s.batch);
+      }
+    }
+  }
+  return u;
+}
 
 // --------------------------------------------------------------- main kernel
 template <int D>
@@ -355,38 +440,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   pdl_launch_dependents();  // the join may be launched; it waits for this grid
 
   // The scheduler warp finds where the block's run begins.
-  long long t = 0, t1 = 0;  // the run
-  Place at = {0, 0, 0, 0};
-  Seq s = {0, 0, 0};
+  Run run;
   if (warp == 10) {
-    long long total = 0;
-    for (int b = lane; b < p.s.batch; b += 32) total += sums[b];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    total *= p.Hkv;
-    t = run_start(total, blockIdx.x);
-    t1 = run_start(total, blockIdx.x + 1);
-    Boundary bd = {0, total, 0, 1, 0, 0, 0, 0};
-    int work = 0;
-    if (t < total) {
-      at = locate(p, sums, t, lane);
-      s = seq_of(p, at.b, false);
-      const int i0 = at.q * 2 * p.tpt;
-      bd.u0 = t - at.off;
-      bd.nt = tiles_to(p, s, i0 + 2 * p.tpt);
-      bd.w = tile_cost(p, s.n - i0);
-      bd.cut = tile_at(p, at.off, bd.w) > 0;
-      bd.tok0 = s.lo + i0;
-      bd.ntok = min(s.n - i0, 2 * p.tpt);
-      bd.head = at.head;
-      // a run that ends before the first key tile that it reaches has nothing to do
-      const long long end = at.off + (t1 - t), cost = p.overhead + (long long)bd.w * bd.nt;
-      work = t < t1 && (end >= cost || tile_at(p, end, bd.w) > tile_at(p, at.off, bd.w));
-    }
-    if (lane == 0) {
-      p.bounds[blockIdx.x] = bd;
-      *has_work = work;
-    }
+    const bool work = begin_run<CTAS>(p, sums, run, lane);
+    if (lane == 0) *has_work = work;
   }
   __syncthreads();
   if (!*has_work) {
@@ -416,37 +473,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     int k = 0;
     bool ok = true;
     while (true) {
-      Unit u = {};
-      u.head = -1;
-      if (t < t1) {
-        const int i0 = at.q * 2 * p.tpt, nt = tiles_to(p, s, i0 + 2 * p.tpt);
-        const int w = tile_cost(p, s.n - i0);
-        const long long cost = p.overhead + (long long)w * nt, end = at.off + (t1 - t);
-        u.j0 = tile_at(p, at.off, w);
-        u.j1 = end >= cost ? nt : tile_at(p, end, w);
-        if (u.j1 > u.j0) {  // else the run ends before the unit's first key tile
-          u.tok0 = s.lo + i0;
-          u.ntok = min(s.n - i0, 2 * p.tpt);
-          u.head = at.head;
-          u.b = at.b;
-          u.ja = tiles_to(p, s, i0 + p.tpt);
-          u.lim0 = p.causal ? s.len - s.n + i0 + 1 : s.len;
-          u.len = s.len;
-          u.slot = u.j0 > 0 ? 0 : (u.j1 < nt ? 1 : -1);
-        }
-        t += cost - at.off;
-        // on to the next unit: of the head, the next head, the next sequence with new tokens
-        at.off = 0;
-        if (t < t1 && ++at.q == units_of(p, s)) {
-          at.q = 0;
-          if (++at.head == p.Hkv) {
-            at.head = 0;
-            do {
-              s = seq_of(p, ++at.b, false);
-            } while (s.n == 0 && at.b + 1 < p.s.batch);
-          }
-        }
-      }
+      const Unit u = next_of(p, run);
       const int sl = k % NU;
       if (k >= NU) ok = mbar_wait_warp(&u_empty[sl], ((k / NU) - 1) & 1, p.wc, abort_flag, SITE_PAGED_SCHED);
       if (!ok) break;
@@ -920,12 +947,300 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
+// ------------------------------------------------------------------- few rows
+// Single tokens, whose G query heads fill a few of a query tile's 128 rows.  There the
+// kernel above waits: one warp of four has rows, each lane exponentiates a row's 128 keys
+// one after another, and a key tile's chain of copies, products and softmax, some 4,000
+// cycles, shows wherever a unit has few tiles.  Here a tile has 16 rows, the least that a
+// warp's own products take (mma.sync: with this few rows the work is memory's, and the tensor
+// core's rate does not matter), and eight warps an SM work for themselves: a warp takes 32 of a tile's
+// 128 keys, copies them, keeps its own running (m, l, O), and the block joins its four
+// warps' at the end of a unit.  Units, runs and partial results are those of the
+// kernel above.
+constexpr int TOK_ROWS = 16;
+template <int D, int WARPS>
+struct TokenLayout {
+  static constexpr int BLOCKS = 8 / WARPS, RUNS = CTAS * BLOCKS;
+  static constexpr int KEYS = BN / WARPS;                       // of a key tile, a warp's
+  static constexpr int KS = KEYS < 2048 / D ? KEYS : 2048 / D;  // of a stage: 8 KB of K and V at most
+  static constexpr int STAGES = 2;
+  static constexpr uint32_t HALF = KS * D * 2, STAGE = 2 * HALF;
+  static constexpr uint32_t WARP = STAGES * STAGE;  // a warp's ring; then its share of O
+  static constexpr uint32_t ALLOC = WARPS * WARP;
+  static constexpr int OPITCH = D + 4;
+  static constexpr int COST = 4, OVERHEAD = D == 128 ? 4 : 8;
+  static_assert(MAX_BATCH * 8 <= ALLOC, "the schedule's sums use the rings");
+  static_assert(TOK_ROWS * OPITCH * 4 <= WARP, "O in the ring");
+  static_assert(KEYS % KS == 0 && KS % 16 == 0, "keys");
+};
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+// c [16][8] += a [16][16] b [16][8]
+__device__ __forceinline__ void mma_16x8x16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// 16 bytes into shared memory, or zeros
+__device__ __forceinline__ void copy_or_zero(uint32_t dst, const void *src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+
+template <int D, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, TokenLayout<D, WARPS>::BLOCKS) paged_token_kernel(const Params p) {
+  using L = TokenLayout<D, WARPS>;
+  constexpr int CH = D / 8;             // 16-byte chunks of a row
+  constexpr int RPC = 32 / CH;          // rows that a copy of the warp covers
+  constexpr int PER = L::KEYS / L::KS;  // stages of a key tile
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Unit next;
+  __shared__ float2 ml[WARPS][TOK_ROWS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  long long *sums = reinterpret_cast<long long *>(smem_raw);
+  for (int b = threadIdx.x; b < p.s.batch; b += 32 * WARPS) sums[b] = head_cost(p, seq_of(p, b, blockIdx.x == 0));
+  __syncthreads();
+  pdl_launch_dependents();  // the join may be launched; it waits for this grid
+  Run run;
+  if (warp == 0) begin_run<L::RUNS>(p, sums, run, lane);
+  const uint32_t ring = smem_u32(smem_raw) + warp * L::WARP;
+  const int page = 1 << p.s.page_shift, pool = (int)p.s.num_pages;
+  while (true) {
+    if (warp == 0) {
+      const Unit u = next_of(p, run);
+      if (lane == 0) next = u;
+    }
+    __syncthreads();
+    const Unit u = next;
+    if (u.head < 0) break;
+    const int steps = (u.j1 - u.j0) * PER;
+    const int *table = p.s.table + u.b * p.s.table_stride;
+    const __nv_bfloat16 *kc = static_cast<const __nv_bfloat16 *>(p.kc.ptr) + u.head * p.kc.s_head;
+    const __nv_bfloat16 *vc = static_cast<const __nv_bfloat16 *>(p.vc.ptr) + u.head * p.vc.s_head;
+    auto first_key = [&](int i) { return (u.j0 + i / PER) * BN + warp * L::KEYS + i % PER * L::KS; };
+    // page numbers of a stage's keys (KS <= 32 and pages of 16 at least: two at most), looked up one stage ahead
+    int ids[2];
+    auto look_up = [&](int i) {
+#pragma unroll
+      for (int h = 0; h < L::KS / 16; ++h) {
+        const int pos = first_key(i) + 16 * h;
+        ids[h] = i < steps && pos < u.len ? __ldg(table + (pos >> p.s.page_shift)) : pool;
+      }
+    };
+    auto fetch = [&](int i) {
+      if (i < steps) {
+        const int base = first_key(i);
+        const uint32_t at = ring + i % L::STAGES * L::STAGE;
+#pragma unroll
+        for (int h = 0; h < L::KS / 16; ++h) {  // 16 positions lie in one page
+          const int pos = base + 16 * h, id = ids[h];
+          const bool known = id >= 0 && id < pool;
+          if (pos < u.len && !known && lane == 0) atomicExch(&p.wc.status->reserved[0], 1);
+          const int left = known ? u.len - pos : 0, r0 = lane / CH, c = lane % CH;
+          const int64_t slot = left > 0 ? pos & (page - 1) : 0, pg = left > 0 ? id : 0;
+          const __nv_bfloat16 *k = kc + pg * p.kc.s_page + (slot + r0) * p.kc.s_slot + c * 8;
+          const __nv_bfloat16 *v = vc + pg * p.vc.s_page + (slot + r0) * p.vc.s_slot + c * 8;
+#pragma unroll
+          for (int it = 0; it < 16 / RPC; ++it) {
+            const int r = it * RPC + r0;
+            const uint32_t dst = at + (16 * h + r) * (D * 2) + ((c ^ (r & 7)) << 4);
+            copy_or_zero(dst, k, r < left);
+            copy_or_zero(dst + L::HALF, v, r < left);
+            k += RPC * p.kc.s_slot;
+            v += RPC * p.vc.s_slot;
+          }
+        }
+        look_up(i + 1);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    look_up(0);
+#pragma unroll
+    for (int i = 0; i < L::STAGES - 1; ++i) fetch(i);
+
+    // The lane's rows lane / 4 and lane / 4 + 8; Q in the products' layout
+    uint32_t q[D / 16][4];
+    int lim[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int row = lane / 4 + 8 * h, tok = row / p.G;
+      const bool valid = tok < u.ntok && tok < p.tpt;
+      lim[h] = valid ? (p.causal ? u.lim0 + tok : u.len) : 0;  // keys below it are seen
+      const __nv_bfloat16 *src =
+          p.Q + ((int64_t)u.tok0 + tok) * p.q_stok + ((int64_t)u.head * p.G + row - tok * p.G) * p.q_shead + lane % 4 * 2;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        q[kk][h] = valid ? *reinterpret_cast<const uint32_t *>(src + kk * 16) : 0u;
+        q[kk][2 + h] = valid ? *reinterpret_cast<const uint32_t *>(src + kk * 16 + 8) : 0u;
+      }
+    }
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, o[D / 8][4];
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[n][e] = 0.0f;
+
+    for (int i = 0; i < steps; ++i) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(L::STAGES - 2) : "memory");
+      __syncwarp();  // every lane's copies are there, and every lane has read the stage before
+      fetch(i + L::STAGES - 1);
+      const uint32_t at = ring + i % L::STAGES * L::STAGE;
+#pragma unroll
+      for (int g = 0; g < L::KS / 16; ++g) {
+        float s[2][4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
+        const int krow = g * 16 + (lane & 7) + (lane >> 4) * 8;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          uint32_t b[4];
+          ldmatrix4(b, at + krow * (D * 2) + (((kk * 2 + ((lane >> 3) & 1)) ^ (krow & 7)) << 4));
+          mma_16x8x16(s[0], q[kk], b[0], b[1]);
+          mma_16x8x16(s[1], q[kk], b[2], b[3]);
+        }
+        const int key = first_key(i) + g * 16 + lane % 4 * 2;
+        float alpha[2], ref[2];
+        bool moved = false;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float mx = -INFINITY;
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              if (key + n * 8 + e >= lim[h]) s[n][2 * h + e] = -INFINITY;
+              mx = fmaxf(mx, s[n][2 * h + e]);
+            }
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * p.scale_log2;
+          alpha[h] = 1.0f;
+          if (mx > m[h]) {
+            alpha[h] = ex2(m[h] - mx);
+            m[h] = mx;
+            moved = true;
+          }
+          ref[h] = m[h] == -INFINITY ? 0.0f : m[h];
+          l[h] *= alpha[h];
+        }
+        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[n][e] *= alpha[e >> 1];
+        }
+        // P = 2^(s scale log2e - m), rounded to bf16 for the second product; l sums it unrounded
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s[n][e] = ex2(fmaf(s[n][e], p.scale_log2, -ref[e >> 1]));
+            l[e >> 1] += s[n][e];
+          }
+        const uint32_t pa[4] = {pack_bf16(s[0][0], s[0][1]), pack_bf16(s[0][2], s[0][3]), pack_bf16(s[1][0], s[1][1]),
+                                pack_bf16(s[1][2], s[1][3])};
+        const int vrow = g * 16 + (lane & 15);
+#pragma unroll
+        for (int n = 0; n < D / 16; ++n) {
+          uint32_t b[4];
+          ldmatrix4_trans(b, at + L::HALF + vrow * (D * 2) + (((n * 2 + (lane >> 4)) ^ (vrow & 7)) << 4));
+          mma_16x8x16(o[2 * n], pa, b[0], b[1]);
+          mma_16x8x16(o[2 * n + 1], pa, b[2], b[3]);
+        }
+      }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncwarp();
+    // the warps' shares: O over the warp's own ring
+    float *mine = reinterpret_cast<float *>(smem_raw + warp * L::WARP);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int row = lane / 4 + 8 * h;
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+      if (lane % 4 == 0) ml[warp][row] = make_float2(m[h], l[h]);
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+        *reinterpret_cast<float2 *>(mine + row * L::OPITCH + n * 8 + lane % 4 * 2) =
+            make_float2(o[n][2 * h], o[n][2 * h + 1]);
+    }
+    __syncthreads();
+    {
+      constexpr int COLS = D / 8;  // a thread's, of row threadIdx.x / 8
+      const int row = threadIdx.x >> 3, c0 = (threadIdx.x & 7) * COLS, tok = row / p.G;
+      if (row < TOK_ROWS && tok < u.ntok && tok < p.tpt) {
+        float top = -INFINITY, sum = 0.0f, x[COLS];
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) top = fmaxf(top, ml[w][row].x);
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) x[c] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+          const float2 v = ml[w][row];
+          const float f = v.x == -INFINITY ? 0.0f : ex2(v.x - top);
+          sum = fmaf(v.y, f, sum);
+          const float4 *src =
+              reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(smem_raw + w * L::WARP) + row * L::OPITCH + c0);
+#pragma unroll
+          for (int c = 0; c < COLS / 4; ++c) {
+            const float4 y = src[c];
+            x[4 * c] = fmaf(y.x, f, x[4 * c]);
+            x[4 * c + 1] = fmaf(y.y, f, x[4 * c + 1]);
+            x[4 * c + 2] = fmaf(y.z, f, x[4 * c + 2]);
+            x[4 * c + 3] = fmaf(y.w, f, x[4 * c + 3]);
+          }
+        }
+        if (u.slot < 0) {
+          const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+          const int64_t qhead = (int64_t)u.head * p.G + row - tok * p.G;
+          uint4 *dst = reinterpret_cast<uint4 *>(p.O + ((int64_t)u.tok0 + tok) * p.o_stok + qhead * p.o_shead + c0);
+#pragma unroll
+          for (int c = 0; c < COLS / 8; ++c)
+            dst[c] = make_uint4(pack_bf16(x[8 * c] * inv, x[8 * c + 1] * inv), pack_bf16(x[8 * c + 2] * inv, x[8 * c + 3] * inv),
+                                pack_bf16(x[8 * c + 4] * inv, x[8 * c + 5] * inv),
+                                pack_bf16(x[8 * c + 6] * inv, x[8 * c + 7] * inv));
+          if ((threadIdx.x & 7) == 0)
+            p.LSE[qhead * p.lse_shead + u.tok0 + tok] =
+                sum > 0.0f ? (top + lg2(sum)) * 0.69314718055994531f : -INFINITY;
+        } else {
+          const int64_t slot = (int64_t)blockIdx.x * 2 + u.slot;
+          float4 *dst = reinterpret_cast<float4 *>(p.part_o) + slot * (TOK_ROWS * D / 4) + row;
+#pragma unroll
+          for (int c = 0; c < COLS / 4; ++c)
+            dst[(c0 / 4 + c) * TOK_ROWS] = make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+          if ((threadIdx.x & 7) == 0) p.part_ml[slot * TOK_ROWS + row] = make_float2(top, sum);
+        }
+      }
+    }
+    __syncthreads();  // the rings, ml and `next` are free
+  }
+}
+
+// Whether a call's rows are few: with a query head's group that fits 16 rows, no more new
+// tokens than sequences, or so few that they fit one tile.  (A sequence with more tokens than a
+// tile, in such a call, is served by several units, which read its keys once each.)
+bool few_rows(const PagedAttnArgs &a, int G) {
+  return G <= TOK_ROWS && (a.total <= a.seqs.batch || a.total * G <= TOK_ROWS);
+}
+
 // Joins a unit that runs' ends cut into parts: block (c, y) the unit that
 // boundary c + 1 falls into, if that is the unit's first boundary.  A block takes
 // `ROWS` rows and a warp D / 8 columns of them; a lane takes a row, as in the
 // parts, and every GROUPS-th part of it, PB loaded at once: the kernel is a
 // few dependent loads long.  Rows go out through shared memory.
-template <int D, int ROWS>
+template <int D, int RUNS, int SLOT, int ROWS>
 __device__ __forceinline__ void combine_rows(const Params &p, const Boundary &bd, int c, int first_row,
                                              uint2 (*rows)[D / 4 + 1]) {
   constexpr int Q = D / 32, PB = 2, GROUPS = 32 / ROWS;  // Q: float4 a lane
@@ -940,7 +1255,7 @@ __device__ __forceinline__ void combine_rows(const Params &p, const Boundary &bd
   // block c - 1 holds the first part, as its last unit; the next blocks the others, as
   // their first, down to the one that holds the unit's last key tile
   const long long end = bd.u0 + p.overhead + (long long)bd.w * bd.nt;
-  auto begins = [&](int k) { return k < CTAS && run_start(bd.total, k) < end; };
+  auto begins = [&](int k) { return k < RUNS && run_start<RUNS>(bd.total, k) < end; };
   // Where a lane takes many parts, one after another, their end is found first (8 tokens over
   // 4,096 keys: 26.3 us -> 22.6); a single token's lanes take one or two (17.3 us, 16.6 without).
   int k1 = c - 1;
@@ -950,12 +1265,12 @@ __device__ __forceinline__ void combine_rows(const Params &p, const Boundary &bd
   }
   auto in_unit = [&](int k) { return ROWS == 32 ? k < k1 : begins(k); };
   // a run shorter than a key tile may hold none of it, and then no part
-  const bool tiny = bd.total < (long long)CTAS * (bd.w + 1);
+  const bool tiny = bd.total < (long long)RUNS * (bd.w + 1);
   auto has_part = [&](int k) {
     if (!in_unit(k)) return false;
     if (!tiny) return true;
-    const int j0 = tile_at(p, run_start(bd.total, k) - bd.u0, bd.w);
-    return run_start(bd.total, k + 1) >= end || tile_at(p, run_start(bd.total, k + 1) - bd.u0, bd.w) > j0;
+    const int j0 = tile_at(p, run_start<RUNS>(bd.total, k) - bd.u0, bd.w);
+    return run_start<RUNS>(bd.total, k + 1) >= end || tile_at(p, run_start<RUNS>(bd.total, k + 1) - bd.u0, bd.w) > j0;
   };
   for (int k0 = c - 1; in_unit(k0); k0 += PB * GROUPS) {
     float2 x[PB];
@@ -968,10 +1283,10 @@ __device__ __forceinline__ void combine_rows(const Params &p, const Boundary &bd
       for (int q = 0; q < Q; ++q) v[i][q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       if (valid && has_part(k)) {
         const int64_t slot = (int64_t)k * 2 + (k < c ? 1 : 0);
-        const float4 *po = reinterpret_cast<const float4 *>(p.part_o) + slot * (2 * BM * D / 4) + r;
-        x[i] = p.part_ml[slot * (2 * BM) + r];
+        const float4 *po = reinterpret_cast<const float4 *>(p.part_o) + slot * (SLOT * D / 4) + r;
+        x[i] = p.part_ml[slot * SLOT + r];
 #pragma unroll
-        for (int q = 0; q < Q; ++q) v[i][q] = po[(warp * Q + q) * (2 * BM)];
+        for (int q = 0; q < Q; ++q) v[i][q] = po[(warp * Q + q) * SLOT];
       }
     }
     float top = m;
@@ -1039,7 +1354,7 @@ __device__ __forceinline__ void combine_rows(const Params &p, const Boundary &bd
   }
 }
 
-template <int D>
+template <int D, int RUNS, int SLOT>
 __global__ void __launch_bounds__(256, 4) paged_combine_kernel(const Params p) {
   __shared__ uint2 rows[32][D / 4 + 1];
   pdl_wait();  // the parts and boundaries
@@ -1050,26 +1365,66 @@ __global__ void __launch_bounds__(256, 4) paged_combine_kernel(const Params p) {
   // no row of this block: those of a tile's tokens lie together from its first row on
   const int tok = bd.ntok - (y * 32 / BM) * p.tpt;
   if ((y * 32) % BM >= min(tok, p.tpt) * p.G) return;
-  if (tile_at(p, run_start(bd.total, c - 1) - bd.u0, bd.w) > 0) return;
+  if (tile_at(p, run_start<RUNS>(bd.total, c - 1) - bd.u0, bd.w) > 0) return;
   // a single token's few rows, over many blocks' parts: the parts are shared out among lanes
   if (bd.ntok * p.G <= 8)
-    combine_rows<D, 8>(p, bd, c, 0, rows);
+    combine_rows<D, RUNS, SLOT, 8>(p, bd, c, 0, rows);
   else
-    combine_rows<D, 32>(p, bd, c, y * 32, rows);
+    combine_rows<D, RUNS, SLOT, 32>(p, bd, c, y * 32, rows);
 }
 
 size_t part_bytes(int d) { return (size_t)CTAS * 2 * 2 * BM * d * sizeof(float); }
 size_t ml_bytes() { return (size_t)CTAS * 2 * 2 * BM * sizeof(float2); }
 
+// Behind the kernel that made the parts: a boundary is a block's, 32 rows of it at a time.
+template <int D, int RUNS, int SLOT>
+cudaError_t launch_join(const PagedAttnArgs &a, const Params &p, cudaStream_t st) {
+  // no sequence is longer than a key tile: no unit is cut
+  if (((int64_t)a.seqs.max_pages << a.seqs.page_shift) <= BN) return cudaSuccess;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(RUNS - 1, SLOT < 32 ? 1 : SLOT / 32);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_combine_kernel<D, RUNS, SLOT>, p);
+}
+
+template <int D, int WARPS>
+cudaError_t launch_tokens(const PagedAttnArgs &a, Params &p, cudaStream_t st) {
+  using L = TokenLayout<D, WARPS>;
+  p.tpt = p.utok = TOK_ROWS / p.G;
+  p.cost1 = p.cost2 = L::COST;
+  p.overhead = L::OVERHEAD;
+  uint8_t *ws = static_cast<uint8_t *>(a.workspace);
+  constexpr size_t SLOTS = (size_t)L::RUNS * 2 * TOK_ROWS;
+  static_assert(SLOTS * (D * 4 + 8) + L::RUNS * sizeof(Boundary) <= (size_t)CTAS * 4 * BM * D * 4, "workspace");
+  p.part_o = reinterpret_cast<float *>(ws);
+  p.part_ml = reinterpret_cast<float2 *>(ws + SLOTS * D * 4);
+  p.bounds = reinterpret_cast<Boundary *>(ws + SLOTS * (D * 4 + 8));
+  auto kernel = paged_token_kernel<D, WARPS>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC);
+  if (e != cudaSuccess) return e;
+  timing_mark(st, 0);
+  kernel<<<L::RUNS, 32 * WARPS, L::ALLOC, st>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  timing_mark(st, 1);
+  return launch_join<D, L::RUNS, TOK_ROWS>(a, p, st);
+}
+
 template <int D>
 cudaError_t launch(const PagedAttnArgs &a, const WaitCfg &wc, cudaStream_t st) {
   using L = Layout<D>;
-  Params p;
+  Params p = {};
   p.s = a.seqs;
   p.total = a.total;
   p.G = a.H / a.Hkv;
   p.Hkv = a.Hkv;
   p.tpt = BM / p.G;
+  p.utok = 2 * p.tpt;
   p.causal = a.causal;
   p.cost1 = L::COST1;
   p.cost2 = L::COST2;
@@ -1085,6 +1440,13 @@ cudaError_t launch(const PagedAttnArgs &a, const WaitCfg &wc, cudaStream_t st) {
   p.part_ml = reinterpret_cast<float2 *>(ws + part_bytes(D));
   p.bounds = reinterpret_cast<Boundary *>(ws + part_bytes(D) + ml_bytes());
   p.wc = wc;
+  p.Q = static_cast<const __nv_bfloat16 *>(a.Q);
+  p.q_stok = a.q_stok;
+  p.q_shead = a.q_shead;
+  p.kc = a.kc;
+  p.vc = a.vc;
+  if (few_rows(a, p.G))
+    return (int64_t)a.seqs.batch * p.Hkv <= CTAS ? launch_tokens<D, 8>(a, p, st) : launch_tokens<D, 4>(a, p, st);
   // Q: {d, head, token}, a tile's box G heads of TPT tokens.  Strides of
   // extents of one are not given: any valid value does.
   CUtensorMap mq, mk, mv;
@@ -1116,18 +1478,7 @@ cudaError_t launch(const PagedAttnArgs &a, const WaitCfg &wc, cudaStream_t st) {
   paged_attn_kernel<D><<<CTAS, THREADS, L::ALLOC, st>>>(mq, mk, mv, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   timing_mark(st, 1);
-  // no sequence is longer than a key tile: no unit is cut
-  if (((int64_t)a.seqs.max_pages << a.seqs.page_shift) <= BN) return cudaSuccess;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(CTAS - 1, 2 * BM / 32);
-  cfg.blockDim = dim3(256);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_combine_kernel<D>, p);
+  return launch_join<D, CTAS, 2 * BM>(a, p, st);
 }
 
 }  // namespace
