@@ -212,3 +212,75 @@ def test_long(cg, name, causal):
     o, lse = cg.attention_fwd_paged(q.cuda(), c.kcd, c.vcd, *c.args, causal=causal)
     assert cg.chain_check()[0] == 0
     check(c, q, o, lse, causal, d ** -0.5)
+
+
+# calls with no more new tokens than sequences, or few rows in all: tiles of 16 rows
+FEW = {
+    "some tokens each": ([700, 0, 90, 5, 300], [3, 0, 2, 0, 0], 8, 2, 128, 16),
+    "all in one sequence": ([10, 2000, 9, 9, 9, 9, 9], [0, 7, 0, 0, 0, 0, 0], 6, 2, 64, 32),
+    "two tokens, cut": ([3000], [2], 8, 1, 128, 64),
+    "four tokens of one sequence, cut": ([1500], [4], 12, 3, 64, 16),
+    "sixteen rows, cut": ([2500], [1], 16, 1, 128, 64),
+    "group of 11": ([400, 1, 129], [1, 1, 1], 22, 2, 64, 16),
+    "group of 5, many units": ([33 * i + 1 for i in range(60)], [1] * 60, 15, 3, 128, 16),
+    "one head, many units": ([77 * i + 1 for i in range(40)], [1] * 40, 6, 6, 64, 64),
+    "more new than cached": ([1, 0, 300], [2, 1, 0], 4, 2, 128, 16),
+    "seventeen rows a token": ([500, 3], [1, 1], 17, 1, 128, 16),
+}
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("name", FEW)
+def test_few_rows(cg, name, causal):
+    lens, news, H, Hkv, d, page = FEW[name]
+    c = Cache(lens, news, Hkv, d, page, 140 + len(name), heads_first=len(name) % 2 == 0).fill().cuda()
+    q = cs.normal((c.total, H, d), 141)
+    o, lse = cg.attention_fwd_paged(q.cuda(), c.kcd, c.vcd, *c.args, causal=causal)
+    assert cg.chain_check()[0] == 0
+    check(c, q, o, lse, causal, d ** -0.5)
+
+
+def test_few_rows_strided_and_rows_behind_the_last_sequence(cg):
+    c = Cache([200, 90, 400], [1, 1, 0], 2, 128, 16, 151, pad_rows=1).fill().cuda()
+    H, d = 6, 128
+    qkv = cs.normal((c.total, H + 4, d), 152)
+    o = torch.full((c.total, 2 * H, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((H, c.total + 3), 9.0, device="cuda")
+    ws = torch.full((cg.chain_fwd_paged_workspace_size(qkv[:, :H], c.kcd),), 255, dtype=torch.uint8, device="cuda")
+    ov, lv = o[:, H:], lse[:, :c.total]
+    cg.chain_fwd_paged(qkv.cuda()[:, :H], c.kcd, c.vcd, *c.args, cg.MASK_CAUSAL, 0.3, ov, lv, ws)
+    assert cg.chain_check()[0] == 0
+    check(c, qkv[:, :H], ov, lv, True, 0.3)
+    n = int(c.cu[-1])
+    assert bool((o[:, :H] == 7).all()) and bool((o[n:] == 7).all()) and bool((lse[:, n:] == 9).all())
+
+
+def test_few_rows_large_scores(cg):
+    c = Cache([900], [1], 1, 128, 64, 153)
+    c.k[0] = (c.k[0].float() * torch.linspace(0.1, 20, 900)[:, None, None]).bfloat16()
+    c.fill().cuda()
+    q = cs.normal((1, 2, 128), 154) * 3
+    o, lse = cg.attention_fwd_paged(q.cuda(), c.kcd, c.vcd, *c.args, causal=True, scale=0.5)
+    assert cg.chain_check()[0] == 0
+    check(c, q, o, lse, True, 0.5)
+
+
+@pytest.mark.parametrize("news", [[1, 1], [30, 20]])
+def test_missing_pages_count_as_zeros(cg, news):
+    # on both sides of the choice of kernel: reported, not accessed; the other sequence is as without
+    c = Cache([300, 120], news, 2, 128, 16, 155).fill().cuda()
+    q = cs.normal((sum(news), 8, 128), 156).cuda()
+    ref, rl = cg.attention_fwd_paged(q, c.kcd, c.vcd, *c.args, causal=True)
+    good = c.tabled.clone()
+    for bad in (-1, c.kcd.shape[0], 2 ** 31 - 1):
+        c.tabled.copy_(good)
+        c.tabled[0, 3] = bad
+        o, lse = cg.attention_fwd_paged(q, c.kcd, c.vcd, *c.args, causal=True)
+        assert cg.chain_check()[0] == cg.ERR_ARG
+        n = news[0]
+        assert torch.equal(o[n:], ref[n:]) and torch.equal(lse[:, n:], rl[:, n:])
+        z = Cache([300], news[:1], 2, 128, 16, 157)
+        z.k, z.v = [c.k[0].clone()], [c.v[0].clone()]
+        z.k[0][48:64], z.v[0][48:64] = 0, 0
+        check(z, q[:n].cpu(), o[:n], lse[:, :n], True, 128 ** -0.5)
+    assert cg.chain_check()[0] == 0
