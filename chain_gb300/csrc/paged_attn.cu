@@ -38,18 +38,17 @@
 // query tiles over the same keys; with fewer (single tokens, short chunks) they are
 // its even and odd key tiles for one query tile, joined before the store.
 //
+// Calls of single tokens go to paged_token_kernel, further down, which shares the split.
+//
 // Bounds, and what was measured (32 heads on 8, pages of 64 to 128):
-//   single tokens: memory.  d = 128, 64 sequences of 8,192: 345 us, 2.15 GB at 6.2 TB/s;
-//   d = 64: 193 us, 1.07 GB at 5.6 TB/s, a key tile's chain of product, softmax and product
-//   showing beside half the bytes.  One sequence of 131,072: 100 us, 5.4 TB/s, 20 us of
-//   them the start, the join and the ends of 152 runs.
 //   chunks: the chain of softmax and products.  d = 128, 2,048 tokens over 32,768: 770 us,
 //   1,380 TFLOP/s, the tensor pipe 54% busy: a stream's softmax takes 2,000 cycles and its two
 //   products 1,500, and P shares S's columns, so that they follow each other; two
 //   streams overlap them.  d = 64: 550 us, 960 TFLOP/s, the tensor pipe 37% and the
 //   exponential unit 37% busy.
-//   one sequence of up to 128 keys: 10 us, latency: set-up 1.1, the schedule 1.3, page numbers
-//   and first copies 1.4, K and S 2.6, softmax and P V 1.9, the store 1.3.
+//   single tokens: memory.  d = 128, 64 sequences of 8,192: 360 us, 2.15 GB at 6.0 TB/s;
+//   d = 64: 197 us, 1.07 GB at 5.5 TB/s.  One sequence of 131,072: 102 us, 5.3 TB/s, with
+//   the start, the join and the ends of the runs; of 100: 6.3 us, all latency.
 #include "internal.h"
 
 namespace chain {
@@ -952,11 +951,12 @@ __global__ void __launch_bounds__(THREADS, 1)
 // kernel above waits: one warp of four has rows, each lane exponentiates a row's 128 keys
 // one after another, and a key tile's chain of copies, products and softmax, some 4,000
 // cycles, shows wherever a unit has few tiles.  Here a tile has 16 rows, the least that a
-// warp's own products take (mma.sync: with this few rows the work is memory's, and the tensor
-// core's rate does not matter), and eight warps an SM work for themselves: a warp takes 32 of a tile's
-// 128 keys, copies them, keeps its own running (m, l, O), and the block joins its four
-// warps' at the end of a unit.  Units, runs and partial results are those of the
-// kernel above.
+// warp's own products take (mma.sync: with this few rows the work is memory's, and the
+// tensor cores' rate does not matter), and eight warps an SM work for themselves: a warp
+// takes its share of a tile's 128 keys, copies them, keeps its own running (m, l, O), and the
+// block joins its warps' at the end of a unit.  Units, runs and partial results are those of
+// the kernel above.  Two stages of 8 KB a warp; a third, or more blocks, made the memory
+// slower (64 sequences of 16,384: 356 us with two stages, 374 with three).
 constexpr int TOK_ROWS = 16;
 template <int D, int WARPS>
 struct TokenLayout {
@@ -1229,8 +1229,13 @@ __global__ void __launch_bounds__(32 * WARPS, TokenLayout<D, WARPS>::BLOCKS) pag
 }
 
 // Whether a call's rows are few: with a query head's group that fits 16 rows, no more new
-// tokens than sequences, or so few that they fit one tile.  (A sequence with more tokens than a
-// tile, in such a call, is served by several units, which read its keys once each.)
+// tokens than sequences, or so few that they fit one tile.  (The counts themselves are on the
+// device.  A sequence with more tokens than a tile, in such a call, is served by several units,
+// which read its keys once each.)  Single tokens, 8 K/V heads, this kernel and the one above: 64
+// sequences of 300 at d = 64 17.5 us and 39.7; of 1,000 at d = 128 40 and 48 (40 sequences), of
+// 2,000 100 and 106, of 4,000 186 and 183, of 8,000 357 and 337, where only the memory is
+// left and the other kernel's larger copies serve it better.  One sequence of 100: 6.3 and 9.5, of
+// 4,096: 12.8 and 16.2, of 65,536: 56.8 and 58.8.
 bool few_rows(const PagedAttnArgs &a, int G) {
   return G <= TOK_ROWS && (a.total <= a.seqs.batch || a.total * G <= TOK_ROWS);
 }
@@ -1445,8 +1450,11 @@ cudaError_t launch(const PagedAttnArgs &a, const WaitCfg &wc, cudaStream_t st) {
   p.q_shead = a.q_shead;
   p.kc = a.kc;
   p.vc = a.vc;
+  // Few units are spread over the warps of one block an SM, more over two blocks, whose starts and
+  // ends overlap (1,000 keys a sequence, 8 K/V heads: 2 sequences 10.8 us, 13.5 with two blocks;
+  // 4 sequences 11.8 and 12.3; 8 15.6 and 14.2; 16 21.5 and 19.2)
   if (few_rows(a, p.G))
-    return (int64_t)a.seqs.batch * p.Hkv <= CTAS ? launch_tokens<D, 8>(a, p, st) : launch_tokens<D, 4>(a, p, st);
+    return (int64_t)a.seqs.batch * p.Hkv <= CTAS / 3 ? launch_tokens<D, 8>(a, p, st) : launch_tokens<D, 4>(a, p, st);
   // Q: {d, head, token}, a tile's box G heads of TPT tokens.  Strides of
   // extents of one are not given: any valid value does.
   CUtensorMap mq, mk, mv;
