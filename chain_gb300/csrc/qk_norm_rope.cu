@@ -315,7 +315,7 @@ __device__ __forceinline__ void fwd_row(float (&f)[16], float eps, const Turn &t
 // At d = 64 a token's angles serve half as many bytes, and two passes hide that
 // arithmetic better (60,011 tokens of 32 heads: 86 us, 92 with one).
 constexpr int STAGES = 2;
-constexpr int FWD_BLOCKS = 5, BWD_BLOCKS = kNormRopeBwdMaxGrid / SMS;  // an SM
+constexpr int FWD_BLOCKS = 5, BWD_BLOCKS = kNormRopeBwdMaxGrid / SMS, ROW_BLOCKS = 5;  // an SM
 
 template <typename T, int D>
 constexpr int fwd_passes() { return sizeof(T) == 2 && D == 64 ? 2 : 1; }  // U
@@ -351,6 +351,15 @@ __device__ __forceinline__ void walk_to(Walk &w, const Plan &pl, uint32_t tokens
 }
 __device__ __forceinline__ void walk_on(Walk &w, const Plan &pl, uint32_t tokens) {
   if (++w.j == w.j1) walk_to(w, pl, tokens, w.c + gridDim.x * WARPS);
+}
+
+__device__ __forceinline__ int position(const NormRopeArgs &a, int t) {
+  return a.positions ? __ldg(a.positions + t) : t % (int)a.n;
+}
+// The position of run c's token, looked up while the token before it is worked on
+__device__ __forceinline__ void look_ahead(int &p, const NormRopeArgs &a, const Plan &pl, uint32_t c) {
+  const uint32_t t = pl.chunks == 1 ? c : c / (uint32_t)pl.chunks;
+  if (t < (uint32_t)a.tokens) p = position(a, (int)t);
 }
 
 __device__ __forceinline__ uint32_t walk_start() { return blockIdx.x * WARPS + (threadIdx.x >> 5); }
@@ -472,14 +481,16 @@ __global__ void __launch_bounds__(THREADS, FWD_BLOCKS) norm_rope_kernel(const No
   __syncthreads();
   Turn turn;
   int of = -1;  // the token of `table`
+  int pos = 0;
+  look_ahead(pos, a, pl, now.c);
   while (now.t >= 0) {
     fetch();
     if (out.batches == 0) {
       aim_at(out, now, a.qo, a.ko);
       if (now.t != of) {
-        const int p = a.positions ? __ldg(a.positions + now.t) : now.t % (int)a.n;
-        put_angles(lane, a.rot, p, turns, table[warp]);
+        put_angles(lane, a.rot, pos, turns, table[warp]);
         of = now.t;
+        look_ahead(pos, a, pl, now.c + gridDim.x * WARPS);
       }
       turn_for<T, D, NEIGHBOUR>(turn, weights, now.j >= pl.bq, ln, a.rot, table[warp], lane);
     }
@@ -488,6 +499,69 @@ __global__ void __launch_bounds__(THREADS, FWD_BLOCKS) norm_rope_kernel(const No
     fwd_batch<T, D, NEIGHBOUR, U>(ring[warp][got], out, a.eps, turn, ln, lane);
     walk_on(now, pl, (uint32_t)a.tokens);
     got = got + 1 == STAGES ? 0 : got + 1;
+  }
+}
+
+// ------------------------------------------------------------------- few heads
+// With few heads a token's angles and addresses cost more than its rows.  There a pass
+// takes its 32 / (D / 16) rows from the row of all tokens' heads, each lane works out the
+// eight angles of its own row, and a warp takes passes of the queries first, then of the keys.
+template <typename T, int D>
+struct RowPass {
+  int t, h;    // the lane's token and head
+  bool there;
+  __device__ __forceinline__ void at(uint32_t pass, uint32_t tokens, uint32_t heads, int lane) {
+    const uint32_t row = pass * rows_per_pass<D>() + lane / (D / EPL), tok = row / heads;
+    t = (int)tok;
+    h = (int)(row - tok * heads);
+    there = tok < tokens;
+  }
+  __device__ __forceinline__ T *in(const NormRopeSide &x, int n, const Lane &ln) const {
+    return static_cast<T *>(x.ptr) + token_off(x, t, n) + h * x.s_head + ln.at;
+  }
+};
+template <typename T, bool NEIGHBOUR>
+__device__ __forceinline__ void own_angles(Angles &an, const Lane &ln, int rot, int p, const unsigned long long *turns) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int e = element<T, NEIGHBOUR>(ln, k);
+    float2 cs = make_float2(1.0f, 0.0f);
+    if (ln.at < rot) cs = angle(p, turns[NEIGHBOUR ? e / 2 : e]);
+    an.c[k] = cs.x;
+    an.s[k] = cs.y;
+  }
+}
+
+template <typename T, int D, bool NEIGHBOUR>
+__global__ void __launch_bounds__(THREADS, ROW_BLOCKS)
+    norm_rows_kernel(const NormRopeArgs a, const uint32_t qpasses, const uint32_t passes) {
+  __shared__ unsigned long long turns[MAX_FREQ];
+  const int lane = threadIdx.x & 31;
+  const Lane ln = lane_of<T, D>(lane, a.rot);
+  for (int f = threadIdx.x; f < a.rot / 2; f += THREADS) turns[f] = turns_per_position(__ldg(a.inv_freq + f));
+  __syncthreads();
+  float g[16];
+  int of = -1;  // the side of g
+  for (uint32_t pass = walk_start(); pass < passes; pass += gridDim.x * WARPS) {
+    const int side = pass >= qpasses;
+    RowPass<T, D> r;
+    r.at(side ? pass - qpasses : pass, (uint32_t)a.tokens, side ? a.Hkv : a.H, lane);
+    Row<T> x = {};
+    int p = 0;
+    if (r.there) {
+      x.load(r.in(side ? a.k : a.q, (int)a.n, ln), ln.step);
+      p = position(a, r.t);
+    }
+    if (side != of) load_weight<T, NEIGHBOUR>(side ? a.gk : a.gq, ln, g);
+    of = side;
+    Angles an;
+    own_angles<T, NEIGHBOUR>(an, ln, a.rot, p, turns);
+    Turn turn;
+    turn_of(turn, an, g);
+    float f[16];
+    x.template get<NEIGHBOUR>(f);
+    fwd_row<D>(f, a.eps, turn);
+    if (r.there) Row<T>::template store<NEIGHBOUR>(r.in(side ? a.ko : a.qo, (int)a.n, ln), ln.step, f);
   }
 }
 
@@ -514,6 +588,28 @@ __device__ __forceinline__ void bwd_row(float (&f)[16], float (&v)[16], const fl
   }
 }
 
+// The lanes' sums to the block's, in one order: rows of a warp, then warps of the block.
+template <typename T, int D, bool NEIGHBOUR>
+__device__ __forceinline__ void sum_block(const float (&dg)[16], const Lane &ln, float (*sums)[D], float *part) {
+  constexpr int LPR = D / EPL;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {  // firsts, then seconds
+    float v = dg[k];
+#pragma unroll
+    for (int o = LPR; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane < LPR) sums[warp][element<T, NEIGHBOUR>(ln, k)] = v;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < D; i += THREADS) {
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) s += sums[w][i];
+    part[i] = s;
+  }
+  __syncthreads();
+}
+
 // One side (queries or keys) of the backward: `heads` heads of every token;
 // the block's sum of a x r into part[D].
 template <typename T, int D, bool NEIGHBOUR>
@@ -523,7 +619,7 @@ __device__ __forceinline__ void bwd_side(const NormRopeArgs &a, const NormRopeSi
                                          uint8_t *ring, float (*sums)[D], float *part) {
   constexpr int LPR = D / EPL, RPW = rows_per_pass<D>();
   constexpr int U = bwd_passes<T>(), BYTES = U * pass_bytes<T>();  // of x, and of dy
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / LPR;
+  const int lane = threadIdx.x & 31, sub = lane / LPR;
   const Lane ln = lane_of<T, D>(lane, a.rot);
   Walk ahead, now;
   walk_to(ahead, pl, (uint32_t)a.tokens, walk_start());
@@ -558,13 +654,15 @@ __device__ __forceinline__ void bwd_side(const NormRopeArgs &a, const NormRopeSi
   load_weight<T, NEIGHBOUR>(weight, ln, g);
   Angles an;
   int of = -1;  // the token of `an`
+  int pos = 0;
+  look_ahead(pos, a, pl, now.c);
   while (now.t >= 0) {
     fetch();
     if (out.batches == 0) {
       aim_at(out, now, dx);
       if (now.t != of) {
-        const int p = a.positions ? __ldg(a.positions + now.t) : now.t % (int)a.n;
-        put_angles(lane, a.rot, p, turns, table);
+        put_angles(lane, a.rot, pos, turns, table);
+        look_ahead(pos, a, pl, now.c + gridDim.x * WARPS);
         take_angles<T, NEIGHBOUR>(an, ln, a.rot, table);
         of = now.t;
       }
@@ -594,28 +692,60 @@ __device__ __forceinline__ void bwd_side(const NormRopeArgs &a, const NormRopeSi
     got = got + 1 == STAGES ? 0 : got + 1;
   }
   wait_async<0>();
-  // rows of a warp, then warps of the block
+  sum_block<T, D, NEIGHBOUR>(dg, ln, sums, part);
+}
+
+// The same with few heads: passes over the rows of all tokens
+template <typename T, int D, bool NEIGHBOUR>
+__device__ __forceinline__ void bwd_rows(const NormRopeArgs &a, const NormRopeSide &x, const NormRopeSide &dy,
+                                         const NormRopeSide &dx, const NormRopeWeight &weight, int heads,
+                                         const unsigned long long *turns, float (*sums)[D], float *part) {
+  const int lane = threadIdx.x & 31;
+  const Lane ln = lane_of<T, D>(lane, a.rot);
+  float g[16], dg[16];
 #pragma unroll
-  for (int k = 0; k < 16; ++k) {  // firsts, then seconds
-    float v = dg[k];
-#pragma unroll
-    for (int o = LPR; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (lane < LPR) sums[warp][element<T, NEIGHBOUR>(ln, k)] = v;
+  for (int k = 0; k < 16; ++k) dg[k] = 0.0f;
+  load_weight<T, NEIGHBOUR>(weight, ln, g);
+  const uint32_t passes = ((uint32_t)a.tokens * heads + rows_per_pass<D>() - 1) / rows_per_pass<D>();
+  for (uint32_t pass = walk_start(); pass < passes; pass += gridDim.x * WARPS) {
+    RowPass<T, D> r;
+    r.at(pass, (uint32_t)a.tokens, heads, lane);
+    Row<T> xr = {}, dr = {};  // a row that is not there adds nothing to dg
+    int p = 0;
+    if (r.there) {
+      xr.load(r.in(x, (int)a.n, ln), ln.step);
+      dr.load(r.in(dy, (int)a.n, ln), ln.step);
+      p = position(a, r.t);
+    }
+    Angles an;
+    own_angles<T, NEIGHBOUR>(an, ln, a.rot, p, turns);
+    float f[16], v[16];
+    xr.template get<NEIGHBOUR>(f);
+    dr.template get<NEIGHBOUR>(v);
+    bwd_row<D>(f, v, g, dg, a.eps, an);
+    if (r.there) Row<T>::template store<NEIGHBOUR>(r.in(dx, (int)a.n, ln), ln.step, f);
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < D; i += THREADS) {
-    float s = 0.0f;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) s += sums[w][i];
-    part[i] = s;
-  }
-  __syncthreads();
+  sum_block<T, D, NEIGHBOUR>(dg, ln, sums, part);
 }
 
 // part[block][2][D]: the block's sums of a x r over its query rows and its
 // key rows.  No atomics: rows are dealt to warps by their number and every
 // sum has one order.  Queries first, then keys: a weight and its sums take 16
 // registers, and holding both sides' at once would cost a third of the warps.
+template <typename T, int D, bool NEIGHBOUR>
+__global__ void __launch_bounds__(THREADS, BWD_BLOCKS) norm_rows_bwd_kernel(const NormRopeBwdArgs b,
+                                                                            float *__restrict__ part) {
+  __shared__ unsigned long long turns[MAX_FREQ];
+  __shared__ float sums[WARPS][D];
+  const NormRopeArgs &a = b.fwd;
+  pdl_launch_dependents();
+  for (int f = threadIdx.x; f < a.rot / 2; f += THREADS) turns[f] = turns_per_position(__ldg(a.inv_freq + f));
+  __syncthreads();
+  part += (int64_t)blockIdx.x * 2 * D;
+  bwd_rows<T, D, NEIGHBOUR>(a, a.q, b.dqo, a.qo, a.gq, a.H, turns, sums, part);
+  bwd_rows<T, D, NEIGHBOUR>(a, a.k, b.dko, a.ko, a.gk, a.Hkv, turns, sums, part + D);
+}
+
 template <typename T, int D, bool NEIGHBOUR>
 __global__ void __launch_bounds__(THREADS, BWD_BLOCKS) norm_rope_bwd_kernel(const NormRopeBwdArgs b, const Plan plq,
                                                                    const Plan plk, float *__restrict__ part) {
@@ -850,8 +980,28 @@ unsigned blocks_for(int64_t tokens, const Plan &pl, int per_sm) {
 }
 int batches_of(int heads, int b) { return (heads + b - 1) / b; }
 
+// Few heads: a token's rows take no more bytes than this.  32,768 tokens of bf16, by tokens and by
+// rows: forward 32.9 us and 10.3 (1 + 1 heads of 64), 32.9 and 28.8 (5 + 5), 32.9 and 36.9
+// (8 + 4), 37 and 37 (4 + 2 of 128), 44 and 49 (6 + 2); backward 47 and 14 (1 + 1 of 64), 66
+// and 63 (6 + 2 of 128), 66 and 70 (8 + 1).
+constexpr int FEW_FWD = 1536, FEW_BWD = 2048;
+bool few_heads(const NormRopeArgs &a, int bytes) {
+  const int heads = a.H + a.Hkv;
+  return heads * a.d * (a.f32 ? 4 : 2) <= bytes && a.tokens * heads < (int64_t(1) << 31);
+}
+template <int D>
+uint32_t row_passes(int64_t tokens, int heads) {
+  return (uint32_t)((tokens * heads + rows_per_pass<D>() - 1) / rows_per_pass<D>());
+}
+
 template <typename T, int D, bool NEIGHBOUR>
 cudaError_t launch_fwd(const NormRopeArgs &a, cudaStream_t st) {
+  if (few_heads(a, FEW_FWD)) {
+    const uint32_t q = row_passes<D>(a.tokens, a.H), all = q + row_passes<D>(a.tokens, a.Hkv);
+    const unsigned blocks = min((all + WARPS - 1) / WARPS, (uint32_t)SMS * ROW_BLOCKS);
+    norm_rows_kernel<T, D, NEIGHBOUR><<<blocks, THREADS, 0, st>>>(a, q, all);
+    return cudaGetLastError();
+  }
   constexpr int B = fwd_passes<T, D>() * rows_per_pass<D>();
   const Plan pl = plan(a.tokens, batches_of(a.H, B), batches_of(a.Hkv, B), 0);
   norm_rope_kernel<T, D, NEIGHBOUR><<<blocks_for(a.tokens, pl, FWD_BLOCKS), THREADS, 0, st>>>(a, pl);
@@ -863,7 +1013,13 @@ cudaError_t launch_bwd(const NormRopeBwdArgs &b, cudaStream_t st) {
   constexpr int B = bwd_passes<T>() * rows_per_pass<D>();
   float *part = static_cast<float *>(b.workspace);
   unsigned blocks = 0;  // no tokens: no sums, dg = 0
-  if (b.fwd.tokens > 0) {
+  if (b.fwd.tokens > 0 && few_heads(b.fwd, FEW_BWD)) {
+    const uint32_t most = row_passes<D>(b.fwd.tokens, b.fwd.H > b.fwd.Hkv ? b.fwd.H : b.fwd.Hkv);
+    blocks = min((most + WARPS - 1) / WARPS, (uint32_t)kNormRopeBwdMaxGrid);
+    norm_rows_bwd_kernel<T, D, NEIGHBOUR><<<blocks, THREADS, 0, st>>>(b, part);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  } else if (b.fwd.tokens > 0) {
     const Plan plq = plan(b.fwd.tokens, batches_of(b.fwd.H, B), 0, 0);
     const Plan plk = plan(b.fwd.tokens, batches_of(b.fwd.Hkv, B), 0, 0);
     blocks = blocks_for(b.fwd.tokens, plq, BWD_BLOCKS);
