@@ -1237,7 +1237,7 @@ __global__ void __launch_bounds__(32 * WARPS, TokenLayout<D, WARPS>::BLOCKS) pag
 // left and the other kernel's larger copies serve it better.  One sequence of 100: 6.3 and 9.5, of
 // 4,096: 12.8 and 16.2, of 65,536: 56.8 and 58.8.
 bool few_rows(const PagedAttnArgs &a, int G) {
-  return G <= TOK_ROWS && (a.total <= a.seqs.batch || a.total * G <= TOK_ROWS);
+  return G <= TOK_ROWS && (a.total <= a.seqs.batch || (int64_t)a.total * G <= TOK_ROWS);
 }
 
 // Joins a unit that runs' ends cut into parts: block (c, y) the unit that

@@ -836,10 +836,9 @@ struct Spot {
   int64_t pos, k, v;
   int in, ok;  // in: it belongs to a sequence
 };
-__device__ __forceinline__ Spot spot_of(const AppendArgs &a, int t, int lane) {
+__device__ __forceinline__ Spot spot_in(const AppendArgs &a, int t, int b, bool report) {
   const PagedSeqs &s = a.seqs;
   Spot sp = {0, 0, 0, 0, 0};
-  const int b = sequence_of(s.cu, s.batch, t, lane);
   const int first = __ldg(s.cu + b), len = __ldg(s.lens + b);
   const int end = min(__ldg(s.cu + b + 1), (int)a.tokens);
   if (t < first || t >= end) return sp;  // a row behind the last sequence
@@ -849,7 +848,7 @@ __device__ __forceinline__ Spot spot_of(const AppendArgs &a, int t, int lane) {
   if (sp.pos >= 0 && sp.pos < ((int64_t)s.max_pages << s.page_shift))
     page = __ldg(s.table + b * s.table_stride + (sp.pos >> s.page_shift));
   if (page < 0 || page >= s.num_pages) {
-    if (lane == 0) atomicExch(&a.status->reserved[0], 1);
+    if (report) atomicExch(&a.status->reserved[0], 1);
     return sp;
   }
   const int64_t slot = sp.pos & ((1 << s.page_shift) - 1);
@@ -857,6 +856,21 @@ __device__ __forceinline__ Spot spot_of(const AppendArgs &a, int t, int lane) {
   sp.v = page * a.vc.s_page + slot * a.vc.s_slot;
   sp.ok = 1;
   return sp;
+}
+
+__device__ __forceinline__ Spot spot_of(const AppendArgs &a, int t, int lane) {
+  return spot_in(a, t, sequence_of(a.seqs.cu, a.seqs.batch, t, lane), lane == 0);
+}
+// The same for a lane's own token
+__device__ __forceinline__ Spot spot_of(const AppendArgs &a, int t) {
+  int b = 0;
+  for (int n = a.seqs.batch; n > 1;) {
+    const int half = n / 2;
+    const bool up = __ldg(a.seqs.cu + b + half) <= t;
+    b += up ? half : 0;
+    n = up ? n - half : half;
+  }
+  return spot_in(a, t, b, true);
 }
 
 // Q normed, rotated and written to qo, K normed, rotated and written into its
@@ -948,6 +962,53 @@ __global__ void __launch_bounds__(THREADS, FWD_BLOCKS) norm_append_kernel(const 
   }
 }
 
+// The same with few heads: passes over the rows of all tokens, queries, keys, then values.
+template <int D, bool NEIGHBOUR>
+__global__ void __launch_bounds__(THREADS, ROW_BLOCKS)
+    norm_append_rows_kernel(const AppendArgs a, const uint32_t qpasses, const uint32_t kpasses) {
+  using T = __nv_bfloat16;
+  __shared__ unsigned long long turns[MAX_FREQ];
+  const int lane = threadIdx.x & 31;
+  const Lane ln = lane_of<T, D>(lane, a.rot);
+  for (int f = threadIdx.x; f < a.rot / 2; f += THREADS) turns[f] = turns_per_position(__ldg(a.inv_freq + f));
+  __syncthreads();
+  float g[16];
+  int of = -1;  // the side of g
+  for (uint32_t pass = walk_start(); pass < qpasses + 2 * kpasses; pass += gridDim.x * WARPS) {
+    const int side = pass < qpasses ? 0 : (pass < qpasses + kpasses ? 1 : 2);
+    RowPass<T, D> r;
+    r.at(side == 0 ? pass : pass - qpasses - (side - 1) * kpasses, (uint32_t)a.tokens, side ? a.Hkv : a.H, lane);
+    Row<T> x = {};
+    Spot sp = {0, 0, 0, 0, 0};
+    if (r.there) {
+      const NormRopeSide &y = side == 0 ? a.q : (side == 1 ? a.k : a.v);
+      x.load(r.in(y, (int)a.tokens, ln), ln.step);
+      sp = spot_of(a, r.t);
+    }
+    T *out = r.in(a.qo, (int)a.tokens, ln);
+    if (side == 1) out = static_cast<T *>(a.kc.ptr) + sp.k + r.h * a.kc.s_head + ln.at;
+    if (side == 2) out = static_cast<T *>(a.vc.ptr) + sp.v + r.h * a.vc.s_head + ln.at;
+    const bool write = side == 0 ? sp.in : sp.ok;
+    if (side == 2) {
+      if (write) {
+        *reinterpret_cast<uint4 *>(out) = x.a;
+        *reinterpret_cast<uint4 *>(out + ln.step) = x.b;
+      }
+      continue;
+    }
+    if (side != of) load_weight<T, NEIGHBOUR>(side ? a.gk : a.gq, ln, g);
+    of = side;
+    Angles an;
+    own_angles<T, NEIGHBOUR>(an, ln, a.rot, (int)sp.pos, turns);
+    Turn turn;
+    turn_of(turn, an, g);
+    float f[16];
+    x.template get<NEIGHBOUR>(f);
+    fwd_row<D>(f, a.eps, turn);
+    if (write) Row<T>::template store<NEIGHBOUR>(out, ln.step, f);
+  }
+}
+
 // K and V copied into their pages, a token to a warp.
 template <int D>
 __global__ void __launch_bounds__(THREADS) append_kernel(const AppendArgs a) {
@@ -984,11 +1045,14 @@ int batches_of(int heads, int b) { return (heads + b - 1) / b; }
 // Few heads: a token's rows take no more bytes than this.  32,768 tokens of bf16, by tokens and by
 // rows: forward 32.9 us and 10.3 (1 + 1 heads of 64), 32.9 and 28.8 (5 + 5), 32.9 and 36.9
 // (8 + 4), 37 and 37 (4 + 2 of 128), 44 and 49 (6 + 2); backward 47 and 14 (1 + 1 of 64), 66
-// and 63 (6 + 2 of 128), 66 and 70 (8 + 1).
-constexpr int FEW_FWD = 1536, FEW_BWD = 2048;
-bool few_heads(const NormRopeArgs &a, int bytes) {
-  const int heads = a.H + a.Hkv;
-  return heads * a.d * (a.f32 ? 4 : 2) <= bytes && a.tokens * heads < (int64_t(1) << 31);
+// and 63 (6 + 2 of 128), 66 and 70 (8 + 1).  Into the cache, with the values: 16 prompts of 18,600
+// tokens in all, 28.8 and 24.7 (8 + 2 of 64), 32.5 and 24.7 (4 + 1 of 128), 37 and 41 (8 + 1).
+constexpr int FEW_FWD = 1536, FEW_BWD = 2048, FEW_APPEND = 2048;
+bool few_heads(int64_t tokens, int heads, int head_bytes, int most) {
+  return (int64_t)heads * head_bytes <= most && tokens * heads < (int64_t(1) << 31);
+}
+bool few_heads(const NormRopeArgs &a, int most) {
+  return few_heads(a.tokens, a.H + a.Hkv, a.d * (a.f32 ? 4 : 2), most);
 }
 template <int D>
 uint32_t row_passes(int64_t tokens, int heads) {
@@ -1043,6 +1107,15 @@ cudaError_t launch_bwd(const NormRopeBwdArgs &b, cudaStream_t st) {
 template <int D>
 cudaError_t launch_app(const AppendArgs &a, cudaStream_t st) {
   constexpr int B = fwd_passes<__nv_bfloat16, D>() * rows_per_pass<D>();
+  if (a.norm && few_heads(a.tokens, a.H + 2 * a.Hkv, D * 2, FEW_APPEND)) {
+    const uint32_t q = row_passes<D>(a.tokens, a.H), k = row_passes<D>(a.tokens, a.Hkv);
+    const unsigned n = min((q + 2 * k + WARPS - 1) / WARPS, (uint32_t)SMS * ROW_BLOCKS);
+    if (a.neighbour)
+      norm_append_rows_kernel<D, true><<<n, THREADS, 0, st>>>(a, q, k);
+    else
+      norm_append_rows_kernel<D, false><<<n, THREADS, 0, st>>>(a, q, k);
+    return cudaGetLastError();
+  }
   const int kv = batches_of(a.Hkv, B);
   const Plan pl = a.norm ? plan(a.tokens, batches_of(a.H, B), kv, kv) : plan(a.tokens, 1, 0, 0);
   const unsigned blocks = blocks_for(a.tokens, pl, a.norm ? FWD_BLOCKS : 16);

@@ -284,3 +284,39 @@ def test_missing_pages_count_as_zeros(cg, news):
         z.k[0][48:64], z.v[0][48:64] = 0, 0
         check(z, q[:n].cpu(), o[:n], lse[:, :n], True, 128 ** -0.5)
     assert cg.chain_check()[0] == 0
+
+
+@pytest.mark.parametrize("H", [2, 20])
+def test_fused_write_with_missing_pages(cg, H):
+    # few heads and many: what cannot be written is reported and leaves the pools alone, its queries are still made
+    Hkv, d, page = 1, 128, 16
+    c = Cache([70, 33, 9], [40, 33, 2], Hkv, d, page, 161, pad_rows=2).cuda()
+    q, k, v = (cs.normal((c.total, h, d), 162 + h).cuda() for h in (H, Hkv, Hkv))
+    g, w = (1 + 0.1 * cs.normal((d,), 166, dtype=torch.float32)).cuda(), freqs(d).cuda()
+    good = [c.kc.cuda(), c.vc.cuda()]
+    qo = torch.full_like(q, 7.0)
+    call = lambda table, lens, pools, out: cg.chain_qk_norm_rope_append(q, k, v, g, g, w, EPS, 0, c.cud, lens, table,
+                                                                        *pools, out)
+    call(c.tabled, c.lensd, good, qo)
+    assert cg.chain_check()[0] == 0
+    assert bool((qo[int(c.cu[-1]):] == 7).all())
+    for bad in (-1, c.kc.shape[0], 2 ** 31 - 1):
+        t = c.tabled.clone()
+        lost = int(t[0, 3])  # positions 48 to 63 of the first sequence
+        t[0, 3] = bad
+        pools, out = [c.kc.cuda(), c.vc.cuda()], torch.full_like(q, 7.0)
+        call(t, c.lensd, pools, out)
+        assert cg.chain_check()[0] == cg.ERR_ARG
+        assert torch.equal(out, qo)
+        for a, b in zip(pools, good):
+            assert bool(torch.isnan(a[lost]).all())
+            a[lost] = b[lost]
+            assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+    # a length below the new tokens: those before position 0 are reported, the others land where they belong
+    pools = [c.kc.cuda(), c.vc.cuda()]
+    call(c.tabled, torch.tensor([70, 33, 1], dtype=torch.int32, device="cuda"), pools, torch.empty_like(q))
+    assert cg.chain_check()[0] == cg.ERR_ARG
+    page0, other = int(c.tabled[2, 0]), int(c.tabled[0, 4])
+    assert torch.isfinite(pools[0][page0, 0].float()).all() and torch.isnan(pools[0][page0, 1].float()).all()
+    assert torch.equal(pools[1][other].view(torch.int16), good[1][other].view(torch.int16))
+    assert cg.chain_check()[0] == 0
