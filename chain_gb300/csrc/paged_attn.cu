@@ -49,6 +49,8 @@
 //   single tokens: memory.  d = 128, 64 sequences of 8,192: 360 us, 2.15 GB at 6.0 TB/s;
 //   d = 64: 197 us, 1.07 GB at 5.5 TB/s.  One sequence of 131,072: 102 us, 5.3 TB/s, with
 //   the start, the join and the ends of the runs; of 100: 6.3 us, all latency.
+#include <atomic>
+
 #include "internal.h"
 
 namespace chain {
@@ -1411,8 +1413,15 @@ cudaError_t launch_tokens(const PagedAttnArgs &a, Params &p, cudaStream_t st) {
   p.part_ml = reinterpret_cast<float2 *>(ws + SLOTS * D * 4);
   p.bounds = reinterpret_cast<Boundary *>(ws + SLOTS * (D * 4 + 8));
   auto kernel = paged_token_kernel<D, WARPS>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC);
+  static std::atomic<uint64_t> allowed{0};  // devices on which the kernel has its shared memory
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(allowed.load(std::memory_order_relaxed) >> dev & 1)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) allowed.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+  }
   timing_mark(st, 0);
   kernel<<<L::RUNS, 32 * WARPS, L::ALLOC, st>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
