@@ -1143,7 +1143,8 @@ __global__ void __launch_bounds__(32 * WARPS, TokenLayout<D, WARPS>::BLOCKS) pag
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[n][e] *= alpha[e >> 1];
         }
-        // P = 2^(s scale log2e - m), rounded to bf16 for the second product; l sums it unrounded
+        // P = 2^(s scale log2e - m) as a pair of bf16, P_hi = bf16(P) and P_lo = bf16(P - P_hi): one bf16
+        // would add as much error to O as O's own rounding does.  l sums P unrounded.
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -1151,15 +1152,22 @@ __global__ void __launch_bounds__(32 * WARPS, TokenLayout<D, WARPS>::BLOCKS) pag
             s[n][e] = ex2(fmaf(s[n][e], p.scale_log2, -ref[e >> 1]));
             l[e >> 1] += s[n][e];
           }
-        const uint32_t pa[4] = {pack_bf16(s[0][0], s[0][1]), pack_bf16(s[0][2], s[0][3]), pack_bf16(s[1][0], s[1][1]),
-                                pack_bf16(s[1][2], s[1][3])};
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float p0 = s[e >> 1][2 * (e & 1)], p1 = s[e >> 1][2 * (e & 1) + 1];
+          hi[e] = pack_bf16(p0, p1);
+          lo[e] = pack_bf16(p0 - __uint_as_float(hi[e] << 16), p1 - __uint_as_float(hi[e] & 0xffff0000u));
+        }
         const int vrow = g * 16 + (lane & 15);
 #pragma unroll
         for (int n = 0; n < D / 16; ++n) {
           uint32_t b[4];
           ldmatrix4_trans(b, at + L::HALF + vrow * (D * 2) + (((n * 2 + (lane >> 4)) ^ (vrow & 7)) << 4));
-          mma_16x8x16(o[2 * n], pa, b[0], b[1]);
-          mma_16x8x16(o[2 * n + 1], pa, b[2], b[3]);
+          mma_16x8x16(o[2 * n], hi, b[0], b[1]);
+          mma_16x8x16(o[2 * n + 1], hi, b[2], b[3]);
+          mma_16x8x16(o[2 * n], lo, b[0], b[1]);
+          mma_16x8x16(o[2 * n + 1], lo, b[2], b[3]);
         }
       }
     }
