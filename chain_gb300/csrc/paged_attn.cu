@@ -452,16 +452,19 @@ __global__ void __launch_bounds__(THREADS, 1)
     return;
   }
 
-  // Every lane waits, and the warp goes on or gives up as one: what follows
-  // holds warp-wide instructions.
+  // The softmax warps' wait: every lane polls, since every lane reads tensor memory next, the warp goes
+  // on or gives up as one, and its lanes are together again before that access, which needs them so.
   auto warp_wait = [&](uint64_t *bar, uint32_t parity, int site) -> bool {
-    const bool ok = mbar_wait(bar, parity, p.wc, abort_flag, site);
-    return __all_sync(0xffffffffu, ok);
+    const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, p.wc, abort_flag, site));
+    __syncwarp();
+    return ok;
   };
-  // Reads the next unit; false when the run is done or a wait expired.
+  // Reads the next unit; false when the run is done or a wait expired.  Lane 0 polls: no vote
+  // in the producer and the issuers, whose lanes leave a poll at different times.
   auto next_unit = [&](int &k, Unit &u, int site) -> bool {
     const int s = k % NU;
-    if (!warp_wait(&u_full[s], (k / NU) & 1, site)) return false;
+    if (!mbar_wait_warp(&u_full[s], (k / NU) & 1, p.wc, abort_flag, site)) return false;
+    __syncwarp();  // what lane 0 saw, every lane may read
     u = *reinterpret_cast<const Unit *>(smem + L::OFF_UNITS + s * 48);
     __syncwarp();
     if (lane == 0) mbar_arrive(&u_empty[s]);
@@ -782,6 +785,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             m = mx;
             rescale = true;
           }
+          __syncwarp();  // the stores of P are the whole warp's
           const float mref = m == -INFINITY ? 0.0f : m;
           if (L::OWN_P && i > 0) {  // the product before this one has read P, and O holds it
             ok = warp_wait(&pv_done[t], (steps[t] + i - 1) & 1, SITE_PAGED_SOFTMAX);

@@ -1,0 +1,28 @@
+"""GPU: the 128-row kernel of attention over a paged cache where a block's warps pass from one
+unit of work to the next: many short units to a block, and units of one and of two query tiles in
+turn.  Against the definition in 64 bits, and bit for bit from call to call."""
+import pytest
+import torch
+
+import chain_synth as cs
+from test_gpu_paged import Cache, cg, check  # noqa: F401  (cg: the fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def run(cg, lens, news, H, Hkv, d, page, times=20):
+    assert sum(news) > len(news)  # not a call of single tokens
+    c = Cache(lens, news, Hkv, d, page, 900 + d).fill().cuda()
+    q = cs.normal((c.total, H, d), 11)
+    ref, rl = cg.attention_fwd_paged(q.cuda(), c.kcd, c.vcd, *c.args, causal=True)
+    assert cg.chain_check()[0] == 0
+    check(c, q, ref, rl, True, d ** -0.5)
+    for _ in range(times):
+        o, lse = cg.attention_fwd_paged(q.cuda(), c.kcd, c.vcd, *c.args, causal=True)
+        assert torch.equal(o, ref) and torch.equal(lse, rl)
+    assert cg.chain_check()[0] == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_units_to_a_block(cg, d):
+    run(cg, [1 + (37 * i) % 300 for i in range(400)], [1 + i % 2 for i in range(400)], 6, 3, d, 16)
