@@ -611,9 +611,14 @@ __global__ void __launch_bounds__(THREADS, 1)
       ns[0] = two ? max(0, min(u.ja, u.j1) - u.j0) : (n + 1) / 2;
       ns[1] = two ? n : n / 2;
       const int single = (int)qsel;  // the Q tile of a unit that has one
+      // An issuer waits for every copy of Q, also for the one that only the other issuer reads: a parity
+      // tells no more than whether the phase before the last is over, so with one left out the next
+      // unit's wait could be met by the phase before it and its products read Q too soon.
       for (int b = 0; b < 2; ++b)
-        if (two ? b >= first && b < end : b == single) ok = ok && wait(&q_full[b], q_uses[b] & 1);
-      for (int b = 0; b < 2; ++b) q_uses[b] += two || b == single;
+        if (two || b == single) {
+          ok = ok && wait(&q_full[b], q_uses[b] & 1);
+          ++q_uses[b];
+        }
       if (!two) qsel ^= 1;
       // Frees a buffer.  With one issuer the last product that reads it does; with two, one
       // arrival comes from each stream that reads it, both from a stream that reads it alone.

@@ -26,3 +26,11 @@ def run(cg, lens, news, H, Hkv, d, page, times=20):
 @pytest.mark.parametrize("d", [64, 128])
 def test_many_units_to_a_block(cg, d):
     run(cg, [1 + (37 * i) % 300 for i in range(400)], [1 + i % 2 for i in range(400)], 6, 3, d, 16)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page", [16, 128])
+def test_units_of_one_and_two_query_tiles_in_turn(cg, d, page):
+    # 32 tokens of four heads fill a query tile: a chunk of 33 to 64 takes two, a token one of the two buffers
+    news = [(1, 40, 3, 64, 33, 2, 1, 1, 50)[i % 9] for i in range(90)]
+    run(cg, [n + (53 * i) % 200 for i, n in enumerate(news)], news, 8, 2, d, page)
