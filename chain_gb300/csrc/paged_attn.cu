@@ -23,14 +23,15 @@
 // Inside a block (384 threads, one block an SM):
 //   warps 0-3, 4-7  softmax of streams 0 and 1, one row a thread, as in the
 //              forward kernels: S from tensor memory, running maximum and sum in
-//              fp32, P back into S's columns as bf16, O rescaled only when the
-//              maximum grew by 2^8.  P's rounding (2^-8 of each weight at
-//              most, unbiased) is below O's own once summed over keys, and one
-//              bf16 product costs half of a compensated pair; l sums the unrounded P.
+//              fp32, P back into S's columns as a pair of bf16, P_hi = bf16(P) and P_lo =
+//              bf16(P - P_hi), O rescaled only when the maximum grew by 2^8.  One bf16
+//              of P would add as much error to O as O's own rounding does, at any number of
+//              keys (sum|O - ref| / sum|ref| 2.1e-3 to 2.2e-3, above the library's bound of 2e-3;
+//              1.4e-3 with the pair).  l sums the unrounded P.
 //   warp 8     TMA producer: Q tiles, then K and V tiles through one ring of
 //              NS tile slots in the order K0 V0 K1 V1 ...; a tile of 128 keys is
 //              128 / page boxes, their pages looked up one tile ahead, one lane a box.
-//   warp 9     MMA issuer; at d = 64 of stream 0, and warp 11 of stream 1.
+//   warp 9     MMA issuer.
 //   warp 10    scheduler: finds the run's units and hands them to the other
 //              warps through a small ring.
 // Two streams share the tensor core, so that one multiplies while the other
@@ -41,11 +42,10 @@
 // Calls of single tokens go to paged_token_kernel, further down, which shares the split.
 //
 // Bounds, and what was measured (32 heads on 8, pages of 64 to 128):
-//   chunks: the chain of softmax and products.  d = 128, 2,048 tokens over 32,768: 770 us,
-//   1,380 TFLOP/s, the tensor pipe 54% busy: a stream's softmax takes 2,000 cycles and its two
-//   products 1,500, and P shares S's columns, so that they follow each other; two
-//   streams overlap them.  d = 64: 550 us, 960 TFLOP/s, the tensor pipe 37% and the
-//   exponential unit 37% busy.
+//   chunks: the chain of softmax and products.  d = 128, 2,048 tokens over 32,768: 1,095 us,
+//   970 TFLOP/s (P_lo's product not counted), against 775 with one bf16 of P: a stream's softmax and
+//   its three products follow each other, since P shares S's columns; two streams overlap them.
+//   d = 64: 771 us, 690 TFLOP/s.
 //   single tokens: memory.  d = 128, 64 sequences of 8,192: 360 us, 2.15 GB at 6.0 TB/s;
 //   d = 64: 197 us, 1.07 GB at 5.5 TB/s.  One sequence of 131,072: 102 us, 5.3 TB/s, with
 //   the start, the join and the ends of the runs; of 100: 6.3 us, all latency.
@@ -98,25 +98,20 @@ template <int D>
 struct Layout {
   static constexpr uint32_t TILE = BM * D * 2;  // a Q, K or V tile
   static constexpr int NS = D == 128 ? 5 : 12;  // 160 or 192 KB of K and V in flight
-  static constexpr int ISSUERS = D == 128 ? 1 : 2;
-  static_assert(ISSUERS == 1 || NS % 4 == 0, "two issuers: a unit's slot stays with one stream");
-  // Costs, in quarters of a key tile against one query tile: fitted to the blocks' times over
-  // mixed batches (cycles at d = 128 / 64: tile 2,600 / 1,400 with one query tile, 3,300 / 2,200
-  // with two; a unit's start and end 5,000 to 7,000), the last then raised, as dearer units
-  // leave fewer of them cut and joined (24 mixed sequences at d = 128: 95 us with 9, 90 with 14).
-  static constexpr int COST1 = 4, COST2 = D == 128 ? 5 : 6, OVERHEAD = D == 128 ? 14 : 20;
-  // Tensor memory: S0 [0,128), S1 [128,256).  At d = 64 P has columns of its own, so that a
-  // stream's next S is computed while its softmax still runs; at d = 128 there is no
-  // room, and P overwrites S.
-  static constexpr bool OWN_P = D == 64;
-  static __host__ __device__ constexpr uint32_t p_col(int t) { return OWN_P ? 256 + 64 * t : BN * t; }
-  static __host__ __device__ constexpr uint32_t o_col(int t) { return OWN_P ? 384 + 64 * t : 256 + 128 * t; }
+  // Costs, in quarters of a key tile against one query tile, chosen by time over mixed batches (24
+  // chunks and tokens of up to 300 over up to 5,000 keys, 32 heads of 128 on 8 / 15 of 64 on 5: 278 us /
+  // 123 us; with 5, 14 / 6, 20 for the last two 296 / 125, with 6, 9 / 7, 12 284 / 130).  The last is a
+  // unit's start and end, raised, as dearer units leave fewer of them cut and joined.
+  static constexpr int COST1 = 4, COST2 = D == 128 ? 6 : 7, OVERHEAD = D == 128 ? 20 : 28;
+  // Tensor memory: S0 [0,128), S1 [128,256), O0 [256,384), O1 [384,512).  P overwrites S: keys
+  // [16g, 16g + 16) take columns [16g, 16g + 8) (P_hi) and [16g + 8, 16g + 16) (P_lo).
+  static __host__ __device__ constexpr uint32_t o_col(int t) { return 256 + 128 * t; }
   static constexpr uint32_t OFF_Q = 0;
   static constexpr uint32_t OFF_RING = 2 * TILE;
   static constexpr uint32_t OFF_BAR = OFF_RING + NS * TILE;
   // q_full[2], q_empty[2], full[NS], empty[NS], s_full[2], p_ready[2],
-  // pv_done[2], s_free[2], u_full[NU], u_empty[NU], joined[2], drain[2]
-  static constexpr uint32_t NBAR = 4 + 2 * NS + 8 + 2 * NU + 2 + 2;
+  // pv_done[2], u_full[NU], u_empty[NU], joined[2], drain
+  static constexpr uint32_t NBAR = 4 + 2 * NS + 6 + 2 * NU + 2 + 1;
   static constexpr uint32_t OFF_UNITS = (OFF_BAR + NBAR * 8 + 15) & ~15u;
   static constexpr uint32_t OFF_ML = OFF_UNITS + NU * 48;
   static constexpr uint32_t OFF_MISC = OFF_ML + BM * 8;
@@ -388,11 +383,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t *s_full = empty + NS;                                       // [2]
   uint64_t *p_ready = s_full + 2;                                      // [2]
   uint64_t *pv_done = p_ready + 2;                                     // [2]
-  uint64_t *s_free = pv_done + 2;                                      // [2]
-  uint64_t *u_full = s_free + 2;                                       // [NU]
+  uint64_t *u_full = pv_done + 2;                                      // [NU]
   uint64_t *u_empty = u_full + NU;                                     // [NU]
   uint64_t *joined = u_empty + NU;                                     // [2]: stream 1's (m, l); O1 read
-  uint64_t *mma_drain = joined + 2;                                    // [2]
+  uint64_t *mma_drain = joined + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::OFF_MISC);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_MISC + 4);
   volatile int *has_work = reinterpret_cast<volatile int *>(smem + L::OFF_MISC + 8);
@@ -403,22 +397,21 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
       mbar_init(&q_full[t], 1);
-      mbar_init(&q_empty[t], L::ISSUERS);
-      mbar_init(&mma_drain[t], 1);
+      mbar_init(&q_empty[t], 1);
       mbar_init(&s_full[t], 1);
       mbar_init(&p_ready[t], 128);
       mbar_init(&pv_done[t], 1);
-      mbar_init(&s_free[t], 128);
       mbar_init(&joined[t], 128);
     }
     for (int s = 0; s < NS; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], L::ISSUERS);
+      mbar_init(&empty[s], 1);
     }
     for (int s = 0; s < NU; ++s) {
       mbar_init(&u_full[s], 1);
-      mbar_init(&u_empty[s], 1 + L::ISSUERS + 8);  // producer, MMA warps, eight softmax warps
+      mbar_init(&u_empty[s], 10);  // producer, MMA warp, eight softmax warps
     }
+    mbar_init(mma_drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -460,7 +453,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     return ok;
   };
   // Reads the next unit; false when the run is done or a wait expired.  Lane 0 polls: no vote
-  // in the producer and the issuers, whose lanes leave a poll at different times.
+  // in the producer and the issuer, whose lanes leave a poll at different times.
   auto next_unit = [&](int &k, Unit &u, int site) -> bool {
     const int s = k % NU;
     if (!mbar_wait_warp(&u_full[s], (k / NU) & 1, p.wc, abort_flag, site)) return false;
@@ -570,13 +563,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncwarp();
   };
 
-  // Issues the products of streams [first, end).  At d = 128 one warp issues both streams', whose
-  // order keeps them half a step apart: one multiplies while the other exponentiates.  (An
-  // issuer for each let them fall into step, and single tokens took 389 us that take 336.)  At
-  // d = 64, where S does not wait for P V and the products are half as long, the issuer's own
-  // waits, some 200 cycles each, bounded the step, and each stream has an issuer (a chunk
-  // over 32768 positions 681 us with one issuer and shared columns, 551 with two and P's own).
-  auto role_mma = [&](const int first, const int end) {
+  // Issues the products of both streams, whose order keeps them half a step apart: one
+  // multiplies while the other exponentiates.  (An issuer for each let them fall into step: at
+  // d = 128 single tokens took 389 us that take 336, at d = 64 a chunk over 32,768 positions 1,131
+  // and 770.)  Measured at d = 64 and dropped: columns of P_hi's own and P_lo in shared memory, so
+  // that a stream's next S is computed while its softmax still runs, with two issuers: the chunk 750 us, 24
+  // mixed sequences no faster, and every buffer freed by two warps that run apart.
+  auto role_mma = [&]() {
     const uint32_t idS = idesc_bf16_f32(BM, BN, 0, 0), idO = idesc_bf16_f32(BM, D, 0, 1);
     const SDesc dQ = sdesc_make(smem_u32(smem + L::OFF_Q), 16, 1024);
     const SDesc dK = sdesc_make(smem_u32(smem + L::OFF_RING), 16, 1024);
@@ -586,7 +579,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint32_t q_uses[2] = {0, 0}, qsel = 0;
     uint32_t base = 0;             // ring number of the unit's first K tile
     uint32_t steps[2] = {0, 0};    // P V products of each stream so far
-    uint32_t s_count[2] = {0, 0};  // S products of each stream so far
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
       return mbar_wait_warp(bar, parity, p.wc, abort_flag, SITE_PAGED_MMA);
@@ -611,39 +603,18 @@ __global__ void __launch_bounds__(THREADS, 1)
       ns[0] = two ? max(0, min(u.ja, u.j1) - u.j0) : (n + 1) / 2;
       ns[1] = two ? n : n / 2;
       const int single = (int)qsel;  // the Q tile of a unit that has one
-      // An issuer waits for every copy of Q, also for the one that only the other issuer reads: a parity
-      // tells no more than whether the phase before the last is over, so with one left out the next
-      // unit's wait could be met by the phase before it and its products read Q too soon.
       for (int b = 0; b < 2; ++b)
         if (two || b == single) {
           ok = ok && wait(&q_full[b], q_uses[b] & 1);
           ++q_uses[b];
         }
       if (!two) qsel ^= 1;
-      // Frees a buffer.  With one issuer the last product that reads it does; with two, one
-      // arrival comes from each stream that reads it, both from a stream that reads it alone.
-      auto release = [&](uint64_t *bar, bool alone) {
-        umma_commit(bar);
-        if (L::ISSUERS == 2 && alone) umma_commit(bar);
-      };
-      // does stream t's step i read its K and V tiles alone, or (one issuer) last
-      auto last_reader = [&](int t, int i) {
-        return !two || (t == 1 && (L::ISSUERS == 1 || i >= ns[0]));
-      };
-      for (int t = first; t < end; ++t) {
-        if (ok && ns[t] == 0 && (two || L::ISSUERS == 2) && elect_one()) release(&q_empty[two ? t : single], two);
-        __syncwarp();
-      }
+      // whether stream t's product is the last that reads its K or V tile
+      auto last_reader = [&](int t) { return !two || t == 1; };
+      // no key tile of this part is seen by tile 0
+      if (ok && two && ns[0] == 0 && elect_one()) umma_commit(&q_empty[0]);
+      __syncwarp();
       auto k_seq = [&](int t, int i) { return base + 2 * (two ? i : 2 * i + t); };
-      // Two issuers wait on the ring's slots out of ring order, and a parity says only whether
-      // the phase before the last is over: at a slot's first use by the unit, that its previous
-      // tile has been freed is waited for first.  (Within a unit a slot goes to the same stream
-      // each time, or both wait on all of them.)
-      auto fresh = [&](uint32_t seq) {
-        const uint32_t turn = seq / NS;
-        if (L::ISSUERS == 2 && turn > 0 && seq - base < NS) return wait(&empty[seq % NS], (turn - 1) & 1);
-        return true;
-      };
       // S of step i into columns [128 t, 128 t + 128), by the elected lane
       auto put_s = [&](int t, int i) {
         const uint32_t st = k_seq(t, i) % NS, qo = (uint32_t)(two ? t : single) * L::TILE, ko = st * L::TILE;
@@ -653,33 +624,23 @@ __global__ void __launch_bounds__(THREADS, 1)
           umma_f16_ss(tmem + t * BN, sdesc_at(dQ, qo + off), sdesc_at(dK, ko + off), idS, kk > 0);
         }
         umma_commit(&s_full[t]);
-        if (L::ISSUERS == 2 || last_reader(t, i)) release(&empty[st], last_reader(t, i));
-        if (two || L::ISSUERS == 2 ? i == ns[t] - 1 : 2 * i + t == n - 1)
-          release(&q_empty[two ? t : single], two);
+        if (last_reader(t)) umma_commit(&empty[st]);
+        if (two ? i == ns[t] - 1 : 2 * i + t == n - 1) umma_commit(&q_empty[two ? t : single]);
       };
       auto issue_s = [&](int t, int i) -> bool {
-        const uint32_t seq = k_seq(t, i), st = seq % NS, turn = seq / NS;
-        if (!fresh(seq)) return false;
-        // where P has its own columns, S may come as soon as the one before it has been read; where it
-        // has not, the P V product before it in the issue order has read them last
-        if (L::OWN_P && s_count[t] > 0) {
-          if (!wait_pair(&full[st], turn & 1, &s_free[t], (s_count[t] - 1) & 1, nullptr, 0)) return false;
-        } else if (!wait(&full[st], turn & 1)) {
-          return false;
-        }
-        ++s_count[t];
+        const uint32_t seq = k_seq(t, i);
+        if (!wait(&full[seq % NS], (seq / NS) & 1)) return false;
         tc_fence_after();
         if (elect_one()) put_s(t, i);
         __syncwarp();
         return true;
       };
-      // O_t += P_t V of step i; where P shares S's columns, with S of the stream's next step right
-      // behind it if its K tile is there
+      // O_t += P_hi V + P_lo V of step i, with S of the stream's next step right behind it if its K
+      // tile is there
       auto issue_pv = [&](int t, int i) -> bool {
         const uint32_t seq = k_seq(t, i) + 1, st = seq % NS;
-        const bool next_s = !L::OWN_P && i + 1 < ns[t];
+        const bool next_s = i + 1 < ns[t];
         const uint32_t nseq = k_seq(t, i + 1);
-        if (!fresh(seq)) return false;
         const int got = wait_pair(&full[st], (seq / NS) & 1, &p_ready[t], steps[t] & 1,
                                   next_s ? &full[nseq % NS] : nullptr, (nseq / NS) & 1);
         if (!(got & 1)) return false;
@@ -702,30 +663,30 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (elect_one()) {
           const uint32_t vo = st * L::TILE;
 #pragma unroll
-          for (int kk = 0; kk < BN / 16; ++kk)
-            umma_f16_ts(tmem + L::o_col(t), tmem + L::p_col(t) + kk * 8, sdesc_at(dV, vo + kk * 2048), idO,
-                        i > 0 || kk > 0);
+          for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int kk = 0; kk < BN / 16; ++kk)
+              umma_f16_ts(tmem + L::o_col(t), tmem + t * BN + kk * 16 + part * 8, sdesc_at(dV, vo + kk * 2048), idO,
+                          i > 0 || part > 0 || kk > 0);
           umma_commit(&pv_done[t]);
-          if (L::ISSUERS == 2 || last_reader(t, i)) release(&empty[st], last_reader(t, i));
+          if (last_reader(t)) umma_commit(&empty[st]);
           if (got & 2) put_s(t, i + 1);
         }
         __syncwarp();
         return !next_s || (got & 2) || issue_s(t, i + 1);
       };
-      for (int t = first; ok && t < end; ++t)
+      for (int t = 0; ok && t < 2; ++t)
         if (ns[t] > 0) ok = issue_s(t, 0);
       for (int i = 0; ok && i < max(ns[0], ns[1]); ++i)
-        for (int t = first; ok && t < end; ++t) {
-          if (L::OWN_P && i + 1 < ns[t]) ok = issue_s(t, i + 1);
-          if (ok && i < ns[t]) ok = issue_pv(t, i);
-        }
+        for (int t = 0; ok && t < 2; ++t)
+          if (i < ns[t]) ok = issue_pv(t, i);
       base += 2 * n;
     }
     // no MMA may still be running when tensor memory is released
     __syncwarp();
-    if (elect_one()) umma_commit(&mma_drain[first]);
+    if (elect_one()) umma_commit(mma_drain);
     __syncwarp();
-    if (lane == 0) drain_wait(&mma_drain[first], 0, p.wc);
+    if (lane == 0) drain_wait(mma_drain, 0, p.wc);
     __syncwarp();
   };
 
@@ -733,7 +694,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int t = warp >> 2;
     const int row = threadIdx.x & 127;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lane_off + t * BN, tP = tmem + lane_off + L::p_col(t);
+    const uint32_t tS = tmem + lane_off + t * BN;
     const int rtok = row / p.G, rhead = row - rtok * p.G;  // token of the tile, head of the group
     Unit u;
     int k = 0;
@@ -761,10 +722,6 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int c = 0; c < BN / 32; ++c)
             tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[c * 32]));
           tmem_wait_ld();
-          if (L::OWN_P) {
-            tc_fence_before();
-            mbar_arrive(&s_free[t]);
-          }
           if (kv0 + BN > lim) {
 #pragma unroll
             for (int e = 0; e < BN; ++e)
@@ -792,28 +749,25 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           __syncwarp();  // the stores of P are the whole warp's
           const float mref = m == -INFINITY ? 0.0f : m;
-          if (L::OWN_P && i > 0) {  // the product before this one has read P, and O holds it
-            ok = warp_wait(&pv_done[t], (steps[t] + i - 1) & 1, SITE_PAGED_SOFTMAX);
-            if (!ok) break;
-            tc_fence_after();
-          }
-          // P = 2^(s scale log2e - m): keys [32 g, 32 g + 32) to columns [16 g, 16 g + 16)
+          // P = 2^(s scale log2e - m) = P_hi + P_lo, sixteen keys at a time
           const uint64_t sc2 = f32x2(p.scale_log2, p.scale_log2), nm2 = f32x2(-mref, -mref);
           uint64_t rs2[4] = {0, 0, 0, 0};
 #pragma unroll
-          for (int g = 0; g < BN / 32; ++g) {
-            uint32_t pk[16];
+          for (int g = 0; g < BN / 16; ++g) {
+            uint32_t pk[16];  // P_hi, P_lo
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
+            for (int e = 0; e < 16; e += 2) {
               float x0, x1;
-              f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[g * 32 + e]), __uint_as_float(s[g * 32 + e + 1])),
+              f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[g * 16 + e]), __uint_as_float(s[g * 16 + e + 1])),
                                     sc2, nm2),
                           x0, x1);
               const float p0 = ex2(x0), p1 = ex2(x1);
               rs2[(e >> 1) & 3] = add_f32x2(rs2[(e >> 1) & 3], f32x2(p0, p1));
-              pk[e >> 1] = pack_bf16(p0, p1);
+              const uint32_t h = pack_bf16(p0, p1);
+              pk[e >> 1] = h;
+              pk[8 + (e >> 1)] = pack_bf16(p0 - __uint_as_float(h << 16), p1 - __uint_as_float(h & 0xffff0000u));
             }
-            tmem_st16(tP + g * 16, pk);
+            tmem_st16(tS + g * 16, pk);
           }
           float rs = 0.0f;
 #pragma unroll
@@ -837,12 +791,6 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           l = l * alpha + rs;
           tmem_wait_st();
-        } else if (L::OWN_P) {
-          // a warp without rows keeps step too: S of step i + 1 does not wait for P of step i, and an
-          // arrival of step i + 1 must not count for step i
-          mbar_arrive(&s_free[t]);
-          if (i > 0) ok = warp_wait(&pv_done[t], (steps[t] + i - 1) & 1, SITE_PAGED_SOFTMAX);
-          if (!ok) break;
         }
         tc_fence_before();
         mbar_arrive(&p_ready[t]);
@@ -935,16 +883,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   };
 
-  if (warp >= 8) {  // with one issuer warp 11 only hands its registers over
+  if (warp >= 8) {  // warp 11 only hands its registers over
     setmaxnreg_dec<REGS_CONTROL>();
     if (warp == 8)
       role_producer();
     else if (warp == 10)
       role_scheduler();
-    else if (L::ISSUERS == 2)
-      role_mma(warp == 9 ? 0 : 1, warp == 9 ? 1 : 2);
     else if (warp == 9)
-      role_mma(0, 2);
+      role_mma();
   } else {
     setmaxnreg_inc<REGS_SOFTMAX>();
     role_softmax();

@@ -563,8 +563,8 @@ int chain_qk_norm_rope_append(const chain_tensor_t *Q, const chain_tensor_t *K,
  * Cached K and V must be finite at positions below kv_lens[b]; slots of later
  * positions may hold anything, NaN included.  A missing page counts as keys and values of zeros.
  * Arithmetic: Q K^T, the softmax's statistics and P V accumulate in fp32;
- * P enters the P V product as bf16, in calls of single tokens as a pair of bf16 (P and what
- * its rounding left), as in chain_fwd.  A call with H / Hkv at most 16 and total at
+ * P enters the P V product as a pair of bf16 (P and what its rounding left), as in
+ * chain_fwd, so that O's own rounding is the only one to bf16.  A call with H / Hkv at most 16 and total at
  * most batch is taken for one of single tokens: a longer chunk in it, beside as many
  * sequences without new tokens, is right too but reads its keys once for every
  * 16 / (H / Hkv) of its tokens, so such sequences are better left out of the batch.

@@ -39,3 +39,21 @@ def run(cg, case, causal=True):
 @pytest.mark.parametrize("name", TOKENS)
 def test_single_tokens(cg, name):
     run(cg, TOKENS[name])
+
+
+CHUNKS = {
+    "a chunk over 2000": ([2000], [200], 16, 4, 128, 128),
+    "a chunk over 2000, d 64": ([2000], [200], 16, 4, 64, 64),
+    "mixed, odd group": ([700, 33, 1500, 70, 900], [60, 1, 1, 70, 300], 14, 2, 128, 16),
+    "mixed, odd group, d 64": ([700, 33, 1500, 70, 900], [60, 1, 1, 70, 300], 15, 5, 64, 16),
+    "whole sequences to a block": ([700 - 3 * i for i in range(64)], [3] * 64, 16, 8, 128, 64),
+    "whole sequences to a block, d 64": ([700 - 3 * i for i in range(64)], [3] * 64, 16, 8, 64, 64),
+    "no grouped heads, d 64": ([900, 600], [130, 257], 4, 4, 64, 32),
+    "more query heads than a small tile takes": ([3000, 900], [1, 1], 64, 2, 128, 128),
+}
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("name", CHUNKS)
+def test_chunks(cg, name, causal):
+    run(cg, CHUNKS[name], causal)
