@@ -168,6 +168,8 @@ static int paged(PyObject *cu, PyObject *lens, PyObject *table, long dev, paged_
 /* A workspace: any tensor; its bytes are given beside it. */
 static int workspace(PyObject *t, long dev, void **ptr) { return on_device(t, dev) || address(t, ptr) ? -1 : 0; }
 
+/* Each call below is made without the interpreter's lock: a launch waits while the queue of the
+ * stream is full, and the program's other threads go on meanwhile. */
 static PyObject *done(int rc, const char *what) {
   if (rc == CHAIN_OK) Py_RETURN_NONE;
   PyObject *e = PyObject_CallFunction(chain_error, "is", rc, what);
@@ -218,8 +220,11 @@ static PyObject *qk_norm_rope(PyObject *self, PyObject *const *a, Py_ssize_t n) 
   const double eps = PyFloat_AsDouble(a[6]);
   const long pairs = PyLong_AsLong(a[7]);
   if (PyErr_Occurred()) return NULL;
-  return done(chain_qk_norm_rope(Q, K, gq, gk, w, (const int32_t *)pos, (float)eps, (int)pairs, Qo, Ko, stream),
-              "chain_qk_norm_rope");
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = chain_qk_norm_rope(Q, K, gq, gk, w, (const int32_t *)pos, (float)eps, (int)pairs, Qo, Ko, stream);
+  Py_END_ALLOW_THREADS
+  return done(rc, "chain_qk_norm_rope");
 }
 
 static PyObject *qk_norm_rope_bwd(PyObject *self, PyObject *const *a, Py_ssize_t n) {
@@ -243,9 +248,12 @@ static PyObject *qk_norm_rope_bwd(PyObject *self, PyObject *const *a, Py_ssize_t
   const long pairs = PyLong_AsLong(a[9]);
   const size_t bytes = PyLong_AsSize_t(a[15]);
   if (PyErr_Occurred()) return NULL;
-  return done(chain_qk_norm_rope_bwd(dQo, dKo, Q, K, gq, gk, w, (const int32_t *)pos, (float)eps, (int)pairs, dQ,
-                                     dK, dgq, dgk, ws, bytes, stream),
-              "chain_qk_norm_rope_bwd");
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = chain_qk_norm_rope_bwd(dQo, dKo, Q, K, gq, gk, w, (const int32_t *)pos, (float)eps, (int)pairs, dQ, dK, dgq,
+                              dgk, ws, bytes, stream);
+  Py_END_ALLOW_THREADS
+  return done(rc, "chain_qk_norm_rope_bwd");
 }
 
 /* Sizes only: Q may lie on any device. */
@@ -267,9 +275,12 @@ static PyObject *paged_append(PyObject *self, PyObject *const *a, Py_ssize_t n) 
   TENSOR(6, Vc);
   paged_t p;
   if (paged(a[2], a[3], a[4], dev, &p)) return NULL;
-  return done(chain_paged_append(K, V, (const int32_t *)p.cu, (const int32_t *)p.lens, (const int32_t *)p.table,
-                                 p.stride, p.batch, p.max_pages, Kc, Vc, stream),
-              "chain_paged_append");
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = chain_paged_append(K, V, (const int32_t *)p.cu, (const int32_t *)p.lens, (const int32_t *)p.table, p.stride,
+                          p.batch, p.max_pages, Kc, Vc, stream);
+  Py_END_ALLOW_THREADS
+  return done(rc, "chain_paged_append");
 }
 
 static PyObject *qk_norm_rope_append(PyObject *self, PyObject *const *a, Py_ssize_t n) {
@@ -290,10 +301,13 @@ static PyObject *qk_norm_rope_append(PyObject *self, PyObject *const *a, Py_ssiz
   const double eps = PyFloat_AsDouble(a[6]);
   const long pairs = PyLong_AsLong(a[7]);
   if (PyErr_Occurred()) return NULL;
-  return done(chain_qk_norm_rope_append(Q, K, V, gq, gk, w, (float)eps, (int)pairs, (const int32_t *)p.cu,
-                                        (const int32_t *)p.lens, (const int32_t *)p.table, p.stride, p.batch,
-                                        p.max_pages, Kc, Vc, Qo, stream),
-              "chain_qk_norm_rope_append");
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = chain_qk_norm_rope_append(Q, K, V, gq, gk, w, (float)eps, (int)pairs, (const int32_t *)p.cu,
+                                 (const int32_t *)p.lens, (const int32_t *)p.table, p.stride, p.batch, p.max_pages,
+                                 Kc, Vc, Qo, stream);
+  Py_END_ALLOW_THREADS
+  return done(rc, "chain_qk_norm_rope_append");
 }
 
 static PyObject *fwd_paged(PyObject *self, PyObject *const *a, Py_ssize_t n) {
@@ -312,9 +326,12 @@ static PyObject *fwd_paged(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   const double scale = PyFloat_AsDouble(a[7]);
   const size_t bytes = PyLong_AsSize_t(a[11]);
   if (PyErr_Occurred()) return NULL;
-  return done(chain_fwd_paged(Q, Kc, Vc, (const int32_t *)p.cu, (const int32_t *)p.lens, (const int32_t *)p.table,
-                              p.stride, p.batch, p.max_pages, (int)mask, (float)scale, O, LSE, ws, bytes, stream),
-              "chain_fwd_paged");
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = chain_fwd_paged(Q, Kc, Vc, (const int32_t *)p.cu, (const int32_t *)p.lens, (const int32_t *)p.table,
+                       p.stride, p.batch, p.max_pages, (int)mask, (float)scale, O, LSE, ws, bytes, stream);
+  Py_END_ALLOW_THREADS
+  return done(rc, "chain_fwd_paged");
 }
 
 #define METHOD(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, NULL}
