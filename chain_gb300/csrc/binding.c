@@ -110,6 +110,15 @@ static int indices(PyObject *t, long dev, const char *what, int nd, void **ptr, 
   return 0;
 }
 
+/* 1 or 0; -1 on error */
+static int is_dense(PyObject *t) {
+  PyObject *c = PyObject_CallMethodNoArgs(t, s_is_contiguous);
+  if (!c) return -1;
+  const int dense = PyObject_IsTrue(c);
+  Py_DECREF(c);
+  return dense;
+}
+
 /* positions: one int32 for each of `tokens`, any shape, or None */
 static int positions(PyObject *t, long dev, int64_t tokens, void **ptr) {
   *ptr = NULL;
@@ -123,10 +132,8 @@ static int positions(PyObject *t, long dev, int64_t tokens, void **ptr) {
     return -1;
   }
   if (on_device(t, dev) || address(t, ptr)) return -1;
-  PyObject *c = PyObject_CallMethodNoArgs(t, s_is_contiguous);
-  if (!c) return -1;
-  const int dense = PyObject_IsTrue(c);
-  Py_DECREF(c);
+  const int dense = is_dense(t);
+  if (dense < 0) return -1;
   int64_t shape[8];
   const int n = read_sizes(PyObject_GetAttr(t, s_shape), shape, 8);
   if (n < 0) return -1;
@@ -165,8 +172,13 @@ static int paged(PyObject *cu, PyObject *lens, PyObject *table, long dev, paged_
   return 0;
 }
 
-/* A workspace: any tensor; its bytes are given beside it. */
-static int workspace(PyObject *t, long dev, void **ptr) { return on_device(t, dev) || address(t, ptr) ? -1 : 0; }
+/* A workspace: any contiguous tensor; its bytes are given beside it. */
+static int workspace(PyObject *t, long dev, void **ptr) {
+  if (on_device(t, dev) || address(t, ptr)) return -1;
+  const int dense = is_dense(t);
+  if (dense == 0) PyErr_SetString(PyExc_ValueError, "the workspace must be contiguous");
+  return dense == 1 ? 0 : -1;
+}
 
 /* Each call below is made without the interpreter's lock: a launch waits while the queue of the
  * stream is full, and the program's other threads go on meanwhile. */
