@@ -341,7 +341,7 @@ def _small():
         _load()
         from . import _build
         if not os.path.exists(_build.NATIVE):
-            build()
+            _build.build_native()
         from . import _native
         _native.setup(torch.bfloat16, torch.float32, torch.int32, ChainError)
         _calls = _native

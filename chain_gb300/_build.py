@@ -4,7 +4,8 @@ Each translation unit under csrc/ compiles in parallel to an object file in
 chain_gb300/_build/, then nvcc links the shared library beside this file.
 Rebuilds only what changed (sources or the shared headers).  binding.c, the
 CPython entry to the library's small calls, is compiled with gcc into
-chain_gb300/_native and linked to the library beside it.
+chain_gb300/_native and linked to the library beside it; where Python's headers
+or gcc are missing the library stands alone, and those calls say so.
 """
 from __future__ import annotations
 
@@ -14,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -38,6 +40,32 @@ def _headers():
         glob.glob(os.path.join(ROOT, "include", "*.h"))
 
 
+def _run(cmd, verbose=False):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compilation failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    if verbose and (r.stdout or r.stderr):
+        print(r.stdout + r.stderr)
+
+
+def build_native(force: bool = False, verbose: bool = False) -> str:
+    """The CPython module, once the library is there."""
+    src = os.path.join(CSRC, "binding.c")
+    newest = max(os.path.getmtime(f) for f in [src, *_headers()])
+    if not force and os.path.exists(NATIVE) and os.path.getmtime(NATIVE) >= newest:
+        return NATIVE
+    include = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(include, "Python.h")):
+        raise RuntimeError(f"chain_gb300: no Python.h in {include}; the native module cannot be built")
+    if not shutil.which("gcc"):
+        raise RuntimeError("chain_gb300: gcc not found; the native module (Python.h) cannot be built")
+    tmp = NATIVE + f".tmp{os.getpid()}"
+    _run(["gcc", "-O2", "-std=c11", "-Wall", "-fPIC", "-shared", "-I", include, src, "-o", tmp, "-L" + HERE,
+          "-lchain_gb300", "-Wl,-rpath,$ORIGIN"], verbose)
+    os.replace(tmp, NATIVE)
+    return NATIVE
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -52,11 +80,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
             jobs.append([nvcc, *ARCH, *FLAGS, *extra, "-c", s, "-o", o])
 
     def run(cmd):
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"compilation failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
-        if verbose and (r.stdout or r.stderr):
-            print(r.stdout + r.stderr)
+        _run(cmd, verbose)
 
     if jobs:
         with cf.ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
@@ -67,12 +91,11 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         tmp = LIB + f".tmp{os.getpid()}"
         run([nvcc, *ARCH, "-shared", "-Xlinker", "-soname=" + os.path.basename(LIB), "-o", tmp, *objs])
         os.replace(tmp, LIB)
-    src = os.path.join(CSRC, "binding.c")
-    if force or not os.path.exists(NATIVE) or os.path.getmtime(NATIVE) < max(os.path.getmtime(src), hdr_t):
-        tmp = NATIVE + f".tmp{os.getpid()}"
-        run(["gcc", "-O2", "-std=c11", "-Wall", "-fPIC", "-shared", "-I", sysconfig.get_paths()["include"], src,
-             "-o", tmp, "-L" + HERE, "-lchain_gb300", "-Wl,-rpath,$ORIGIN"])
-        os.replace(tmp, NATIVE)
+    if shutil.which("gcc") and os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        build_native(force, verbose)
+    else:
+        warnings.warn("chain_gb300: built without its native module, which needs gcc and Python.h: the norm, "
+                      "rotation and paged cache calls are there from C only", RuntimeWarning, stacklevel=2)
     return LIB
 
 
