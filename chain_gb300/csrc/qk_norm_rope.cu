@@ -47,7 +47,7 @@ constexpr unsigned long long INV_2PI_LO = 0x7f09d5f47d4d3770ull;
 __device__ __forceinline__ unsigned long long turns_per_position(float w) {
   const uint32_t b = __float_as_uint(w);
   const int ex = (int)((b >> 23) & 0xff);
-  if (ex == 255) return 0;  // infinite or NaN frequency: no rotation
+  if (ex == 255) return 0;  // infinite or NaN: see put_turns
   const unsigned long long m = (b & 0x7fffffu) | (ex ? 0x800000u : 0u);
   const int sh = 150 - (ex ? ex : 1);  // -e
   const unsigned __int128 hi = (unsigned __int128)m * INV_2PI_HI;
@@ -85,6 +85,19 @@ __device__ __forceinline__ float2 angle(int p, unsigned long long u) {
     c = -w;
   }
   return q & 2 ? make_float2(-c, -s) : make_float2(c, s);
+}
+
+// The block's frequencies as turns, and whether one of them is infinite or NaN.  That has to show in
+// the result, so the weights of its pairs become NaN then: a test at the angles themselves cost
+// the kernels of few heads 2 to 35% of their time.  Holds the block's barrier.
+__device__ __forceinline__ bool put_turns(unsigned long long *turns, const float *inv_freq, int rot) {
+  bool odd = false;
+  for (int f = threadIdx.x; f < rot / 2; f += THREADS) {
+    const float w = __ldg(inv_freq + f);
+    turns[f] = turns_per_position(w);
+    odd = odd || !isfinite(w);
+  }
+  return __syncthreads_or(odd);
 }
 
 // ------------------------------------------------------ sixteen elements a lane
@@ -217,6 +230,17 @@ __device__ __forceinline__ void load_weight(const NormRopeWeight &g, const Lane 
   for (int k = 0; k < 16; ++k) {
     const int e = element<T, NEIGHBOUR>(ln, k);
     f[k] = g.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(g.ptr)[e]) : static_cast<const float *>(g.ptr)[e];
+  }
+}
+
+// NaN in place of what belongs to a pair whose frequency is infinite or NaN
+template <typename T, bool NEIGHBOUR>
+__device__ __forceinline__ void spoil(const float *inv_freq, int rot, const Lane &ln, float (&f)[16]) {
+  if (ln.at >= rot) return;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int e = element<T, NEIGHBOUR>(ln, k);
+    if (!isfinite(__ldg(inv_freq + (NEIGHBOUR ? e / 2 : e)))) f[k] = f[8 + k] = __int_as_float(0x7fffffff);
   }
 }
 
@@ -433,6 +457,20 @@ __device__ __forceinline__ void put_weights(Weights &w, const NormRopeWeight &gq
   }
 }
 template <typename T, int D, bool NEIGHBOUR>
+__device__ __forceinline__ void spoil_weights(Weights &w, const float *inv_freq, int rot) {
+  constexpr int LPR = D / EPL;
+  if ((int)threadIdx.x < 2 * LPR) {
+    const int side = threadIdx.x / LPR, l = threadIdx.x % LPR;
+    float g[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) g[k] = w.g[side][k][l];
+    spoil<T, NEIGHBOUR>(inv_freq, rot, lane_of<T, D>(l, rot), g);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) w.g[side][k][l] = g[k];
+  }
+  __syncthreads();
+}
+template <typename T, int D, bool NEIGHBOUR>
 __device__ __forceinline__ void turn_for(Turn &t, const Weights &w, int side, const Lane &ln, int rot, const float2 *table,
                                          int lane) {
   Angles an;
@@ -477,9 +515,9 @@ __global__ void __launch_bounds__(THREADS, FWD_BLOCKS) norm_rope_kernel(const No
   };
 #pragma unroll
   for (int i = 0; i < STAGES - 1; ++i) fetch();
-  for (int f = threadIdx.x; f < a.rot / 2; f += THREADS) turns[f] = turns_per_position(__ldg(a.inv_freq + f));
   put_weights<T, D, NEIGHBOUR>(weights, a.gq, a.gk, a.rot);
-  __syncthreads();
+  const bool odd = put_turns(turns, a.inv_freq, a.rot);
+  if (odd) spoil_weights<T, D, NEIGHBOUR>(weights, a.inv_freq, a.rot);
   Turn turn;
   int of = -1;  // the token of `table`
   int pos = 0;
@@ -539,8 +577,7 @@ __global__ void __launch_bounds__(THREADS, ROW_BLOCKS)
   __shared__ unsigned long long turns[MAX_FREQ];
   const int lane = threadIdx.x & 31;
   const Lane ln = lane_of<T, D>(lane, a.rot);
-  for (int f = threadIdx.x; f < a.rot / 2; f += THREADS) turns[f] = turns_per_position(__ldg(a.inv_freq + f));
-  __syncthreads();
+  const bool odd = put_turns(turns, a.inv_freq, a.rot);
   float g[16];
   int of = -1;  // the side of g
   for (uint32_t pass = walk_start(); pass < passes; pass += gridDim.x * WARPS) {
@@ -553,7 +590,10 @@ __global__ void __launch_bounds__(THREADS, ROW_BLOCKS)
       x.load(r.in(side ? a.k : a.q, (int)a.n, ln), ln.step);
       p = position(a, r.t);
     }
-    if (side != of) load_weight<T, NEIGHBOUR>(side ? a.gk : a.gq, ln, g);
+    if (side != of) {
+      load_weight<T, NEIGHBOUR>(side ? a.gk : a.gq, ln, g);
+      if (odd) spoil<T, NEIGHBOUR>(a.inv_freq, a.rot, ln, g);
+    }
     of = side;
     Angles an;
     own_angles<T, NEIGHBOUR>(an, ln, a.rot, p, turns);
@@ -616,7 +656,7 @@ __device__ __forceinline__ void sum_block(const float (&dg)[16], const Lane &ln,
 template <typename T, int D, bool NEIGHBOUR>
 __device__ __forceinline__ void bwd_side(const NormRopeArgs &a, const NormRopeSide &x, const NormRopeSide &dy,
                                          const NormRopeSide &dx, const NormRopeWeight &weight, int heads,
-                                         const Plan &pl, const unsigned long long *turns, float2 *table,
+                                         const Plan &pl, const unsigned long long *turns, bool odd, float2 *table,
                                          uint8_t *ring, float (*sums)[D], float *part) {
   constexpr int LPR = D / EPL, RPW = rows_per_pass<D>();
   constexpr int U = bwd_passes<T>(), BYTES = U * pass_bytes<T>();  // of x, and of dy
@@ -653,6 +693,10 @@ __device__ __forceinline__ void bwd_side(const NormRopeArgs &a, const NormRopeSi
 #pragma unroll
   for (int k = 0; k < 16; ++k) dg[k] = 0.0f;
   load_weight<T, NEIGHBOUR>(weight, ln, g);
+  if (odd) {
+    spoil<T, NEIGHBOUR>(a.inv_freq, a.rot, ln, g);
+    spoil<T, NEIGHBOUR>(a.inv_freq, a.rot, ln, dg);
+  }
   Angles an;
   int of = -1;  // the token of `an`
   int pos = 0;
@@ -700,13 +744,17 @@ __device__ __forceinline__ void bwd_side(const NormRopeArgs &a, const NormRopeSi
 template <typename T, int D, bool NEIGHBOUR>
 __device__ __forceinline__ void bwd_rows(const NormRopeArgs &a, const NormRopeSide &x, const NormRopeSide &dy,
                                          const NormRopeSide &dx, const NormRopeWeight &weight, int heads,
-                                         const unsigned long long *turns, float (*sums)[D], float *part) {
+                                         const unsigned long long *turns, bool odd, float (*sums)[D], float *part) {
   const int lane = threadIdx.x & 31;
   const Lane ln = lane_of<T, D>(lane, a.rot);
   float g[16], dg[16];
 #pragma unroll
   for (int k = 0; k < 16; ++k) dg[k] = 0.0f;
   load_weight<T, NEIGHBOUR>(weight, ln, g);
+  if (odd) {
+    spoil<T, NEIGHBOUR>(a.inv_freq, a.rot, ln, g);
+    spoil<T, NEIGHBOUR>(a.inv_freq, a.rot, ln, dg);
+  }
   const uint32_t passes = ((uint32_t)a.tokens * heads + rows_per_pass<D>() - 1) / rows_per_pass<D>();
   for (uint32_t pass = walk_start(); pass < passes; pass += gridDim.x * WARPS) {
     RowPass<T, D> r;
@@ -740,11 +788,10 @@ __global__ void __launch_bounds__(THREADS, BWD_BLOCKS) norm_rows_bwd_kernel(cons
   __shared__ float sums[WARPS][D];
   const NormRopeArgs &a = b.fwd;
   pdl_launch_dependents();
-  for (int f = threadIdx.x; f < a.rot / 2; f += THREADS) turns[f] = turns_per_position(__ldg(a.inv_freq + f));
-  __syncthreads();
+  const bool odd = put_turns(turns, a.inv_freq, a.rot);
   part += (int64_t)blockIdx.x * 2 * D;
-  bwd_rows<T, D, NEIGHBOUR>(a, a.q, b.dqo, a.qo, a.gq, a.H, turns, sums, part);
-  bwd_rows<T, D, NEIGHBOUR>(a, a.k, b.dko, a.ko, a.gk, a.Hkv, turns, sums, part + D);
+  bwd_rows<T, D, NEIGHBOUR>(a, a.q, b.dqo, a.qo, a.gq, a.H, turns, odd, sums, part);
+  bwd_rows<T, D, NEIGHBOUR>(a, a.k, b.dko, a.ko, a.gk, a.Hkv, turns, odd, sums, part + D);
 }
 
 template <typename T, int D, bool NEIGHBOUR>
@@ -758,11 +805,10 @@ __global__ void __launch_bounds__(THREADS, BWD_BLOCKS) norm_rope_bwd_kernel(cons
   const NormRopeArgs &a = b.fwd;
   const int warp = threadIdx.x >> 5;
   pdl_launch_dependents();  // the sums over blocks may be launched; they wait for this grid
-  for (int f = threadIdx.x; f < a.rot / 2; f += THREADS) turns[f] = turns_per_position(__ldg(a.inv_freq + f));
-  __syncthreads();
+  const bool odd = put_turns(turns, a.inv_freq, a.rot);
   part += (int64_t)blockIdx.x * 2 * D;
-  bwd_side<T, D, NEIGHBOUR>(a, a.q, b.dqo, a.qo, a.gq, a.H, plq, turns, table[warp], ring[warp], sums, part);
-  bwd_side<T, D, NEIGHBOUR>(a, a.k, b.dko, a.ko, a.gk, a.Hkv, plk, turns, table[warp], ring[warp], sums, part + D);
+  bwd_side<T, D, NEIGHBOUR>(a, a.q, b.dqo, a.qo, a.gq, a.H, plq, turns, odd, table[warp], ring[warp], sums, part);
+  bwd_side<T, D, NEIGHBOUR>(a, a.k, b.dko, a.ko, a.gk, a.Hkv, plk, turns, odd, table[warp], ring[warp], sums, part + D);
 }
 
 // dgq, dgk [D] from the blocks' sums: a block for 8 of the 2 D columns, its warps
@@ -915,9 +961,9 @@ __global__ void __launch_bounds__(THREADS, FWD_BLOCKS) norm_append_kernel(const 
   };
 #pragma unroll
   for (int i = 0; i < STAGES - 1; ++i) fetch();
-  for (int f = threadIdx.x; f < a.rot / 2; f += THREADS) turns[f] = turns_per_position(__ldg(a.inv_freq + f));
   put_weights<T, D, NEIGHBOUR>(weights, a.gq, a.gk, a.rot);
-  __syncthreads();
+  const bool odd = put_turns(turns, a.inv_freq, a.rot);
+  if (odd) spoil_weights<T, D, NEIGHBOUR>(weights, a.inv_freq, a.rot);
   Turn turn;
   Spot sp = {0, 0, 0, 0, 0};
   int of = -1, side = 0;  // the token of `table` and `sp`, the side of `out` and `turn`
@@ -970,8 +1016,7 @@ __global__ void __launch_bounds__(THREADS, ROW_BLOCKS)
   __shared__ unsigned long long turns[MAX_FREQ];
   const int lane = threadIdx.x & 31;
   const Lane ln = lane_of<T, D>(lane, a.rot);
-  for (int f = threadIdx.x; f < a.rot / 2; f += THREADS) turns[f] = turns_per_position(__ldg(a.inv_freq + f));
-  __syncthreads();
+  const bool odd = put_turns(turns, a.inv_freq, a.rot);
   float g[16];
   int of = -1;  // the side of g
   for (uint32_t pass = walk_start(); pass < qpasses + 2 * kpasses; pass += gridDim.x * WARPS) {
@@ -996,7 +1041,10 @@ __global__ void __launch_bounds__(THREADS, ROW_BLOCKS)
       }
       continue;
     }
-    if (side != of) load_weight<T, NEIGHBOUR>(side ? a.gk : a.gq, ln, g);
+    if (side != of) {
+      load_weight<T, NEIGHBOUR>(side ? a.gk : a.gq, ln, g);
+      if (odd) spoil<T, NEIGHBOUR>(a.inv_freq, a.rot, ln, g);
+    }
     of = side;
     Angles an;
     own_angles<T, NEIGHBOUR>(an, ln, a.rot, (int)sp.pos, turns);

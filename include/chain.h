@@ -450,7 +450,8 @@ int chain_fwd_fp8(const chain_tensor_t *Q, const chain_tensor_t *K,
  *              overlap another.
  *   gq, gk     [d] weights, bf16 or f32, contiguous, 16-byte aligned.
  *   inv_freq   [rot/2] f32, contiguous, |w| < 2^24; rot a multiple of 16,
- *              at most d.  NULL: no rotation (positions are then ignored).
+ *              at most d.  NULL: no rotation (positions are then ignored).  An infinite or
+ *              NaN frequency makes its pairs NaN.
  *   positions  DEVICE int32, one for each token in order, any value; NULL:
  *              the token's index in its batch entry.
  *   eps        > 0, finite.
