@@ -1090,17 +1090,21 @@ unsigned blocks_for(int64_t tokens, const Plan &pl, int per_sm) {
 }
 int batches_of(int heads, int b) { return (heads + b - 1) / b; }
 
-// Few heads: a token's rows take no more bytes than this.  32,768 tokens of bf16, by tokens and by
-// rows: forward 32.9 us and 10.3 (1 + 1 heads of 64), 32.9 and 28.8 (5 + 5), 32.9 and 36.9
-// (8 + 4), 37 and 37 (4 + 2 of 128), 44 and 49 (6 + 2); backward 47 and 14 (1 + 1 of 64), 66
-// and 63 (6 + 2 of 128), 66 and 70 (8 + 1).  Into the cache, with the values: 16 prompts of 18,600
-// tokens in all, 28.8 and 24.7 (8 + 2 of 64), 32.5 and 24.7 (4 + 1 of 128), 37 and 41 (8 + 1).
-constexpr int FEW_FWD = 1536, FEW_BWD = 2048, FEW_APPEND = 2048;
+// Few heads: a token's rows take no more bytes than this.  32,768 tokens, by tokens and by rows, in us.
+// Forward, bf16: 30.2 and 8.6 (1 + 1 heads of 64), 30.8 and 30.3 (5 + 5: 1,280 bytes), 31.5 and 34.2
+// (7 + 4), 35.4 and 25.8 (3 + 1 of 128), 35.6 and 31.7 (4 + 1: 1,280), 35.7 and 36.8 (4 + 2).  f32, whose
+// rows hold half the angles a byte: 30.6 and 23.4 (4 + 2 of 64), 31.1 and 29.5 (5 + 3: 2,048), 31.1 and 32.1
+// (6 + 3), 33.1 and 29.2 (3 + 1 of 128: 2,048), 33.7 and 35.6 (4 + 1).  Backward, bf16: 46.4 and 37.1 (8 + 1 of
+// 64), 59.4 and 63.7 (16 + 1), 63.6 and 60.8 (6 + 2 of 128: 2,048), 63.8 and 67.9 (8 + 1).  f32: 45.8 and 23.0
+// (3 + 1 of 64), 67.1 and 63.1 (10 + 4: 3,584), 70.6 and 70.9 (12 + 4), 68.1 and 63.4 (5 + 2 of 128: 3,584), 70.2 and
+// 71.2 (6 + 2).  Into the cache, bf16 with the values: 16 prompts of 18,600 tokens in all, 28.8 and 24.7
+// (8 + 2 of 64), 32.5 and 24.7 (4 + 1 of 128), 37 and 41 (8 + 1).
+constexpr int FEW_FWD[2] = {1280, 2048}, FEW_BWD[2] = {2048, 3584}, FEW_APPEND = 2048;  // bf16, f32
 bool few_heads(int64_t tokens, int heads, int head_bytes, int most) {
   return (int64_t)heads * head_bytes <= most && tokens * heads < (int64_t(1) << 31);
 }
-bool few_heads(const NormRopeArgs &a, int most) {
-  return few_heads(a.tokens, a.H + a.Hkv, a.d * (a.f32 ? 4 : 2), most);
+bool few_heads(const NormRopeArgs &a, const int (&most)[2]) {
+  return few_heads(a.tokens, a.H + a.Hkv, a.d * (a.f32 ? 4 : 2), most[a.f32 ? 1 : 0]);
 }
 template <int D>
 uint32_t row_passes(int64_t tokens, int heads) {
