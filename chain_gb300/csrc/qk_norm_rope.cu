@@ -23,7 +23,9 @@
 // is slow here, so angles are kept in turns as 64-bit fixed point: w_i / 2 pi
 // is formed once per block as an integer U_i = w_i / (2 pi) 2^64 (mod 2^64,
 // exact to one unit), and p U_i mod 2^64 is the angle of position p: exact
-// modular arithmetic whose error is |p| 2^-64 turns.
+// modular arithmetic whose error is |p| 2^-64 turns.  Its low 32 bits are dropped (2^-32 turns); the
+// rest, less its quarter turns, becomes an fp32 number of radians by one conversion (2^-28 turns) and
+// one product (2^-27 with the constant's own rounding).
 #include <algorithm>
 
 #include "internal.h"

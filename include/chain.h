@@ -455,9 +455,10 @@ int chain_fwd_fp8(const chain_tensor_t *Q, const chain_tensor_t *K,
  *   positions  DEVICE int32, one for each token in order, any value; NULL:
  *              the token's index in its batch entry.
  *   eps        > 0, finite.
- * Arithmetic: fp32, one rounding to bf16 at the store; angles p w_i exact
- * modulo a turn to within 2^-32 turns before their sine and cosine, at any
- * int32 position.  T = 0 returns CHAIN_OK and launches nothing.  Returns
+ * Arithmetic: fp32, one rounding to bf16 at the store.  Angles p w_i are taken modulo a
+ * turn in 64-bit fixed point, to within 2^-31 turns at any int32 position; what is left of a
+ * quarter turn enters the sine and cosine as an fp32 number, which adds 2^-26 turns at most.
+ * T = 0 returns CHAIN_OK and launches nothing.  Returns
  * CHAIN_ERR_DTYPE for other or mixed types, CHAIN_ERR_ARG for a shape,
  * stride, alignment or value violation.  Asynchronous on `stream`.
  */
