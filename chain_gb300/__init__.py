@@ -654,7 +654,8 @@ def attention_fwd_paged(q, k_cache, v_cache, cu_seqlens, kv_lens, page_table, ca
                         scale: float | None = None, workspace=None, stream=None):
     """Packed new tokens q [total, H, d] over a paged cache that already holds
     them.  Returns (O [total, H, d], LSE [H, total]); rows behind the last
-    sequence are not written."""
+    sequence are not written.  As many rows as sequences are taken for single
+    tokens; see include/chain.h."""
     if stream is not None:
         with _current(stream):
             return attention_fwd_paged(q, k_cache, v_cache, cu_seqlens, kv_lens, page_table, causal, scale,

@@ -124,6 +124,7 @@ struct Layout {
 struct Params {
   PagedSeqs s;
   int total, G, Hkv, causal;
+  int above, upto;             // new tokens of the sequences that this launch serves: above < n <= upto
   int tpt, utok;               // tokens of a query tile, of a unit
   int cost1, cost2, overhead;  // of a key tile against one and two query tiles, of a unit
   float scale_log2;
@@ -198,7 +199,8 @@ __device__ __forceinline__ Seq seq_of(const Params &p, int b, bool report) {
     if (report) atomicExch(&p.wc.status->reserved[0], 1);
     len = len < 0 ? 0 : most;
   }
-  return Seq{lo, hi - lo, len};
+  const int n = hi - lo;
+  return Seq{lo, n > p.above && n <= p.upto ? n : 0, len};
 }
 
 // Key tiles that tokens below `end` of the sequence see; at least one, so
@@ -1193,16 +1195,21 @@ __global__ void __launch_bounds__(32 * WARPS, TokenLayout<D, WARPS>::BLOCKS) pag
   }
 }
 
-// Whether a call's rows are few: with a query head's group that fits 16 rows, no more new
-// tokens than sequences, or so few that they fit one tile.  (The counts themselves are on the
-// device.  A sequence with more tokens than a tile, in such a call, is served by several units,
-// which read its keys once each.)  Single tokens, 8 K/V heads, this kernel and the one above: 64
-// sequences of 300 at d = 64 17.5 us and 39.7; of 1,000 at d = 128 40 and 48 (40 sequences), of
-// 2,000 100 and 106, of 4,000 186 and 183, of 8,000 357 and 337, where only the memory is
-// left and the other kernel's larger copies serve it better.  One sequence of 100: 6.3 and 9.5, of
-// 4,096: 12.8 and 16.2, of 65,536: 56.8 and 58.8.
+// Whether a call's rows may be few: with a query head's group that fits 16 rows, no more new
+// tokens than sequences, or so few that they fit one tile.  Single tokens, 8 K/V heads, this kernel
+// and the one above: 64 sequences of 300 at d = 64 19.4 us and 36, at d = 128 27 and 53; of 2,000 100 and 133;
+// of 300 and 200 sequences 62 and 140.
 bool few_rows(const PagedAttnArgs &a, int G) {
   return G <= TOK_ROWS && (a.total <= a.seqs.batch || (int64_t)a.total * G <= TOK_ROWS);
+}
+// The counts themselves are on the device.  As many tokens as sequences are single tokens but for a
+// coincidence; fewer may be a chunk in a batch that is padded with empty sequences, whose keys 16-row
+// tiles would read once for every 16 rows.  Then sequences of more than two tiles are left to a launch
+// of the kernel above, which finds nothing to do where there are none (32 heads on 8, d = 128, a batch
+// of 256 padded with empty sequences: 200 tokens over 8,192 keys 61 us, 217 without that launch; 64 single
+// tokens over 300 keys 33 and 28).
+bool may_have_chunks(const PagedAttnArgs &a, int G) {
+  return a.total < a.seqs.batch && (int64_t)a.total * G > 2 * TOK_ROWS;
 }
 
 // Joins a unit that runs' ends cut into parts: block (c, y) the unit that
@@ -1364,9 +1371,10 @@ cudaError_t launch_join(const PagedAttnArgs &a, const Params &p, cudaStream_t st
 }
 
 template <int D, int WARPS>
-cudaError_t launch_tokens(const PagedAttnArgs &a, Params &p, cudaStream_t st) {
+cudaError_t launch_tokens(const PagedAttnArgs &a, Params p, cudaStream_t st) {
   using L = TokenLayout<D, WARPS>;
   p.tpt = p.utok = TOK_ROWS / p.G;
+  if (may_have_chunks(a, p.G)) p.upto = 2 * p.utok;
   p.cost1 = p.cost2 = L::COST;
   p.overhead = L::OVERHEAD;
   uint8_t *ws = static_cast<uint8_t *>(a.workspace);
@@ -1403,6 +1411,8 @@ cudaError_t launch(const PagedAttnArgs &a, const WaitCfg &wc, cudaStream_t st) {
   p.tpt = BM / p.G;
   p.utok = 2 * p.tpt;
   p.causal = a.causal;
+  p.above = 0;
+  p.upto = a.total;
   p.cost1 = L::COST1;
   p.cost2 = L::COST2;
   p.overhead = L::OVERHEAD;
@@ -1425,8 +1435,14 @@ cudaError_t launch(const PagedAttnArgs &a, const WaitCfg &wc, cudaStream_t st) {
   // Few units are spread over the warps of one block an SM, more over two blocks, whose starts and
   // ends overlap (1,000 keys a sequence, 8 K/V heads: 2 sequences 10.8 us, 13.5 with two blocks;
   // 4 sequences 11.8 and 12.3; 8 15.6 and 14.2; 16 21.5 and 19.2)
-  if (few_rows(a, p.G))
-    return (int64_t)a.seqs.batch * p.Hkv <= CTAS / 3 ? launch_tokens<D, 8>(a, p, st) : launch_tokens<D, 4>(a, p, st);
+  cudaError_t e;
+  int mark = 0;  // kernel boundaries so far
+  if (few_rows(a, p.G)) {
+    e = (int64_t)a.seqs.batch * p.Hkv <= CTAS / 3 ? launch_tokens<D, 8>(a, p, st) : launch_tokens<D, 4>(a, p, st);
+    if (e != cudaSuccess || !may_have_chunks(a, p.G)) return e;
+    p.above = 2 * (TOK_ROWS / p.G);
+    mark = 1;
+  }
   // Q: {d, head, token}, a tile's box G heads of TPT tokens.  Strides of
   // extents of one are not given: any valid value does.
   CUtensorMap mq, mk, mv;
@@ -1447,17 +1463,16 @@ cudaError_t launch(const PagedAttnArgs &a, const WaitCfg &wc, cudaStream_t st) {
   // At d = 128 the row is the 256 bytes (64 sequences of 8,192: 341 us, 343 with 128).
   const CUtensorMapL2promotion promote =
       D == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
-  cudaError_t e;
   if ((e = make_tmap(&mq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.Q, dq, sq, bq)) != cudaSuccess ||
       (e = make_tmap(&mk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, a.kc.ptr, dk, sk, bk, promote)) != cudaSuccess ||
       (e = make_tmap(&mv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, a.vc.ptr, dk, sv, bk, promote)) != cudaSuccess)
     return e;
   e = cudaFuncSetAttribute(paged_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC);
   if (e != cudaSuccess) return e;
-  timing_mark(st, 0);
+  if (mark == 0) timing_mark(st, 0);
   paged_attn_kernel<D><<<CTAS, THREADS, L::ALLOC, st>>>(mq, mk, mv, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  timing_mark(st, 1);
+  timing_mark(st, mark + 1);
   return launch_join<D, CTAS, 2 * BM>(a, p, st);
 }
 

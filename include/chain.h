@@ -567,9 +567,10 @@ int chain_qk_norm_rope_append(const chain_tensor_t *Q, const chain_tensor_t *K,
  * Arithmetic: Q K^T, the softmax's statistics and P V accumulate in fp32;
  * P enters the P V product as a pair of bf16 (P and what its rounding left), as in
  * chain_fwd, so that O's own rounding is the only one to bf16.  A call with H / Hkv at most 16 and total at
- * most batch is taken for one of single tokens: a longer chunk in it, beside as many
- * sequences without new tokens, is right too but reads its keys once for every
- * 16 / (H / Hkv) of its tokens, so such sequences are better left out of the batch.
+ * most batch is taken for one of single tokens.  With total below batch, as in a batch
+ * that is padded with empty sequences, a second launch serves longer chunks among them; with
+ * total equal to batch a longer chunk beside as many sequences without new tokens is right too, but
+ * reads its keys once for every 16 / (H / Hkv) of its tokens.
  * batch at most 8192 (else CHAIN_ERR_UNSUPPORTED).  total = 0 or batch = 0 returns CHAIN_OK and
  * launches nothing.  Asynchronous on `stream`.
  * chain_fwd_paged_workspace_size returns 0 for a Q or Kc it cannot take.
