@@ -42,13 +42,13 @@
 // Calls of single tokens go to paged_token_kernel, further down, which shares the split.
 //
 // Bounds, and what was measured (32 heads on 8, pages of 64 to 128):
-//   chunks: the chain of softmax and products.  d = 128, 2,048 tokens over 32,768: 1,095 us,
-//   970 TFLOP/s (P_lo's product not counted), against 775 with one bf16 of P: a stream's softmax and
-//   its three products follow each other, since P shares S's columns; two streams overlap them.
-//   d = 64: 771 us, 690 TFLOP/s.
-//   single tokens: memory.  d = 128, 64 sequences of 8,192: 360 us, 2.15 GB at 6.0 TB/s;
-//   d = 64: 197 us, 1.07 GB at 5.5 TB/s.  One sequence of 131,072: 102 us, 5.3 TB/s, with
-//   the start, the join and the ends of the runs; of 100: 6.3 us, all latency.
+//   chunks: the chain of softmax and products.  d = 128, 2,048 tokens over 32,768: 1,090 us,
+//   980 TFLOP/s (P_lo's product not counted; 775 us with one bf16 of P), the tensor pipe 61% busy: a
+//   stream's softmax and its three products follow each other, since P shares S's columns; two
+//   streams overlap them.  d = 64: 765 us, 700 TFLOP/s, the tensor pipe 39% busy.
+//   single tokens: memory.  d = 128, 64 sequences of 8,192: 363 us, 2.15 GB at 5.9 TB/s;
+//   d = 64: 196 us, 1.07 GB at 5.5 TB/s.  One sequence of 131,072: 99 us, 5.4 TB/s, with
+//   the start, the join and the ends of the runs; of 100: 6.4 us, all latency.
 #include <atomic>
 
 #include "internal.h"
@@ -1196,9 +1196,10 @@ __global__ void __launch_bounds__(32 * WARPS, TokenLayout<D, WARPS>::BLOCKS) pag
 }
 
 // Whether a call's rows may be few: with a query head's group that fits 16 rows, no more new
-// tokens than sequences, or so few that they fit one tile.  Single tokens, 8 K/V heads, this kernel
-// and the one above: 64 sequences of 300 at d = 64 19.4 us and 36, at d = 128 27 and 53; of 2,000 100 and 133;
-// of 300 and 200 sequences 62 and 140.
+// tokens than sequences, or so few that they fit one tile.  Single tokens, 32 heads on 8, this kernel
+// and the one above: 64 sequences of 300 at d = 64 19.5 us and 44.1, at d = 128 27.2 and 53.3; of
+// 1,000 57 and 90, of 4,000 190 and 212, of 8,192 366 and 369 (d = 64 206 and 252); 200 of 300 62 and 140.
+// One sequence of 100: 6.4 and 11.9, of 4,096: 14.6 and 19.7, of 131,072: 101 and 107.
 bool few_rows(const PagedAttnArgs &a, int G) {
   return G <= TOK_ROWS && (a.total <= a.seqs.batch || (int64_t)a.total * G <= TOK_ROWS);
 }
@@ -1458,9 +1459,9 @@ cudaError_t launch(const PagedAttnArgs &a, const WaitCfg &wc, cudaStream_t st) {
   const uint64_t sv[3] = {(uint64_t)a.vc.s_slot * 2, (uint64_t)a.vc.s_head * 2, (uint64_t)a.vc.s_page * 2};
   const uint32_t bk[4] = {64, (uint32_t)(page < BN ? page : BN), 1, 1};
   // A token's row of one K/V head is 128 bytes at d = 64, and the bytes after it belong to
-  // another head, which another unit reads much later: fetched 256 at a time, half of the
-  // traffic is for nothing (64 sequences of 32,768 keys, 8 K/V heads: 885 us, against 637).
-  // At d = 128 the row is the 256 bytes (64 sequences of 8,192: 341 us, 343 with 128).
+  // another head, which another unit reads much later: fetched 256 at a time, they are read for
+  // nothing (single tokens of 64 sequences of 8,192 keys, 64 heads on 2: 75 us, 79 with 256).  At
+  // d = 128 the row is the 256 bytes.
   const CUtensorMapL2promotion promote =
       D == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
   if ((e = make_tmap(&mq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.Q, dq, sq, bq)) != cudaSuccess ||

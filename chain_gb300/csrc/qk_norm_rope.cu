@@ -12,12 +12,12 @@
 // Everything between the load and the store is fp32; the one rounding to
 // bf16 is the store's.  Both passes read each input once and write each
 // output once, so memory bandwidth bounds them: 32 + 8 heads of d = 128, 32,768
-// tokens, bf16: the forward 105 us (0.67 GB, 6.4 TB/s; a copy of the same bytes takes 100),
-// the backward 160 us (1.01 GB, 6.3 TB/s), 16 prompts of 18,632 tokens in all into the
-// cache 79 us (0.46 GB, 5.8 TB/s).  At d = 64 a token's angles are shared by half as many
-// bytes and the arithmetic shows: backward 92 us of 0.5 GB.  A few tokens take what a
-// launch takes: 4 us, two launches with the sums of a weight's gradient 8.  With few heads the
-// angles bound it: 32,768 tokens of 3 + 1 heads of 128 25 us, where the bytes take 10.
+// tokens, bf16: the forward 103 us (0.67 GB, 6.5 TB/s; a copy of the same bytes takes 100),
+// the backward 157 us (1.01 GB, 6.4 TB/s), 16 prompts of 18,632 tokens in all into the
+// cache 77 us (0.46 GB, 5.9 TB/s).  At d = 64 a token's angles are shared by half as many
+// bytes and the arithmetic shows: backward 80 us of 0.46 GB.  A few tokens take what a
+// launch takes: 3 to 4 us, two launches with the sums of a weight's gradient 6 to 8.  With few heads
+// the angles bound it: 32,768 tokens of 3 + 1 heads of 128 26 us, where the bytes take 10.
 //
 // Angles.  p w_i mod 2 pi keeps no fp32 accuracy at far positions, and fp64
 // is slow here, so angles are kept in turns as 64-bit fixed point: w_i / 2 pi
@@ -107,7 +107,7 @@ __device__ __forceinline__ bool put_turns(unsigned long long *turns, const float
 // four f32), and the lanes' parts lie side by side: with n lanes, lane l's part j is the
 // (j n + l)th, so that a warp's access covers whole sectors.  (Sixteen elements in a row a
 // lane, forward of 40 heads of d = 128: pairs (2i, 2i + 1) of 32,768 tokens in bf16 150 us,
-// 118 so; 16,384 tokens in f32 149 us, 110 so; the backward gains as much again.)  The lanes
+// 102 so; 16,384 tokens in f32 149 us, 108 so.  The f32 backward of as many takes 160.)  The lanes
 // of the rotated elements and those of the others are dealt apart; pairs (i, i + rot/2)
 // then lie in one lane, as pairs (2i, 2i + 1) do, and a rotation needs no other lane.  (With
 // eight elements a lane, the reduction, the addressing and the loop cost twice as much for
