@@ -188,6 +188,10 @@ def prepare(case, seed):
         s["rows"] = sum(n for n, _ in lens) + case["pad"]
         if own:
             import chain_gb300
+            # a program that steps keeps the arrays of its step, and the scratch
+            i32 = lambda n: torch.empty(n, dtype=torch.int32, device="cuda")
+            s["out"] = (i32(case["batch"] + 1), i32(case["batch"]), i32(1), i32(s["rows"]),
+                        torch.empty(s["rows"], dtype=torch.int64, device="cuda"))
             s["workspace"] = torch.empty(chain_gb300.chain_page_plan_workspace_size(case["batch"]),
                                          dtype=torch.uint8, device="cuda")
         return s
@@ -202,6 +206,7 @@ def prepare(case, seed):
         s["pool"] = sum(need) + 5
         if own:
             import chain_gb300
+            s["out"] = (torch.empty_like(s["kv"]), torch.empty_like(s["count"]))
             s["workspace"] = torch.empty(chain_gb300.chain_page_trim_workspace_size(case["batch"]),
                                          dtype=torch.uint8, device="cuda")
         return s
@@ -237,7 +242,8 @@ def prepare(case, seed):
     s["start"] = _ints(start)
     if own:
         import chain_gb300
-        # the scratch of the attention, kept by a program that decodes
+        # the outputs and the scratch of the attention, kept by a program that decodes
+        s["o"], s["lse"] = torch.empty_like(s["q"]), torch.empty(H, s["q"].shape[0], device="cuda")
         s["workspace"] = torch.empty(chain_gb300.chain_fwd_paged_prefix_workspace_size(s["q"], s["kc"]),
                                      dtype=torch.uint8, device="cuda")
     return s
@@ -362,12 +368,14 @@ def run(s):
     import chain_gb300 as cg
     if op == "plan":
         return (*cg.page_plan(s["new"], s["kv"], s["table"], s["free"], s["count"], s["case"]["page"], s["rows"],
-                              workspace=s["workspace"]), s["table"])
+                              out=s["out"], workspace=s["workspace"]), s["table"])
     if op == "trim":
         return (*cg.page_trim(s["keep"], s["kv"], s["table"], s["free"], s["count"], s["case"]["page"], s["pool"],
-                              workspace=s["workspace"]), s["free"])
-    return cg.attention_fwd_paged_prefix(s["q"], s["kc"], s["vc"], s["cu"], s["lens"], s["table"], s["prefix_cu"],
-                                         s["prefix_lens"], causal=s["case"]["causal"], workspace=s["workspace"])
+                              out=s["out"], workspace=s["workspace"]), s["free"])
+    cg.chain_fwd_paged_prefix(s["q"], s["kc"], s["vc"], s["cu"], s["lens"], s["table"], s["prefix_cu"],
+                              s["prefix_lens"], cg.MASK_CAUSAL if s["case"]["causal"] else cg.MASK_NONE,
+                              s["q"].shape[2] ** -0.5, s["o"], s["lse"], s["workspace"])
+    return s["o"], s["lse"]
 
 
 # ------------------------------------------------------------- the definition, 64 bits
