@@ -19,10 +19,14 @@ Entry points (same names as the C ABI):
                             Kc, Vc, Qo, stream=None)
   chain_fwd_paged(Q, Kc, Vc, cu_seqlens, kv_lens, page_table, mask, scale, O, LSE, workspace,
                   stream=None)
+  chain_page_plan(new_lens, kv_lens, page_table, free_pages, free_count, page, cu_seqlens, kv_out,
+                  count_out, positions, slots, workspace, stream=None)
+  chain_page_trim(keep_lens, kv_lens, page_table, free_pages, free_count, page, num_pages, kv_out,
+                  count_out, workspace, stream=None)
   chain_check(stream=None)
 plus allocating conveniences ``attention_fwd``, ``attention_bwd``,
 ``mlp_chain_fwd``, ``relayout``, ``qk_norm_rope``, ``qk_norm_rope_bwd``,
-``qk_norm_rope_append`` and ``attention_fwd_paged``.
+``qk_norm_rope_append``, ``attention_fwd_paged``, ``page_plan`` and ``page_trim``.
 """
 from __future__ import annotations
 
@@ -111,6 +115,12 @@ def _load():
             lib.chain_qk_norm_rope_append.argtypes = [P, P, P, P, P, P, fl, ci, vp, vp, vp, i64, ci, ci,
                                                       P, P, P, vp]
             lib.chain_fwd_paged.argtypes = [P, P, P, vp, vp, vp, i64, ci, ci, ci, fl, P, P, vp, sz, vp]
+            lib.chain_page_plan.argtypes = [vp, vp, vp, i64, ci, ci, ci, vp, i64, vp, vp, vp, vp, vp, vp, i64, vp,
+                                            sz, vp]
+            lib.chain_page_trim.argtypes = [vp, vp, vp, i64, ci, ci, ci, i64, vp, i64, vp, vp, vp, vp, sz, vp]
+            for fn in ("chain_page_plan_workspace_size", "chain_page_trim_workspace_size"):
+                getattr(lib, fn).argtypes = [ci]
+                getattr(lib, fn).restype = sz
             for fn, n in (("chain_qk_norm_rope_bwd_workspace_size", 1),
                           ("chain_fwd_paged_workspace_size", 2)):
                 getattr(lib, fn).argtypes = [P] * n
@@ -130,7 +140,8 @@ def _load():
                        "chain_bwd_noalloc", "chain_fwd_fp8", "chain_fwd_f16pv",
                        "chain_fwd_sp_f16pv",
                        "chain_qk_norm_rope", "chain_qk_norm_rope_bwd", "chain_paged_append",
-                       "chain_qk_norm_rope_append", "chain_fwd_paged",
+                       "chain_qk_norm_rope_append", "chain_fwd_paged", "chain_page_plan",
+                       "chain_page_trim",
                        "sp_relayout",
                        "sp_relayout_inverse",
                        "chain_check", "chain_selftest_wait_timeout", "chain_umma_selftest",
@@ -343,7 +354,7 @@ def _small():
         if not os.path.exists(_build.NATIVE):
             _build.build_native()
         from . import _native
-        _native.setup(torch.bfloat16, torch.float32, torch.int32, ChainError)
+        _native.setup(torch.bfloat16, torch.float32, torch.int32, torch.int64, ChainError)
         _calls = _native
     return _calls
 
@@ -398,6 +409,28 @@ def chain_fwd_paged(Q, Kc, Vc, cu_seqlens, kv_lens, page_table, mask, scale, O, 
     """Attention of a chunk of new tokens over a paged cache; see include/chain.h."""
     _small().fwd_paged(Q, Kc, Vc, cu_seqlens, kv_lens, page_table, mask, scale, O, LSE, workspace,
                        _bytes(workspace), *_where(stream))
+
+
+def chain_page_plan_workspace_size(batch) -> int:
+    return int(_load().chain_page_plan_workspace_size(int(batch)))
+
+
+def chain_page_plan(new_lens, kv_lens, page_table, free_pages, free_count, page, cu_seqlens, kv_out, count_out,
+                    positions, slots, workspace, stream=None):
+    """Pages for a step's new tokens, and its index arrays; see include/chain.h."""
+    _small().page_plan(new_lens, kv_lens, page_table, free_pages, free_count, page, cu_seqlens, kv_out, count_out,
+                       positions, slots, workspace, _bytes(workspace), *_where(stream))
+
+
+def chain_page_trim_workspace_size(batch) -> int:
+    return int(_load().chain_page_trim_workspace_size(int(batch)))
+
+
+def chain_page_trim(keep_lens, kv_lens, page_table, free_pages, free_count, page, num_pages, kv_out, count_out,
+                    workspace, stream=None):
+    """Cuts sequences and puts their pages back on the stack; see include/chain.h."""
+    _small().page_trim(keep_lens, kv_lens, page_table, free_pages, free_count, page, num_pages, kv_out, count_out,
+                       workspace, _bytes(workspace), *_where(stream))
 
 
 def sp_relayout(shards, p, head_group, out, stream=None):
@@ -669,3 +702,40 @@ def attention_fwd_paged(q, k_cache, v_cache, cu_seqlens, kv_lens, page_table, ca
     chain_fwd_paged(q, k_cache, v_cache, cu_seqlens, kv_lens, page_table,
                     MASK_CAUSAL if causal else MASK_NONE, scale, o, lse, workspace)
     return o, lse
+
+
+def page_plan(new_lens, kv_lens, page_table, free_pages, free_count, page: int, rows: int, out=None, workspace=None,
+              stream=None):
+    """Pages for the new tokens [batch] of sequences with kv_lens [batch] cached positions: fills page_table
+    [batch, max_pages] from the stack free_pages[:free_count].  Returns (cu_seqlens [batch + 1], kv_lens,
+    free_count, positions [rows], slots [rows]), what the cache's calls and a program's own kernels take;
+    `out` gives these five tensors (kv_lens and free_count themselves keep the state in place)."""
+    if stream is not None:
+        with _current(stream):
+            return page_plan(new_lens, kv_lens, page_table, free_pages, free_count, page, rows, out, workspace)
+    if out is None:
+        new = kv_lens.new_empty
+        out = (new(kv_lens.shape[0] + 1), new(kv_lens.shape[0]), new(1), new(rows), new(rows, dtype=torch.int64))
+    if out[3].shape[0] != rows:
+        raise ValueError(f"positions and slots must have {rows} entries")
+    if workspace is None:
+        workspace = torch.empty(max(chain_page_plan_workspace_size(kv_lens.shape[0]), 16), dtype=torch.uint8,
+                                device=kv_lens.device)
+    chain_page_plan(new_lens, kv_lens, page_table, free_pages, free_count, page, *out, workspace)
+    return tuple(out)
+
+
+def page_trim(keep_lens, kv_lens, page_table, free_pages, free_count, page: int, num_pages: int, out=None,
+              workspace=None, stream=None):
+    """Cuts sequences to keep_lens [batch] positions; the pages behind go back on the stack free_pages, in
+    place.  Returns (kv_lens, free_count); `out` gives these two tensors (or kv_lens and free_count themselves)."""
+    if stream is not None:
+        with _current(stream):
+            return page_trim(keep_lens, kv_lens, page_table, free_pages, free_count, page, num_pages, out, workspace)
+    if out is None:
+        out = (torch.empty_like(kv_lens), torch.empty_like(free_count))
+    if workspace is None:
+        workspace = torch.empty(max(chain_page_trim_workspace_size(kv_lens.shape[0]), 16), dtype=torch.uint8,
+                                device=kv_lens.device)
+    chain_page_trim(keep_lens, kv_lens, page_table, free_pages, free_count, page, num_pages, *out, workspace)
+    return tuple(out)

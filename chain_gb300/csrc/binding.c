@@ -12,16 +12,17 @@
 #include "../../include/chain.h"
 
 static PyObject *s_data_ptr, *s_dtype, *s_shape, *s_stride, *s_get_device, *s_is_contiguous;
-static PyObject *t_bf16, *t_f32, *t_i32, *chain_error;
+static PyObject *t_bf16, *t_f32, *t_i32, *t_i64, *chain_error;
 
-/* chain_gb300._native.setup(torch.bfloat16, torch.float32, torch.int32, ChainError) */
+/* chain_gb300._native.setup(torch.bfloat16, torch.float32, torch.int32, torch.int64, ChainError) */
 static PyObject *setup(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   (void)self;
-  if (n != 4) return PyErr_Format(PyExc_TypeError, "setup takes four arguments");
+  if (n != 5) return PyErr_Format(PyExc_TypeError, "setup takes five arguments");
   Py_XSETREF(t_bf16, Py_NewRef(a[0]));
   Py_XSETREF(t_f32, Py_NewRef(a[1]));
   Py_XSETREF(t_i32, Py_NewRef(a[2]));
-  Py_XSETREF(chain_error, Py_NewRef(a[3]));
+  Py_XSETREF(t_i64, Py_NewRef(a[3]));
+  Py_XSETREF(chain_error, Py_NewRef(a[4]));
   Py_RETURN_NONE;
 }
 
@@ -88,18 +89,18 @@ static int tensor(PyObject *t, long dev, int optional, chain_tensor_t *d, chain_
   return 0;
 }
 
-/* int32 index array of `nd` dimensions, innermost contiguous */
-static int indices(PyObject *t, long dev, const char *what, int nd, void **ptr, int64_t *shape,
-                   int64_t *stride) {
+/* Index array of `nd` dimensions, innermost contiguous: int32, or int64 where `wide` */
+static int index_array(PyObject *t, long dev, const char *what, int wide, int nd, void **ptr, int64_t *shape,
+                       int64_t *stride) {
   PyObject *dt = PyObject_GetAttr(t, s_dtype);
   if (!dt) return -1;
-  const int ok = dt == t_i32;
+  const int ok = dt == (wide ? t_i64 : t_i32);
   Py_DECREF(dt);
   if (on_device(t, dev) || address(t, ptr)) return -1;
   const int n = read_sizes(PyObject_GetAttr(t, s_shape), shape, nd);
   if (n < 0 || read_sizes(PyObject_CallMethodNoArgs(t, s_stride), stride, nd) < 0) return -1;
   if (!ok || n != nd) {
-    PyErr_Format(PyExc_ValueError, "%s must be a CUDA int32 tensor of %d dimension%s", what, nd,
+    PyErr_Format(PyExc_ValueError, "%s must be a CUDA %s tensor of %d dimension%s", what, wide ? "int64" : "int32", nd,
                  nd > 1 ? "s" : "");
     return -1;
   }
@@ -107,6 +108,22 @@ static int indices(PyObject *t, long dev, const char *what, int nd, void **ptr, 
     PyErr_Format(PyExc_ValueError, "%s must be contiguous", what);
     return -1;
   }
+  return 0;
+}
+
+static int indices(PyObject *t, long dev, const char *what, int nd, void **ptr, int64_t *shape, int64_t *stride) {
+  return index_array(t, dev, what, 0, nd, ptr, shape, stride);
+}
+
+/* One dimension of `len` entries, or of any number of them where it is -1, which is then returned in it. */
+static int row_of(PyObject *t, long dev, const char *what, int wide, int64_t *len, void **ptr) {
+  int64_t shape[1], stride[1];
+  if (index_array(t, dev, what, wide, 1, ptr, shape, stride)) return -1;
+  if (*len >= 0 && shape[0] != *len) {
+    PyErr_Format(PyExc_ValueError, "%s must have %lld entries, not %lld", what, (long long)*len, (long long)shape[0]);
+    return -1;
+  }
+  *len = shape[0];
   return 0;
 }
 
@@ -346,10 +363,79 @@ static PyObject *fwd_paged(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   return done(rc, "chain_fwd_paged");
 }
 
+/* What a plan and a trim share: lengths, the table and the stack. */
+typedef struct {
+  void *lens, *kv, *table, *free, *count, *kv_out, *count_out, *ws;
+  int64_t batch, stride, capacity;
+  int max_pages;
+} pages_t;
+
+static int pages(PyObject *lens, const char *what, PyObject *kv, PyObject *table, PyObject *free_, PyObject *count_,
+                 PyObject *kv_out, PyObject *count_out, PyObject *ws, long dev, pages_t *p) {
+  int64_t st[2], tt[2], one = 1;
+  p->batch = p->capacity = -1;
+  if (row_of(lens, dev, what, 0, &p->batch, &p->lens) || row_of(kv, dev, "kv_lens", 0, &p->batch, &p->kv) ||
+      indices(table, dev, "page_table", 2, &p->table, st, tt) ||
+      row_of(free_, dev, "free_pages", 0, &p->capacity, &p->free) ||
+      row_of(count_, dev, "free_count", 0, &one, &p->count) ||
+      row_of(kv_out, dev, "the new kv_lens", 0, &p->batch, &p->kv_out) ||
+      row_of(count_out, dev, "the new free_count", 0, &one, &p->count_out) || workspace(ws, dev, &p->ws))
+    return -1;
+  if (st[0] != p->batch || p->batch > 0x7fffffff || st[1] > 0x7fffffff) {
+    PyErr_SetString(PyExc_ValueError, "page_table [batch][max_pages] and the lengths [batch] must agree on the batch");
+    return -1;
+  }
+  p->max_pages = (int)st[1];
+  p->stride = p->batch > 1 ? tt[0] : st[1];
+  return 0;
+}
+
+static PyObject *page_plan(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+  (void)self;
+  if (count(n, 15, "chain_page_plan")) return NULL;
+  DEV_STREAM(13);
+  pages_t p;
+  void *cu, *positions_, *slots;
+  int64_t rows = -1;
+  if (pages(a[0], "new_lens", a[1], a[2], a[3], a[4], a[7], a[8], a[11], dev, &p)) return NULL;
+  int64_t ends = p.batch + 1;
+  if (row_of(a[6], dev, "cu_seqlens", 0, &ends, &cu) || row_of(a[9], dev, "positions", 0, &rows, &positions_) ||
+      row_of(a[10], dev, "slots", 1, &rows, &slots))
+    return NULL;
+  const long page = PyLong_AsLong(a[5]);
+  const size_t bytes = PyLong_AsSize_t(a[12]);
+  if (PyErr_Occurred()) return NULL;
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = chain_page_plan(p.lens, p.kv, p.table, p.stride, (int)p.batch, p.max_pages, (int)page, p.free, p.capacity,
+                       p.count, cu, p.kv_out, p.count_out, positions_, slots, rows, p.ws, bytes, stream);
+  Py_END_ALLOW_THREADS
+  return done(rc, "chain_page_plan");
+}
+
+static PyObject *page_trim(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+  (void)self;
+  if (count(n, 13, "chain_page_trim")) return NULL;
+  DEV_STREAM(11);
+  pages_t p;
+  if (pages(a[0], "keep_lens", a[1], a[2], a[3], a[4], a[7], a[8], a[9], dev, &p)) return NULL;
+  const long page = PyLong_AsLong(a[5]);
+  const long long pool = PyLong_AsLongLong(a[6]);
+  const size_t bytes = PyLong_AsSize_t(a[10]);
+  if (PyErr_Occurred()) return NULL;
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = chain_page_trim(p.lens, p.kv, p.table, p.stride, (int)p.batch, p.max_pages, (int)page, pool, p.free,
+                       p.capacity, p.count, p.kv_out, p.count_out, p.ws, bytes, stream);
+  Py_END_ALLOW_THREADS
+  return done(rc, "chain_page_trim");
+}
+
 #define METHOD(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, NULL}
 static PyMethodDef methods[] = {METHOD(setup),        METHOD(qk_norm_rope),        METHOD(qk_norm_rope_bwd),
                                 METHOD(paged_append), METHOD(qk_norm_rope_append), METHOD(fwd_paged),
                                 METHOD(qk_norm_rope_bwd_workspace_size),
+                                METHOD(page_plan),    METHOD(page_trim),
                                 {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", NULL, -1, methods, NULL, NULL, NULL, NULL};
 

@@ -1181,6 +1181,78 @@ int chain_fwd_paged(const chain_tensor_t *Q, const chain_tensor_t *Kc, const cha
   return e == cudaSuccess ? CHAIN_OK : cuda_fail(e);
 }
 
+// What a plan and a trim share: a table and its geometry, a stack, outputs and a workspace.
+static int page_args(int batch, const void *const *arrays, int count, int64_t stride, int max_pages, int page,
+                     int64_t capacity, const void *workspace, size_t ws_bytes, size_t need, int *shift) {
+  if (batch < 0 || max_pages < 1 || capacity < 0 || capacity > 0x7fffffff) return CHAIN_ERR_ARG;
+  if (page < 16 || page > 1024 || (page & (page - 1)) || batch > kMaxPagedBatch) return CHAIN_ERR_UNSUPPORTED;
+  *shift = 0;
+  while ((1 << *shift) < page) ++*shift;
+  if (((int64_t)max_pages << *shift) > (1 << 30)) return CHAIN_ERR_ARG;
+  if ((batch > 1 && stride < max_pages) || stride < 0) return CHAIN_ERR_ARG;
+  for (int i = 0; i < count; ++i)
+    if (!arrays[i] || !aligned4(arrays[i])) return CHAIN_ERR_ARG;
+  if (!workspace || !aligned16(workspace) || ws_bytes < need) return CHAIN_ERR_ARG;
+  return CHAIN_OK;
+}
+
+size_t chain_page_plan_workspace_size(int batch) {
+  return batch < 0 || batch > kMaxPagedBatch ? 0 : page_plan_workspace(batch);
+}
+
+int chain_page_plan(const int32_t *new_lens, const int32_t *kv_lens, int32_t *page_table,
+                    int64_t page_table_stride, int batch, int max_pages, int page, const int32_t *free_pages,
+                    int64_t capacity, const int32_t *free_count, int32_t *cu_seqlens, int32_t *kv_lens_out,
+                    int32_t *free_count_out, int32_t *positions, int64_t *slots, int64_t rows, void *workspace,
+                    size_t ws_bytes, void *stream) {
+  const void *const arrays[8] = {free_count, cu_seqlens, free_count_out, new_lens, kv_lens, page_table, kv_lens_out,
+                                 free_pages};
+  PagePlanArgs a = {};
+  if (rows < 0 || rows >= (1 << 30)) return CHAIN_ERR_ARG;
+  // without sequences there are no lengths and no table, without a stack no entries
+  const int used = batch == 0 ? 3 : (capacity == 0 ? 7 : 8);
+  if (int rc = page_args(batch, arrays, used, page_table_stride, max_pages, page, capacity, workspace, ws_bytes,
+                         page_plan_workspace(batch < 0 || batch > kMaxPagedBatch ? 0 : batch), &a.page_shift))
+    return rc;
+  if (rows > 0 && (!positions || !aligned4(positions) || !slots || (reinterpret_cast<uintptr_t>(slots) & 7u)))
+    return CHAIN_ERR_ARG;
+  a.new_lens = new_lens; a.kv_lens = kv_lens; a.table = page_table; a.table_stride = page_table_stride;
+  a.batch = batch; a.max_pages = max_pages; a.free_pages = free_pages; a.free_count = free_count;
+  a.capacity = capacity; a.cu = cu_seqlens; a.kv_out = kv_lens_out; a.count_out = free_count_out;
+  a.positions = positions; a.slots = reinterpret_cast<long long *>(slots); a.rows = rows; a.workspace = workspace;
+  DevInfo *di = nullptr;
+  if (int rc = device_ready(&di)) return rc;
+  a.status = di->status;
+  cudaError_t e = launch_page_plan(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? CHAIN_OK : cuda_fail(e);
+}
+
+size_t chain_page_trim_workspace_size(int batch) {
+  return batch < 0 || batch > kMaxPagedBatch ? 0 : page_trim_workspace(batch);
+}
+
+int chain_page_trim(const int32_t *keep_lens, const int32_t *kv_lens, const int32_t *page_table,
+                    int64_t page_table_stride, int batch, int max_pages, int page, int64_t num_pages,
+                    int32_t *free_pages, int64_t capacity, const int32_t *free_count, int32_t *kv_lens_out,
+                    int32_t *free_count_out, void *workspace, size_t ws_bytes, void *stream) {
+  const void *const arrays[7] = {free_count, free_count_out, keep_lens, kv_lens, page_table, kv_lens_out, free_pages};
+  PageTrimArgs a = {};
+  if (num_pages < 0 || num_pages > 0x7ffffffe) return CHAIN_ERR_ARG;
+  const int used = batch == 0 ? 2 : (capacity == 0 ? 6 : 7);
+  if (int rc = page_args(batch, arrays, used, page_table_stride, max_pages, page, capacity, workspace, ws_bytes,
+                         page_trim_workspace(batch < 0 || batch > kMaxPagedBatch ? 0 : batch), &a.page_shift))
+    return rc;
+  a.keep = keep_lens; a.kv_lens = kv_lens; a.table = page_table; a.table_stride = page_table_stride;
+  a.batch = batch; a.max_pages = max_pages; a.num_pages = num_pages; a.free_pages = free_pages;
+  a.free_count = free_count; a.capacity = capacity; a.kv_out = kv_lens_out; a.count_out = free_count_out;
+  a.workspace = workspace;
+  DevInfo *di = nullptr;
+  if (int rc = device_ready(&di)) return rc;
+  a.status = di->status;
+  cudaError_t e = launch_page_trim(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? CHAIN_OK : cuda_fail(e);
+}
+
 int sp_relayout(const chain_tensor_t *shards, int p, int head_group, chain_tensor_t *out,
                 void *stream) {
   return relayout_common(shards, out, p, head_group, 0, stream);

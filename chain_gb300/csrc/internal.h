@@ -143,6 +143,40 @@ struct PagedAttnArgs {
 size_t paged_attn_workspace(int d);
 cudaError_t launch_paged_attn(const PagedAttnArgs &a, const WaitCfg &wc, cudaStream_t st);
 
+// ---- pages given and taken back (page_plan.cu)
+struct PagePlanArgs {
+  const int *new_lens, *kv_lens;  // [batch]
+  int *table;
+  int64_t table_stride;
+  int batch, max_pages, page_shift;
+  const int *free_pages, *free_count;
+  int64_t capacity;  // of free_pages
+  int *cu, *kv_out, *count_out;
+  int *positions;    // [rows]
+  long long *slots;  // [rows]
+  int64_t rows;
+  void *workspace;
+  DevStatus *status;
+};
+size_t page_plan_workspace(int batch);
+cudaError_t launch_page_plan(const PagePlanArgs &a, cudaStream_t st);
+struct PageTrimArgs {
+  const int *keep, *kv_lens;  // [batch]
+  const int *table;
+  int64_t table_stride;
+  int batch, max_pages, page_shift;
+  int64_t num_pages;
+  int *free_pages;
+  const int *free_count;
+  int64_t capacity;
+  int *kv_out, *count_out;
+  void *workspace;
+  DevStatus *status;
+};
+size_t page_trim_workspace(int batch);
+cudaError_t launch_page_trim(const PageTrimArgs &a, cudaStream_t st);
+constexpr int kMaxPagedBatch = 8192;
+
 struct MlpBwdArgs {
   const void *X, *W1, *W2, *dO;  // [M][K], [K][N], [N][P], [M][P] bf16 row-major
   void *dX, *dW1, *dW2;          // [M][K], [K][N], [N][P] bf16

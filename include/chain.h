@@ -583,6 +583,73 @@ int chain_fwd_paged(const chain_tensor_t *Q, const chain_tensor_t *Kc, const cha
                     void *stream);
 
 /*
+ * chain_page_plan -- pages for the new tokens of a step, and the arrays that
+ * chain_paged_append, chain_qk_norm_rope_append and chain_fwd_paged take, from the
+ * requests' lengths, all on the device.  (An addition of this library.)  For
+ * sequence b with L_b = kv_lens[b] cached positions, n_b = new_lens[b] new tokens:
+ *   cu_seqlens[b] = n_0 + .. + n_(b-1), kv_lens_out[b] = L_b + n_b;
+ *   the pages ceil(L_b / page) .. ceil((L_b + n_b) / page) - 1 of page_table's row b
+ *   are taken off the top of the stack, sequence by sequence and page by page;
+ *   its new token i, in row cu_seqlens[b] + i, has position L_b + i and slot
+ *   page_table[b][position / page] * page + position % page of a pool (token
+ *   slots counted through all pages).
+ *   new_lens, kv_lens  DEVICE int32 [batch].
+ *   page_table   DEVICE int32 [batch][max_pages], rows page_table_stride apart;
+ *                only entries of pages given are written.
+ *   free_pages   DEVICE int32 [capacity]: the stack of free pages, its first
+ *                free_count[0] entries; read only.
+ *   cu_seqlens [batch + 1], kv_lens_out [batch], free_count_out [1]  DEVICE
+ *                int32.  kv_lens_out may be kv_lens and free_count_out free_count
+ *                (a state kept in place); otherwise nothing written may overlap
+ *                anything else.
+ *   positions    DEVICE int32 [rows], slots DEVICE int64 [rows]; rows behind the last
+ *                sequence, as in a batch padded to a captured graph's size, get -1.
+ *   page         a power of two from 16 to 1024, max_pages * page at most 2^30;
+ *                batch at most 8192 (else CHAIN_ERR_UNSUPPORTED); rows below 2^30.
+ *   workspace    at least chain_page_plan_workspace_size(batch) bytes, 16-byte
+ *                aligned, contents ignored on entry; calls that may overlap on the
+ *                GPU need one each.
+ * Reported by the next chain_check() as CHAIN_ERR_ARG: a negative length (taken as 0), a
+ * cached length above max_pages * page (taken as that), tokens beyond `rows` (left out), a stack whose count
+ * is not in [0, capacity] (taken as the nearer end), a stack that runs out and a table that is full: pages that are
+ * not there are entries of -1 (none is written beyond the table), slots in them -1, and
+ * free_count_out is 0.  Whole numbers: the result does not depend on the
+ * order of execution.  Asynchronous on `stream`.
+ */
+size_t chain_page_plan_workspace_size(int batch);
+int chain_page_plan(const int32_t *new_lens, const int32_t *kv_lens, int32_t *page_table,
+                    int64_t page_table_stride, int batch, int max_pages, int page,
+                    const int32_t *free_pages, int64_t capacity, const int32_t *free_count,
+                    int32_t *cu_seqlens, int32_t *kv_lens_out, int32_t *free_count_out,
+                    int32_t *positions, int64_t *slots, int64_t rows, void *workspace,
+                    size_t ws_bytes, void *stream);
+
+/*
+ * chain_page_trim -- the inverse: sequences are cut to their first keep_lens[b]
+ * positions (rejected tokens, evicted and finished requests), and the pages that
+ * hold none of them go back on the stack.  (An addition of this library.)
+ *   kv_lens_out[b] = min(kv_lens[b], max(keep_lens[b], 0)); the entries
+ *   ceil(kv_lens_out[b] / page) .. ceil(kv_lens[b] / page) - 1 of row b follow
+ *   free_pages[free_count[0] - 1], sequence by sequence and page by page.
+ *   free_pages is written from there on; page_table is left as it was.  A page
+ *   that several sequences share goes back once for each that is cut before it: keep
+ *   a shared prefix in all but the last of them.
+ *   num_pages    pages of the pool: an entry outside [0, num_pages), as a plan
+ *                without free pages leaves, is not put on the stack.
+ *   kv_lens_out may be kv_lens and free_count_out free_count; the other arguments as
+ *   for chain_page_plan, the workspace by chain_page_trim_workspace_size.
+ * Reported by the next chain_check() as CHAIN_ERR_ARG: entries outside
+ * [0, num_pages), a length out of range, a stack that overflows (what does not
+ * fit is lost) or whose count is out of range.  Asynchronous on `stream`.
+ */
+size_t chain_page_trim_workspace_size(int batch);
+int chain_page_trim(const int32_t *keep_lens, const int32_t *kv_lens, const int32_t *page_table,
+                    int64_t page_table_stride, int batch, int max_pages, int page,
+                    int64_t num_pages, int32_t *free_pages, int64_t capacity,
+                    const int32_t *free_count, int32_t *kv_lens_out, int32_t *free_count_out,
+                    void *workspace, size_t ws_bytes, void *stream);
+
+/*
  * sp_relayout -- Ulysses sequence shards -> head-major for one head group
  * ("Ulysses Sequence Parallelism", "Contexte Technique": every position of
  * the sequence, a subset of the heads).
