@@ -19,6 +19,8 @@ Entry points (same names as the C ABI):
                             Kc, Vc, Qo, stream=None)
   chain_fwd_paged(Q, Kc, Vc, cu_seqlens, kv_lens, page_table, mask, scale, O, LSE, workspace,
                   stream=None)
+  chain_fwd_paged_prefix(Q, Kc, Vc, cu_seqlens, kv_lens, page_table, prefix_cu, prefix_lens, mask, scale,
+                         O, LSE, workspace, stream=None)
   chain_page_plan(new_lens, kv_lens, page_table, free_pages, free_count, page, cu_seqlens, kv_out,
                   count_out, positions, slots, workspace, stream=None)
   chain_page_trim(keep_lens, kv_lens, page_table, free_pages, free_count, page, num_pages, kv_out,
@@ -26,7 +28,8 @@ Entry points (same names as the C ABI):
   chain_check(stream=None)
 plus allocating conveniences ``attention_fwd``, ``attention_bwd``,
 ``mlp_chain_fwd``, ``relayout``, ``qk_norm_rope``, ``qk_norm_rope_bwd``,
-``qk_norm_rope_append``, ``attention_fwd_paged``, ``page_plan`` and ``page_trim``.
+``qk_norm_rope_append``, ``attention_fwd_paged``, ``attention_fwd_paged_prefix``,
+``page_plan`` and ``page_trim``.
 """
 from __future__ import annotations
 
@@ -115,6 +118,8 @@ def _load():
             lib.chain_qk_norm_rope_append.argtypes = [P, P, P, P, P, P, fl, ci, vp, vp, vp, i64, ci, ci,
                                                       P, P, P, vp]
             lib.chain_fwd_paged.argtypes = [P, P, P, vp, vp, vp, i64, ci, ci, ci, fl, P, P, vp, sz, vp]
+            lib.chain_fwd_paged_prefix.argtypes = [P, P, P, vp, vp, vp, i64, ci, ci, vp, vp, ci, ci, fl, P, P, vp, sz,
+                                                   vp]
             lib.chain_page_plan.argtypes = [vp, vp, vp, i64, ci, ci, ci, vp, i64, vp, vp, vp, vp, vp, vp, i64, vp,
                                             sz, vp]
             lib.chain_page_trim.argtypes = [vp, vp, vp, i64, ci, ci, ci, i64, vp, i64, vp, vp, vp, vp, sz, vp]
@@ -122,7 +127,7 @@ def _load():
                 getattr(lib, fn).argtypes = [ci]
                 getattr(lib, fn).restype = sz
             for fn, n in (("chain_qk_norm_rope_bwd_workspace_size", 1),
-                          ("chain_fwd_paged_workspace_size", 2)):
+                          ("chain_fwd_paged_workspace_size", 2), ("chain_fwd_paged_prefix_workspace_size", 2)):
                 getattr(lib, fn).argtypes = [P] * n
                 getattr(lib, fn).restype = sz
             lib.sp_relayout.argtypes = [P, ci, ci, P, vp]
@@ -140,8 +145,8 @@ def _load():
                        "chain_bwd_noalloc", "chain_fwd_fp8", "chain_fwd_f16pv",
                        "chain_fwd_sp_f16pv",
                        "chain_qk_norm_rope", "chain_qk_norm_rope_bwd", "chain_paged_append",
-                       "chain_qk_norm_rope_append", "chain_fwd_paged", "chain_page_plan",
-                       "chain_page_trim",
+                       "chain_qk_norm_rope_append", "chain_fwd_paged",
+                       "chain_fwd_paged_prefix", "chain_page_plan", "chain_page_trim",
                        "sp_relayout",
                        "sp_relayout_inverse",
                        "chain_check", "chain_selftest_wait_timeout", "chain_umma_selftest",
@@ -409,6 +414,17 @@ def chain_fwd_paged(Q, Kc, Vc, cu_seqlens, kv_lens, page_table, mask, scale, O, 
     """Attention of a chunk of new tokens over a paged cache; see include/chain.h."""
     _small().fwd_paged(Q, Kc, Vc, cu_seqlens, kv_lens, page_table, mask, scale, O, LSE, workspace,
                        _bytes(workspace), *_where(stream))
+
+
+def chain_fwd_paged_prefix_workspace_size(Q, Kc) -> int:
+    return int(_load().chain_fwd_paged_prefix_workspace_size(_ref(desc(Q)), _ref(desc(Kc))))
+
+
+def chain_fwd_paged_prefix(Q, Kc, Vc, cu_seqlens, kv_lens, page_table, prefix_cu, prefix_lens, mask, scale, O, LSE,
+                           workspace, stream=None):
+    """chain_fwd_paged with prefixes that groups of sequences share; see include/chain.h."""
+    _small().fwd_paged_prefix(Q, Kc, Vc, cu_seqlens, kv_lens, page_table, prefix_cu, prefix_lens, mask, scale, O, LSE,
+                              workspace, _bytes(workspace), *_where(stream))
 
 
 def chain_page_plan_workspace_size(batch) -> int:
@@ -701,6 +717,27 @@ def attention_fwd_paged(q, k_cache, v_cache, cu_seqlens, kv_lens, page_table, ca
                                 device=q.device)
     chain_fwd_paged(q, k_cache, v_cache, cu_seqlens, kv_lens, page_table,
                     MASK_CAUSAL if causal else MASK_NONE, scale, o, lse, workspace)
+    return o, lse
+
+
+def attention_fwd_paged_prefix(q, k_cache, v_cache, cu_seqlens, kv_lens, page_table, prefix_cu, prefix_lens,
+                               causal: bool, scale: float | None = None, workspace=None, stream=None):
+    """attention_fwd_paged of sequences that share prefixes: those of group g, prefix_cu[g] to prefix_cu[g + 1] - 1
+    (int32 [groups + 1]), have their first prefix_lens[g] (int32 [groups]) positions in the same pages, all of
+    them before any new token.  Returns (O [total, H, d], LSE [H, total]) as attention_fwd_paged does; a shared
+    prefix is read and multiplied once."""
+    if stream is not None:
+        with _current(stream):
+            return attention_fwd_paged_prefix(q, k_cache, v_cache, cu_seqlens, kv_lens, page_table, prefix_cu,
+                                              prefix_lens, causal, scale, workspace)
+    scale = q.shape[-1] ** -0.5 if scale is None else scale
+    o = _dense_like(q)
+    lse = torch.empty(q.shape[1], q.shape[0], dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = torch.empty(max(chain_fwd_paged_prefix_workspace_size(q, k_cache), 16), dtype=torch.uint8,
+                                device=q.device)
+    chain_fwd_paged_prefix(q, k_cache, v_cache, cu_seqlens, kv_lens, page_table, prefix_cu, prefix_lens,
+                           MASK_CAUSAL if causal else MASK_NONE, scale, o, lse, workspace)
     return o, lse
 
 

@@ -363,6 +363,35 @@ static PyObject *fwd_paged(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   return done(rc, "chain_fwd_paged");
 }
 
+static PyObject *fwd_paged_prefix(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+  (void)self;
+  if (count(n, 16, "chain_fwd_paged_prefix")) return NULL;
+  DEV_STREAM(14);
+  TENSOR(0, Q);
+  TENSOR(1, Kc);
+  TENSOR(2, Vc);
+  TENSOR(10, O);
+  TENSOR(11, LSE);
+  paged_t p;
+  void *ws, *group_cu, *group_lens;
+  int64_t groups = -1;
+  if (paged(a[3], a[4], a[5], dev, &p) || row_of(a[7], dev, "prefix_lens", 0, &groups, &group_lens)) return NULL;
+  int64_t ends = groups + 1;
+  if (row_of(a[6], dev, "prefix_cu", 0, &ends, &group_cu) || workspace(a[12], dev, &ws)) return NULL;
+  const long mask = PyLong_AsLong(a[8]);
+  const double scale = PyFloat_AsDouble(a[9]);
+  const size_t bytes = PyLong_AsSize_t(a[13]);
+  if (PyErr_Occurred()) return NULL;
+  if (groups > 0x7fffffff) return PyErr_Format(PyExc_ValueError, "too many groups");
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = chain_fwd_paged_prefix(Q, Kc, Vc, (const int32_t *)p.cu, (const int32_t *)p.lens, (const int32_t *)p.table,
+                              p.stride, p.batch, p.max_pages, group_cu, group_lens, (int)groups, (int)mask,
+                              (float)scale, O, LSE, ws, bytes, stream);
+  Py_END_ALLOW_THREADS
+  return done(rc, "chain_fwd_paged_prefix");
+}
+
 /* What a plan and a trim share: lengths, the table and the stack. */
 typedef struct {
   void *lens, *kv, *table, *free, *count, *kv_out, *count_out, *ws;
@@ -435,7 +464,7 @@ static PyObject *page_trim(PyObject *self, PyObject *const *a, Py_ssize_t n) {
 static PyMethodDef methods[] = {METHOD(setup),        METHOD(qk_norm_rope),        METHOD(qk_norm_rope_bwd),
                                 METHOD(paged_append), METHOD(qk_norm_rope_append), METHOD(fwd_paged),
                                 METHOD(qk_norm_rope_bwd_workspace_size),
-                                METHOD(page_plan),    METHOD(page_trim),
+                                METHOD(page_plan),    METHOD(page_trim),           METHOD(fwd_paged_prefix),
                                 {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", NULL, -1, methods, NULL, NULL, NULL, NULL};
 

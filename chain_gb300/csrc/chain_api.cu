@@ -1143,14 +1143,15 @@ size_t chain_fwd_paged_workspace_size(const chain_tensor_t *Q, const chain_tenso
   return paged_attn_workspace((int)d);
 }
 
-int chain_fwd_paged(const chain_tensor_t *Q, const chain_tensor_t *Kc, const chain_tensor_t *Vc,
-                    const int32_t *cu_seqlens, const int32_t *kv_lens, const int32_t *page_table,
-                    int64_t page_table_stride, int batch, int max_pages, int mask, float scale,
-                    chain_tensor_t *O, chain_tensor_t *LSE, void *workspace, size_t ws_bytes,
-                    void *stream) {
+// The arguments of chain_fwd_paged but its workspace.  *work: there is something to do.
+static int paged_attn_args(const chain_tensor_t *Q, const chain_tensor_t *Kc, const chain_tensor_t *Vc,
+                           const int32_t *cu_seqlens, const int32_t *kv_lens, const int32_t *page_table,
+                           int64_t page_table_stride, int batch, int max_pages, int mask, float scale,
+                           chain_tensor_t *O, chain_tensor_t *LSE, PagedAttnArgs *args, bool *work) {
+  *work = false;
   if (mask != CHAIN_MASK_NONE && mask != CHAIN_MASK_CAUSAL) return CHAIN_ERR_ARG;
   if (!(scale > 0.0f) || !(scale < 1e30f)) return CHAIN_ERR_ARG;
-  PagedAttnArgs a;
+  PagedAttnArgs &a = *args;
   NormRopeSide q, o;
   int64_t b1, total, H, d, n2, h2, d2, pk[4], pv[4];
   int rc;
@@ -1164,19 +1165,65 @@ int chain_fwd_paged(const chain_tensor_t *Q, const chain_tensor_t *Kc, const cha
   if (pk[3] != d || H % pk[2]) return CHAIN_ERR_ARG;
   if ((rc = paged_seqs(cu_seqlens, kv_lens, page_table, page_table_stride, batch, max_pages, pk, &a.seqs)))
     return rc;
-  if (H / pk[2] > 128 || batch > 8192) return CHAIN_ERR_UNSUPPORTED;
+  if (H / pk[2] > 128 || batch > kMaxPagedBatch) return CHAIN_ERR_UNSUPPORTED;
+  a.total = (int)total; a.H = (int)H; a.Hkv = (int)pk[2]; a.d = (int)d;
   if (total == 0 || batch == 0) return CHAIN_OK;
   int64_t lse_shead = 0;
   if ((rc = lse_view(LSE, H, total, &lse_shead))) return rc;
-  if (!workspace || !aligned16(workspace) || ws_bytes < paged_attn_workspace((int)d)) return CHAIN_ERR_ARG;
   a.Q = q.ptr; a.q_stok = q.s_tok; a.q_shead = q.s_head;
   a.O = o.ptr; a.o_stok = o.s_tok; a.o_shead = o.s_head;
   a.LSE = static_cast<float *>(LSE->ptr); a.lse_shead = lse_shead;
-  a.total = (int)total; a.H = (int)H; a.Hkv = (int)pk[2]; a.d = (int)d;
-  a.causal = mask == CHAIN_MASK_CAUSAL; a.scale = scale; a.workspace = workspace;
+  a.causal = mask == CHAIN_MASK_CAUSAL; a.scale = scale;
+  *work = true;
+  return CHAIN_OK;
+}
+
+int chain_fwd_paged(const chain_tensor_t *Q, const chain_tensor_t *Kc, const chain_tensor_t *Vc,
+                    const int32_t *cu_seqlens, const int32_t *kv_lens, const int32_t *page_table,
+                    int64_t page_table_stride, int batch, int max_pages, int mask, float scale,
+                    chain_tensor_t *O, chain_tensor_t *LSE, void *workspace, size_t ws_bytes,
+                    void *stream) {
+  PagedAttnArgs a;
+  bool work;
+  int rc = paged_attn_args(Q, Kc, Vc, cu_seqlens, kv_lens, page_table, page_table_stride, batch, max_pages, mask, scale,
+                           O, LSE, &a, &work);
+  if (rc || !work) return rc;
+  if (!workspace || !aligned16(workspace) || ws_bytes < paged_attn_workspace(a.d)) return CHAIN_ERR_ARG;
+  a.workspace = workspace;
   DevInfo *di = nullptr;
   if ((rc = device_ready(&di))) return rc;
   cudaError_t e = launch_paged_attn(a, wait_cfg(di), static_cast<cudaStream_t>(stream));
+  if (e == cudaErrorNotSupported) return CHAIN_ERR_UNSUPPORTED;
+  return e == cudaSuccess ? CHAIN_OK : cuda_fail(e);
+}
+
+size_t chain_fwd_paged_prefix_workspace_size(const chain_tensor_t *Q, const chain_tensor_t *Kc) {
+  if (chain_fwd_paged_workspace_size(Q, Kc) == 0) return 0;
+  return prefix_attn_workspace((int)Q->shape[2], Q->shape[0], (int)Q->shape[1]);
+}
+
+int chain_fwd_paged_prefix(const chain_tensor_t *Q, const chain_tensor_t *Kc, const chain_tensor_t *Vc,
+                           const int32_t *cu_seqlens, const int32_t *kv_lens, const int32_t *page_table,
+                           int64_t page_table_stride, int batch, int max_pages, const int32_t *prefix_cu,
+                           const int32_t *prefix_lens, int groups, int mask, float scale, chain_tensor_t *O,
+                           chain_tensor_t *LSE, void *workspace, size_t ws_bytes, void *stream) {
+  PrefixAttnArgs x;
+  bool work;
+  int rc = paged_attn_args(Q, Kc, Vc, cu_seqlens, kv_lens, page_table, page_table_stride, batch, max_pages, mask, scale,
+                           O, LSE, &x.a, &work);
+  if (rc) return rc;
+  if (groups < 0 || (groups > 0 && (!prefix_cu || !prefix_lens || !aligned4(prefix_cu) || !aligned4(prefix_lens))))
+    return CHAIN_ERR_ARG;
+  if (groups > kMaxPagedBatch) return CHAIN_ERR_UNSUPPORTED;
+  if (!work) return CHAIN_OK;
+  if (!workspace || !aligned16(workspace) || ws_bytes < prefix_attn_workspace(x.a.d, x.a.total, x.a.H))
+    return CHAIN_ERR_ARG;
+  x.a.workspace = workspace;
+  x.group_cu = prefix_cu; x.group_lens = prefix_lens; x.groups = groups;
+  DevInfo *di = nullptr;
+  if ((rc = device_ready(&di))) return rc;
+  cudaError_t e = groups == 0 ? launch_paged_attn(x.a, wait_cfg(di), static_cast<cudaStream_t>(stream))
+                              : launch_prefix_attn(x, wait_cfg(di), static_cast<cudaStream_t>(stream));
   if (e == cudaErrorNotSupported) return CHAIN_ERR_UNSUPPORTED;
   return e == cudaSuccess ? CHAIN_OK : cuda_fail(e);
 }

@@ -143,6 +143,15 @@ struct PagedAttnArgs {
 size_t paged_attn_workspace(int d);
 cudaError_t launch_paged_attn(const PagedAttnArgs &a, const WaitCfg &wc, cudaStream_t st);
 
+// The same, with groups of sequences that share a prefix (prefix_attn.cu).
+struct PrefixAttnArgs {
+  PagedAttnArgs a;
+  const int *group_cu, *group_lens;  // [groups + 1], [groups]
+  int groups;
+};
+size_t prefix_attn_workspace(int d, int64_t total, int H);
+cudaError_t launch_prefix_attn(const PrefixAttnArgs &x, const WaitCfg &wc, cudaStream_t st);
+
 // ---- pages given and taken back (page_plan.cu)
 struct PagePlanArgs {
   const int *new_lens, *kv_lens;  // [batch]

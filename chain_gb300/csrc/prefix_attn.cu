@@ -1,0 +1,59 @@
+// prefix_attn.cu -- attention over a paged cache for a batch whose sequences share long prefixes.
+//
+// Softmax attention of a row over keys in two sets is the join of its sums over each: with m the
+// largest score of a set, l = sum exp(s - m) and A = sum exp(s - m) v,
+//   m = max(m1, m2),  O = (A1 e^(m1 - m) + A2 e^(m2 - m)) / (l1 e^(m1 - m) + l2 e^(m2 - m)).
+// The first set is the group's prefix, whole key tiles of it.  It is the same for every row of the group, and
+// the packed rows of a group's sequences lie together, so the group is one long sequence of new tokens without
+// a mask over it: its keys are read once for 128 rows instead of once for each sequence, and
+// multiplied in full tiles.  The second is what each sequence has behind, masked as ever.
+//
+// Two passes of the kernels of paged_attn.cuh, then: SHARED writes (m, l, A) in 32 bits, [head][column / 4][row][4],
+// lanes side by side as in the parts of a cut unit; OWN joins them where it would have
+// written O, in a unit's end or in the join of a cut one, so that O is rounded once.  Each pass deals its work as a
+// call alone does.  OWN begins while SHARED ends, and waits for it only where it joins.
+#include "paged_attn.cuh"
+
+namespace chain {
+namespace {
+
+size_t rows_bytes(int64_t rows, int d) { return (size_t)rows * d * sizeof(float); }
+
+template <int D>
+cudaError_t launch(const PrefixAttnArgs &x, const WaitCfg &wc, cudaStream_t st) {
+  const PagedAttnArgs &a = x.a;
+  Params own = params_of<D>(a, wc);
+  own.group_cu = x.group_cu;
+  own.group_lens = x.group_lens;
+  own.groups = x.groups;
+  const int64_t rows = (int64_t)a.total * a.H;
+  uint8_t *ws = static_cast<uint8_t *>(a.workspace) + 2 * pass_workspace(D);
+  own.pre_o = reinterpret_cast<float *>(ws);
+  own.pre_ml = reinterpret_cast<float2 *>(ws + rows_bytes(rows, D));
+  Params shared = own;
+  shared.causal = 0;
+  PagedAttnArgs b = a;  // the passes' workspaces are apart: they overlap
+  b.workspace = static_cast<uint8_t *>(a.workspace) + pass_workspace(D);
+  shared.part_o = reinterpret_cast<float *>(b.workspace);
+  shared.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(b.workspace) + part_bytes(D));
+  shared.bounds = reinterpret_cast<Boundary *>(static_cast<uint8_t *>(b.workspace) + part_bytes(D) + ml_bytes());
+  // Tiles of 16 rows where the groups' rows fit one on the average; what is longer than two of them then goes to a launch
+  // of its own, as with single tokens.
+  const int64_t group_rows = (int64_t)a.total * own.G;
+  const bool few = own.G <= TOK_ROWS && group_rows <= (int64_t)TOK_ROWS * x.groups;
+  cudaError_t e = launch_pass<D, SHARED>(b, shared, x.groups, few, x.groups > 1 && group_rows > 2 * TOK_ROWS, false, st);
+  if (e != cudaSuccess) return e;
+  return launch_pass<D, OWN>(a, own, a.seqs.batch, few_rows(a, own.G), may_have_chunks(a, own.G), true, st);
+}
+
+}  // namespace
+
+size_t prefix_attn_workspace(int d, int64_t total, int H) {
+  return 2 * pass_workspace(d) + rows_bytes(total * H, d) + (size_t)total * H * sizeof(float2);
+}
+
+cudaError_t launch_prefix_attn(const PrefixAttnArgs &x, const WaitCfg &wc, cudaStream_t st) {
+  return x.a.d == 128 ? launch<128>(x, wc, st) : launch<64>(x, wc, st);
+}
+
+}  // namespace chain

@@ -583,6 +583,38 @@ int chain_fwd_paged(const chain_tensor_t *Q, const chain_tensor_t *Kc, const cha
                     void *stream);
 
 /*
+ * chain_fwd_paged_prefix -- chain_fwd_paged for a batch whose sequences share long
+ * prefixes (one system prompt or document before many requests, one prompt
+ * sampled many times), whose keys and values are read and multiplied once
+ * for all of them.  (An addition of this library.)  All of chain_fwd_paged, its cache, arguments, masks
+ * and results, and
+ *   prefix_cu    DEVICE int32 [groups + 1], nondecreasing: group g is the sequences
+ *                [prefix_cu[g], prefix_cu[g+1]), clamped to [0, batch].  Sequences of
+ *                no group share nothing.
+ *   prefix_lens  DEVICE int32 [groups]: the caller's word that the page_table rows of all of the group's
+ *                sequences that have new tokens name the same pages for the positions below
+ *                prefix_lens[g].  Any number, also inside a page.  groups at most 8192
+ *                (else CHAIN_ERR_UNSUPPORTED); with groups = 0 the call is chain_fwd_paged.
+ *   workspace    at least chain_fwd_paged_prefix_workspace_size(Q, Kc) bytes, 16-byte aligned,
+ *                contents ignored on entry; calls that may overlap on the GPU need one each.
+ * Every new token must see its group's whole prefix: prefix_lens[g] at most kv_lens[b] - n_b
+ * with CAUSAL, kv_lens[b] with NONE.  A sequence with new tokens for which it is not so is
+ * reported by the next chain_check() as CHAIN_ERR_ARG and its rows are not valid; a prefix_lens[g]
+ * below 0 or above max_pages * page of a group with new tokens is reported and taken as the nearer end.
+ * Arithmetic: as chain_fwd_paged; a row's sums over the prefix (whole tiles of 128 keys of it) and over
+ * what its sequence has behind are held in fp32 and joined before the rounding of O.  Results are
+ * deterministic, but not the bits of chain_fwd_paged.  Asynchronous on `stream`.
+ * chain_fwd_paged_prefix_workspace_size returns 0 for a Q or Kc it cannot take.
+ */
+size_t chain_fwd_paged_prefix_workspace_size(const chain_tensor_t *Q, const chain_tensor_t *Kc);
+int chain_fwd_paged_prefix(const chain_tensor_t *Q, const chain_tensor_t *Kc, const chain_tensor_t *Vc,
+                           const int32_t *cu_seqlens, const int32_t *kv_lens, const int32_t *page_table,
+                           int64_t page_table_stride, int batch, int max_pages, const int32_t *prefix_cu,
+                           const int32_t *prefix_lens, int groups, int mask, float scale,
+                           chain_tensor_t *O, chain_tensor_t *LSE, void *workspace, size_t ws_bytes,
+                           void *stream);
+
+/*
  * chain_page_plan -- pages for the new tokens of a step, and the arrays that
  * chain_paged_append, chain_qk_norm_rope_append and chain_fwd_paged take, from the
  * requests' lengths, all on the device.  (An addition of this library.)  For
