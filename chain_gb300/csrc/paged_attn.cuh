@@ -153,7 +153,7 @@ struct Params {
   // group_lens[g] positions lie in the same pages
   const int *group_cu, *group_lens;
   int groups;
-  float *pre_o;    // [Hkv][D / 4][total G][4]
+  float *pre_o;    // [Hkv][D / 4][total G][4]; null: no prefix is taken together
   float2 *pre_ml;  // [Hkv][total G]
 };
 
@@ -213,14 +213,9 @@ __device__ __forceinline__ int seqs_of(const Params &p) {
 }
 
 // The positions of a group's prefix that are taken together: whole key tiles.
-__device__ __forceinline__ int shared_len(const Params &p, int g, bool report) {
-  int len = __ldg(p.group_lens + g);
+__device__ __forceinline__ int shared_len(const Params &p, int len) {
   const int most = p.s.max_pages << p.s.page_shift;
-  if (len < 0 || len > most) {
-    if (report) atomicExch(&p.wc.status->reserved[0], 1);
-    len = len < 0 ? 0 : most;
-  }
-  return len & ~(BN - 1);
+  return (len < 0 ? 0 : (len > most ? most : len)) & ~(BN - 1);
 }
 
 // The group of sequence b, or -1.
@@ -258,7 +253,7 @@ __device__ __forceinline__ Seq seq_of(const Params &p, int b, bool report) {
   if (MODE == SHARED) {
     const int2 m = members(p, b);
     s = rows_of(p, m.x, m.y);
-    s.len = shared_len(p, b, report && s.n > 0);
+    s.len = shared_len(p, __ldg(p.group_lens + b));
     if (s.len == 0) s.n = 0;
   } else {
     s = rows_of(p, b, b + 1);
@@ -271,9 +266,10 @@ __device__ __forceinline__ Seq seq_of(const Params &p, int b, bool report) {
     if (MODE == OWN) {
       const int g = group_of(p, b);
       if (g >= 0) {
-        s.j = shared_len(p, g, false) / BN;
+        const int len = __ldg(p.group_lens + g);
+        if (p.pre_o) s.j = shared_len(p, len) / BN;
         // every new token must see the whole prefix
-        if (report && s.n > 0 && __ldg(p.group_lens + g) > (p.causal ? s.len - s.n : s.len))
+        if (report && s.n > 0 && (len < 0 || len > (p.causal ? s.len - s.n : s.len)))
           atomicExch(&p.wc.status->reserved[0], 1);
       }
     }
@@ -1480,14 +1476,6 @@ __device__ __forceinline__ void combine_rows(const Params &p, const Boundary &bd
   const int64_t pre_pitch = (int64_t)p.total * p.G;
   const int64_t pre_row = ((int64_t)bd.tok0 + tok) * p.G + r % BM - rt * p.G;
   float4 *pre = reinterpret_cast<float4 *>(p.pre_o) + (bd.head * (D / 4) + warp * Q) * pre_pitch + pre_row;
-  if (MODE == SHARED) {
-    if (group == 0 && valid) {
-#pragma unroll
-      for (int q = 0; q < Q; ++q) pre[q * pre_pitch] = o[q];
-      if (warp == 0) p.pre_ml[bd.head * pre_pitch + pre_row] = make_float2(m, l);
-    }
-    return;
-  }
   if (MODE == OWN && bd.pre && valid) {  // the row's sums over its group's prefix
     const float2 x = p.pre_ml[bd.head * pre_pitch + pre_row];
     const float top = fmaxf(m, x.x);
@@ -1527,7 +1515,6 @@ __device__ __forceinline__ void combine_rows(const Params &p, const Boundary &bd
 template <int D, int RUNS, int SLOT, int MODE>
 __global__ void __launch_bounds__(256, 4) paged_combine_kernel(const Params p) {
   __shared__ uint2 rows[32][D / 4 + 1];
-  if (MODE == SHARED) pdl_launch_dependents();  // the pass over the sequences' own keys, which waits where it joins
   pdl_wait();  // the parts and boundaries
   const int c = blockIdx.x + 1, y = blockIdx.y;
   const Boundary bd = p.bounds[c];
@@ -1542,6 +1529,166 @@ __global__ void __launch_bounds__(256, 4) paged_combine_kernel(const Params p) {
     combine_rows<D, RUNS, SLOT, MODE, 8>(p, bd, c, 0, rows);
   else
     combine_rows<D, RUNS, SLOT, MODE, 32>(p, bd, c, y * 32, rows);
+}
+
+// The same with SHARED, whose units have many rows and may have many parts, into the sums that OWN joins.
+// A block takes ROWS rows, a lane a row, as in the parts (with 16 rows, half a warp's lanes take other parts).  Of a few
+// parts a warp takes COLS float4 of every row, and the unit's first boundary all columns; many parts are dealt to the
+// warps, PB loaded at once, and the unit's boundaries share its columns out.  The groups' sums are joined
+// through shared memory.
+template <int ROWS>
+struct JoinShared {
+  static constexpr int COLS = 4, GROUPS = 8 * (32 / ROWS);
+  float4 part[GROUPS][COLS][ROWS];
+  float2 ml[GROUPS][ROWS];
+};
+
+// A lane's share of its row: parts first, first + step, ... below last, columns [col0, col0 + COLS).
+template <int D, int SLOT, int PB, int COLS, typename F>
+__device__ __forceinline__ void join_parts(const Params &p, int c, int first, int step, int last, int r, int col0,
+                                           const F &has_part, float &m, float &l, float4 (&o)[COLS]) {
+  m = -INFINITY;
+  l = 0.0f;
+#pragma unroll
+  for (int q = 0; q < COLS; ++q) o[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int k0 = first; k0 < last; k0 += PB * step) {
+    float2 x[PB];
+    float4 v[PB][COLS];
+#pragma unroll
+    for (int i = 0; i < PB; ++i) {
+      const int k = k0 + i * step;
+      x[i] = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+      for (int q = 0; q < COLS; ++q) v[i][q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (k < last && has_part(k)) {
+        const int64_t slot = (int64_t)k * 2 + (k < c ? 1 : 0);
+        const float4 *po = reinterpret_cast<const float4 *>(p.part_o) + (slot * (D / 4) + col0) * SLOT + r;
+        x[i] = p.part_ml[slot * SLOT + r];
+#pragma unroll
+        for (int q = 0; q < COLS; ++q) v[i][q] = po[q * SLOT];
+      }
+    }
+    float top = m;
+#pragma unroll
+    for (int i = 0; i < PB; ++i) top = fmaxf(top, x[i].x);
+    if (top == -INFINITY) continue;
+    const float w0 = ex2(m - top);
+    m = top;
+    l *= w0;
+#pragma unroll
+    for (int q = 0; q < COLS; ++q) {
+      o[q].x *= w0;
+      o[q].y *= w0;
+      o[q].z *= w0;
+      o[q].w *= w0;
+    }
+#pragma unroll
+    for (int i = 0; i < PB; ++i) {
+      const float w = ex2(x[i].x - top);
+      l = fmaf(w, x[i].y, l);
+#pragma unroll
+      for (int q = 0; q < COLS; ++q) {
+        o[q].x = fmaf(w, v[i][q].x, o[q].x);
+        o[q].y = fmaf(w, v[i][q].y, o[q].y);
+        o[q].z = fmaf(w, v[i][q].z, o[q].z);
+        o[q].w = fmaf(w, v[i][q].w, o[q].w);
+      }
+    }
+  }
+}
+
+template <int D, int RUNS, int SLOT>
+__global__ void __launch_bounds__(256, 2) shared_join_kernel(const Params p) {
+  constexpr int ROWS = SLOT < 32 ? SLOT : 32, HALVES = 32 / ROWS;
+  using J = JoinShared<ROWS>;
+  constexpr int COLS = J::COLS, GROUPS = J::GROUPS, CHUNKS = D / 4 / COLS, FEW = 8;
+  __shared__ J sh;
+  pdl_launch_dependents();  // the pass over the sequences' own keys, which waits where it joins
+  pdl_wait();               // the parts and boundaries
+  const int first_row = blockIdx.y * ROWS;
+  const Boundary bd = p.bounds[blockIdx.x + 1];
+  const int tiles = bd.ntok > p.tpt ? 2 : 1;
+  if (!bd.cut || (SLOT > ROWS && first_row >= tiles * BM)) return;
+  const int left = bd.ntok - first_row / BM * p.tpt;
+  if (first_row % BM >= min(left, p.tpt) * p.G) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = lane / ROWS;
+  const long long end = bd.u0 + p.overhead + (long long)bd.w * bd.nt;
+  auto tile_of = [&](int k) { return tile_at(p, run_start<RUNS>(bd.total, k) - bd.u0, bd.w); };
+  auto in_unit = [&](int k) { return k < RUNS && run_start<RUNS>(bd.total, k) < end; };
+  auto cuts = [&](int k) { return k > 0 && run_start<RUNS>(bd.total, k) > bd.u0 && tile_of(k) > 0; };
+  int before = 0, last = (int)blockIdx.x + 2;  // the unit's boundaries before this one, and the end of its parts
+  for (uint32_t in = ~0u; in == ~0u;) {
+    in = __ballot_sync(0xffffffffu, cuts((int)blockIdx.x - before - lane));
+    before += in == ~0u ? 32 : __ffs(~in) - 1;
+  }
+  if (before >= CHUNKS) return;
+  for (uint32_t in = ~0u; in == ~0u;) {
+    in = __ballot_sync(0xffffffffu, in_unit(last + lane));
+    last += in == ~0u ? 32 : __ffs(~in) - 1;
+  }
+  const int c = (int)blockIdx.x + 1 - before;  // the unit's first boundary; its first part is run c - 1's
+  const bool few = last - c + 1 <= FEW;
+  if (few && before > 0) return;
+  // a run shorter than a key tile may hold none of the unit, and then no part
+  const bool tiny = bd.total < (long long)RUNS * (bd.w + 1);
+  auto row_at = [&](int r, int &tok) {  // whether row r of the unit's tiles is a token's
+    const int rt = r % BM / p.G;
+    tok = r / BM * p.tpt + rt;
+    return rt < p.tpt && tok < bd.ntok;
+  };
+  const int64_t pitch = (int64_t)p.total * p.G;
+  auto put = [&](int r, int tok, int col, const float4 &v, float m, float l) {
+    const int64_t at = ((int64_t)bd.tok0 + tok) * p.G + r % BM % p.G;
+    reinterpret_cast<float4 *>(p.pre_o)[(bd.head * (D / 4) + col) * pitch + at] = v;
+    if (col == 0) p.pre_ml[bd.head * pitch + at] = make_float2(m, l);
+  };
+  const int r = first_row + lane % ROWS;
+  int tok;
+  const bool valid = row_at(r, tok);
+  auto has_part = [&](int k) {
+    return valid && (!tiny || run_start<RUNS>(bd.total, k + 1) >= end || tile_of(k + 1) > tile_of(k));
+  };
+  float m, l;
+  float4 o[COLS];
+  if (few) {
+    for (int col0 = (warp * HALVES + half) * COLS; col0 < D / 4; col0 += 8 * HALVES * COLS) {
+      join_parts<D, SLOT, 4, COLS>(p, c, c - 1, 1, last, r, col0, has_part, m, l, o);
+      if (!valid) continue;
+#pragma unroll
+      for (int q = 0; q < COLS; ++q) put(r, tok, col0 + q, o[q], m, l);
+    }
+    return;
+  }
+  const int group = warp * HALVES + half;
+  for (int col0 = before * COLS; col0 < D / 4; col0 += (last - c) * COLS) {
+    join_parts<D, SLOT, 4, COLS>(p, c, c - 1 + group, GROUPS, last, r, col0, has_part, m, l, o);
+    sh.ml[group][lane % ROWS] = make_float2(m, l);
+#pragma unroll
+    for (int q = 0; q < COLS; ++q) sh.part[group][q][lane % ROWS] = o[q];
+    __syncthreads();
+    for (int i = threadIdx.x; i < ROWS * COLS; i += 256) {
+      const int y = i % ROWS, q = i / ROWS;
+      int ty;
+      if (!row_at(first_row + y, ty)) continue;
+      float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+      for (int g = 0; g < GROUPS; ++g) top = fmaxf(top, sh.ml[g][y].x);
+      float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int g = 0; g < GROUPS; ++g) {
+        const float2 x = sh.ml[g][y];
+        const float w = x.x == -INFINITY ? 0.0f : ex2(x.x - top);
+        const float4 v = sh.part[g][q][y];
+        sum = fmaf(w, x.y, sum);
+        s.x = fmaf(w, v.x, s.x);
+        s.y = fmaf(w, v.y, s.y);
+        s.z = fmaf(w, v.z, s.z);
+        s.w = fmaf(w, v.w, s.w);
+      }
+      put(first_row + y, ty, col0 + q, s, top, sum);
+    }
+    __syncthreads();
+  }
 }
 
 size_t part_bytes(int d) { return (size_t)CTAS * 2 * 2 * BM * d * sizeof(float); }
@@ -1569,8 +1716,9 @@ template <int D, int RUNS, int SLOT, int MODE>
 cudaError_t launch_join(const PagedAttnArgs &a, const Params &p, cudaStream_t st) {
   // no sequence is longer than a key tile: no unit is cut
   if (((int64_t)a.seqs.max_pages << a.seqs.page_shift) <= BN) return cudaSuccess;
-  return launch_kernel(paged_combine_kernel<D, RUNS, SLOT, MODE>, dim3(RUNS - 1, SLOT < 32 ? 1 : SLOT / 32), 256, 0,
-                       true, st, p);
+  const dim3 grid(RUNS - 1, SLOT < 32 ? 1 : SLOT / 32);
+  if constexpr (MODE == SHARED) return launch_kernel(shared_join_kernel<D, RUNS, SLOT>, grid, 256, 0, true, st, p);
+  return launch_kernel(paged_combine_kernel<D, RUNS, SLOT, MODE>, grid, 256, 0, true, st, p);
 }
 
 template <int D, int WARPS, int MODE>

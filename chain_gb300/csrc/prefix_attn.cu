@@ -17,6 +17,8 @@
 namespace chain {
 namespace {
 
+constexpr int64_t ALONE_BYTES = int64_t(1) << 27;
+
 size_t rows_bytes(int64_t rows, int d) { return (size_t)rows * d * sizeof(float); }
 
 template <int D>
@@ -26,6 +28,11 @@ cudaError_t launch(const PrefixAttnArgs &x, const WaitCfg &wc, cudaStream_t st) 
   own.group_cu = x.group_cu;
   own.group_lens = x.group_lens;
   own.groups = x.groups;
+  // So few keys that single tokens read them sooner each by itself than in two passes: the most that the table
+  // can name, since the lengths are on the device.
+  const int64_t keys = (int64_t)a.seqs.batch * a.seqs.max_pages << a.seqs.page_shift;
+  if (few_rows(a, own.G) && keys * a.Hkv * D * 4 <= ALONE_BYTES)
+    return launch_pass<D, OWN>(a, own, a.seqs.batch, true, may_have_chunks(a, own.G), false, st);
   const int64_t rows = (int64_t)a.total * a.H;
   uint8_t *ws = static_cast<uint8_t *>(a.workspace) + 2 * pass_workspace(D);
   own.pre_o = reinterpret_cast<float *>(ws);

@@ -35,7 +35,14 @@ class Shared(Cache):
             self.prefix_cu.append(b)
             self.prefix_lens.append(P)
 
-    def cuda(self):
+    def cuda(self, wide=True):
+        """wide: a table whose rows are so long that the call cannot tell its keys are few."""
+        if wide:
+            cols = -(-(2 ** 27 + 1) // (len(self.lens) * self.page * self.Hkv * self.d * 4))
+            if cols > self.table.shape[1]:
+                table = torch.full((len(self.lens), cols), -7, dtype=torch.int32)
+                table[:, :self.table.shape[1]] = self.table
+                self.table = table
         super().cuda()
         self.gcu = torch.tensor(self.prefix_cu, dtype=torch.int32).cuda()
         self.glens = torch.tensor(self.prefix_lens, dtype=torch.int32).cuda()
@@ -46,8 +53,8 @@ class Shared(Cache):
         return (*super().args, self.gcu, self.glens)
 
 
-def made(groups, lens, news, H, Hkv, d, page, seed, **kw):
-    c = Shared(groups, lens, news, Hkv, d, page, seed, **kw).fill().cuda()
+def made(groups, lens, news, H, Hkv, d, page, seed, wide=True, **kw):
+    c = Shared(groups, lens, news, Hkv, d, page, seed, **kw).fill().cuda(wide)
     return c, cs.normal((c.total, H, d), seed + 1)
 
 
@@ -97,10 +104,11 @@ CASES = {
 
 
 @pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("wide", [True, False])
 @pytest.mark.parametrize("name", CASES)
-def test_prefix(cg, name, causal):
+def test_prefix(cg, name, wide, causal):
     groups, lens, news, H, Hkv, d, page = CASES[name]
-    c, q = made(groups, lens, news, H, Hkv, d, page, 2000 + 7 * len(name), heads_first=len(name) % 3 == 0)
+    c, q = made(groups, lens, news, H, Hkv, d, page, 2000 + 7 * len(name), wide, heads_first=len(name) % 3 == 0)
     o, lse = cg.attention_fwd_paged_prefix(q.cuda(), c.kcd, c.vcd, *c.args, causal=causal)
     assert cg.chain_check()[0] == 0
     check(c, q, o, lse, causal, d ** -0.5)
@@ -225,9 +233,10 @@ def test_two_calls_at_once(cg):
             assert all(torch.equal(a, b) for a, b in zip(out, ref[i]))
 
 
+@pytest.mark.parametrize("wide", [True, False])
 @pytest.mark.parametrize("news", [[1, 1, 1], [20, 1, 30]])
-def test_what_is_reported(cg, news):
-    c, q = made([(2, 256), (1, 128)], [300, 290, 400], news, 8, 2, 128, 16, 53)
+def test_what_is_reported(cg, news, wide):
+    c, q = made([(2, 256), (1, 128)], [300, 290, 400], news, 8, 2, 128, 16, 53, wide)
     q = q.cuda()
     run = lambda glens: cg.attention_fwd_paged_prefix(q, c.kcd, c.vcd, *c.args[:3], c.gcu,
                                                       torch.tensor(glens, dtype=torch.int32).cuda(), causal=True)
