@@ -816,26 +816,29 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc_fence_after();
         if (active) {
           const int kv0 = (u.j0 + (two ? i : 2 * i + t)) * BN;
-          uint32_t s[BN];
-#pragma unroll
-          for (int c = 0; c < BN / 32; ++c)
-            tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[c * 32]));
-          tmem_wait_ld();
-          if (kv0 + BN > lim) {
-#pragma unroll
-            for (int e = 0; e < BN; ++e)
-              if (kv0 + e >= lim) s[e] = __float_as_uint(-INFINITY);
-          }
-          __syncwarp();
           float mx4[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            mx4[e] = fmaxf(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+          for (int e = 0; e < 4; ++e) mx4[e] = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < BN; c += 64) {
+            uint32_t s[64];
+            tmem_ld32(tS + c, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+            tmem_ld32(tS + c + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+            tmem_wait_ld();
+            if (__any_sync(0xffffffffu, kv0 + c + 64 > lim)) {
 #pragma unroll
-          for (int c = 8; c < BN; c += 8)
+              for (int e = 0; e < 64; ++e)
+                if (kv0 + c + e >= lim) s[e] = __float_as_uint(-INFINITY);
+              tmem_st32(tS + c, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+              tmem_st32(tS + c + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+              tmem_wait_st();
+            }
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              mx4[e] = fmax3(mx4[e], __uint_as_float(s[c + 2 * e]), __uint_as_float(s[c + 2 * e + 1]));
+            for (int i = 0; i < 64; i += 8)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                mx4[e] = fmax3(mx4[e], __uint_as_float(s[i + 2 * e]), __uint_as_float(s[i + 2 * e + 1]));
+          }
           const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.scale_log2;
           float alpha = 1.0f;
           bool rescale = false;
@@ -851,22 +854,28 @@ __global__ void __launch_bounds__(THREADS, 1)
           // P = 2^(s scale log2e - m) = P_hi + P_lo, sixteen keys at a time
           const uint64_t sc2 = f32x2(p.scale_log2, p.scale_log2), nm2 = f32x2(-mref, -mref);
           uint64_t rs2[4] = {0, 0, 0, 0};
+#pragma unroll 1
+          for (int c = 0; c < BN; c += 32) {
+            uint32_t s[32];
+            tmem_ld32(tS + c, s);
+            tmem_wait_ld();
 #pragma unroll
-          for (int g = 0; g < BN / 16; ++g) {
-            uint32_t pk[16];  // P_hi, P_lo
+            for (int g = 0; g < 2; ++g) {
+              uint32_t pk[16];  // P_hi, P_lo
 #pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              float x0, x1;
-              f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[g * 16 + e]), __uint_as_float(s[g * 16 + e + 1])),
-                                    sc2, nm2),
-                          x0, x1);
-              const float p0 = ex2(x0), p1 = ex2(x1);
-              rs2[(e >> 1) & 3] = add_f32x2(rs2[(e >> 1) & 3], f32x2(p0, p1));
-              const uint32_t h = pack_bf16(p0, p1);
-              pk[e >> 1] = h;
-              pk[8 + (e >> 1)] = pack_bf16(p0 - __uint_as_float(h << 16), p1 - __uint_as_float(h & 0xffff0000u));
+              for (int e = 0; e < 16; e += 2) {
+                float x0, x1;
+                f32x2_split(fma_f32x2(f32x2(__uint_as_float(s[g * 16 + e]), __uint_as_float(s[g * 16 + e + 1])),
+                                      sc2, nm2),
+                            x0, x1);
+                const float p0 = ex2(x0), p1 = ex2(x1);
+                rs2[(e >> 1) & 3] = add_f32x2(rs2[(e >> 1) & 3], f32x2(p0, p1));
+                const uint32_t h = pack_bf16(p0, p1);
+                pk[e >> 1] = h;
+                pk[8 + (e >> 1)] = pack_bf16(p0 - __uint_as_float(h << 16), p1 - __uint_as_float(h & 0xffff0000u));
+              }
+              tmem_st16(tS + c + g * 16, pk);
             }
-            tmem_st16(tS + g * 16, pk);
           }
           float rs = 0.0f;
 #pragma unroll
