@@ -92,66 +92,67 @@ __device__ __forceinline__ void put_row(const PagePlanArgs &a, int r, int b, int
   a.slots[r] = page < 0 ? -1 : ((long long)page << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
 }
 
-// Lengths as they may be: a negative one counts as 0, one past the table as the table's end.
-__device__ __forceinline__ int length_of(const PagePlanArgs &a, int b, bool &bad) {
-  const int x = a.kv_lens[b], most = a.max_pages << a.page_shift;
-  bad |= x < 0 || x > most;
-  return x < 0 ? 0 : (x > most ? most : x);
-}
-__device__ __forceinline__ int new_of(const PagePlanArgs &a, int b, bool &bad) {
-  const int x = a.new_lens[b];
-  bad |= x < 0;
-  return x < 0 ? 0 : x;
-}
+// A stack's count as it may be.
 __device__ __forceinline__ int count_of(const int *count, int64_t capacity, bool &bad) {
   const int x = *count;
   bad |= x < 0 || x > capacity;
   return x < 0 ? 0 : (x > capacity ? (int)capacity : x);
 }
 
-// The sums; and, where WHOLE, the rows.
-template <bool WHOLE>
+// The sums; and, where WHOLE, the rows.  A thread takes PER sequences and reads their lengths once, all at a time.
+template <bool WHOLE, int PER>
 __global__ void __launch_bounds__(THREADS, 1) plan_kernel(const PagePlanArgs a) {
   __shared__ long long warps[32];
   __shared__ int cu[WHOLE ? ONE_BATCH + 1 : 1];
   __shared__ Grown grown[WHOLE ? ONE_BATCH : 1];
-  const int per = (a.batch + THREADS - 1) / THREADS;
-  const int b0 = min((int64_t)threadIdx.x * per, (int64_t)a.batch), b1 = min(b0 + per, a.batch);
+  const int b0 = threadIdx.x * PER;
   bool bad = false;
+  int fresh[PER], len[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    fresh[i] = b0 + i < a.batch ? a.new_lens[b0 + i] : 0;
+    len[i] = b0 + i < a.batch ? a.kv_lens[b0 + i] : 0;
+  }
   const int count = count_of(a.free_count, a.capacity, bad);
-  long long n = 0, all;
-  for (int b = b0; b < b1; ++b) n += new_of(a, b, bad);
-  const long long before = block_sum(n, all, warps);
+  const int most = a.max_pages << a.page_shift;
+  long long n = 0, all, given;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {  // lengths as they may be
+    bad |= fresh[i] < 0 || len[i] < 0 || len[i] > most;
+    fresh[i] = max(fresh[i], 0);
+    len[i] = min(max(len[i], 0), most);
+    n += fresh[i];
+  }
+  long long at = block_sum(n, all, warps);
   const int rows = (int)min(all, (long long)a.rows);
   bad |= all > a.rows;
-  // tokens behind the rows are not planned
-  auto clipped = [&](long long at) { return (int)min(at, (long long)a.rows); };
-  auto pages = [&](long long len) { return min((len + (1 << a.page_shift) - 1) >> a.page_shift, (long long)a.max_pages); };
-  long long need = 0, at = before;
-  for (int b = b0; b < b1; ++b) {
-    const int x = new_of(a, b, bad), len = length_of(a, b, bad), m = clipped(at + x) - clipped(at);
-    need += pages((long long)len + m) - pages(len);
-    at += x;
+  auto pages = [&](long long x) { return min((x + (1 << a.page_shift) - 1) >> a.page_shift, (long long)a.max_pages); };
+  int first[PER], pages_of[PER];
+  long long need = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {  // tokens behind the rows are not planned
+    first[i] = (int)min(at, (long long)a.rows);
+    at += fresh[i];
+    fresh[i] = (int)min(at, (long long)a.rows) - first[i];
+    pages_of[i] = (int)(pages((long long)len[i] + fresh[i]) - pages(len[i]));
+    need += pages_of[i];
   }
-  long long given;
-  long long off = block_sum(need, given, warps);
+  long long off = block_sum(need, given, warps);  // its barriers lie between the reads above and the writes below
   bad |= given > count;
-  at = before;
-  for (int b = b0; b < b1; ++b) {
-    const int x = new_of(a, b, bad), len = length_of(a, b, bad), m = clipped(at + x) - clipped(at);
-    const Grown g = {len, (int)off};
-    a.cu[b] = clipped(at);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (b0 + i >= a.batch) break;
+    const Grown g = {len[i], (int)off};
+    a.cu[b0 + i] = first[i];
+    a.kv_out[b0 + i] = len[i] + fresh[i];
     if (WHOLE) {
-      cu[b] = clipped(at);
-      grown[b] = g;
+      cu[b0 + i] = first[i];
+      grown[b0 + i] = g;
     } else {
-      static_cast<Grown *>(a.workspace)[1 + b] = g;
+      static_cast<Grown *>(a.workspace)[1 + b0 + i] = g;
     }
-    off += pages((long long)len + m) - pages(len);
-    a.kv_out[b] = len + m;
-    at += x;
+    off += pages_of[i];
   }
-  // every thread has read the count: block_sum's barriers lie between
   if (threadIdx.x == 0) {
     a.cu[a.batch] = rows;
     if (WHOLE) cu[a.batch] = rows;
@@ -183,8 +184,20 @@ __global__ void __launch_bounds__(WIDE) rows_kernel(const PagePlanArgs a) {
   const int rows = ws[0].len, count = ws[0].off;
   auto cu = [&](int i) { return a.cu[i]; };
   const int64_t r0 = (int64_t)blockIdx.x * SPAN;
-  if (threadIdx.x < 2 && r0 < rows)  // the first row's sequence and the last one's
-    range[threadIdx.x] = owner(0, a.batch, (int)min(r0 + threadIdx.x * (SPAN - 1), (int64_t)rows - 1), cu);
+  // The first row's sequence and the last one's, a warp for each, 32 places at a time.
+  if (threadIdx.x < 64 && r0 < rows) {
+    const int end = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int r = (int)min(r0 + end * (SPAN - 1), (int64_t)rows - 1);
+    int lo = 0, hi = a.batch;  // cu[lo] <= r < cu[hi]
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32, mid = min(lo + lane * step, hi);
+      const uint32_t in = __ballot_sync(0xffffffffu, mid < hi && cu(mid) <= r);
+      const int k = 31 - __clz(in);  // lane 0 is always in
+      hi = min(hi, lo + (k + 1) * step);
+      lo += k * step;
+    }
+    if (lane == 0) range[end] = lo;
+  }
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -216,75 +229,129 @@ __device__ __forceinline__ Cut cut_of(const PageTrimArgs &a, int b, int &left, b
   return Cut{(left + up) >> a.page_shift, (len + up) >> a.page_shift};
 }
 
-// The warp counts the entries that name a page, or puts them on the stack from `to` on.
+// A warp counts the entries of [c.first, c.last) that name a page, or puts them on the stack from `to` on.
 template <bool PUT>
 __device__ __forceinline__ int entries(const PageTrimArgs &a, int b, Cut c, long long to, bool &bad) {
+  constexpr int BATCH = 4;  // loads under way
   const int lane = threadIdx.x & 31;
   const int *table = a.table + (int64_t)b * a.table_stride;
   int n = 0;
-  for (int k = c.first; k < c.last; k += 32) {
-    const int x = k + lane < c.last ? table[k + lane] : -1;
-    const bool is = x >= 0 && x < a.num_pages;
-    const uint32_t in = __ballot_sync(0xffffffffu, is);
-    if (PUT && is) {
-      const long long at = to + n + __popc(in & ((1u << lane) - 1));
-      if (at < a.capacity) a.free_pages[at] = x;
+  for (int k = c.first; k < c.last; k += 32 * BATCH) {
+    int x[BATCH];
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) x[i] = k + 32 * i + lane < c.last ? table[k + 32 * i + lane] : -1;
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const bool is = x[i] >= 0 && x[i] < a.num_pages;
+      const uint32_t in = __ballot_sync(0xffffffffu, is);
+      if (PUT && is) {
+        const long long at = to + n + __popc(in & ((1u << lane) - 1));
+        if (at < a.capacity) a.free_pages[at] = x[i];
+      }
+      bad |= k + 32 * i + lane < c.last && !is;
+      n += __popc(in);
     }
-    bad |= k + lane < c.last && !is;
-    n += __popc(in);
   }
   return n;
 }
 
-// All in one block.
+// All in one block: a thread takes a sequence that gives back few pages, a warp one that gives back many.
 __global__ void __launch_bounds__(THREADS, 1) trim_kernel(const PageTrimArgs a) {
+  constexpr int FEW = 4;
   __shared__ long long warps[32];
   __shared__ Cut cuts[ONE_BATCH];
   __shared__ int sums[ONE_BATCH];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = threadIdx.x;
   bool bad = false;
   const int count = count_of(a.free_count, a.capacity, bad);
+  Cut c = {0, 0};
+  int x[FEW], n = 0;
   if (b < a.batch) {
     int left;
-    cuts[b] = cut_of(a, b, left, bad);
+    c = cut_of(a, b, left, bad);
     a.kv_out[b] = left;
   }
-  __syncthreads();
-  for (int i = warp; i < a.batch; i += THREADS / 32) {
-    const int n = entries<false>(a, i, cuts[i], 0, bad);
-    if (lane == 0) sums[i] = n;
+  const bool few = c.last - c.first <= FEW;
+#pragma unroll
+  for (int i = 0; i < FEW; ++i) {
+    x[i] = few && c.first + i < c.last ? a.table[(int64_t)b * a.table_stride + c.first + i] : -1;
+    const bool is = x[i] >= 0 && x[i] < a.num_pages;
+    bad |= few && c.first + i < c.last && !is;
+    if (!is) x[i] = -1;
+    n += is;
   }
-  __syncthreads();
+  uint32_t many = __ballot_sync(0xffffffffu, !few);
+  cuts[b] = c;
+  __syncwarp();
+  for (uint32_t m = many; m; m &= m - 1) {
+    const int i = __ffs(m) - 1, got = entries<false>(a, 32 * warp + i, cuts[32 * warp + i], 0, bad);
+    if (lane == i) n = got;
+  }
   long long all;
-  const long long before = block_sum(b < a.batch ? sums[b] : 0, all, warps);
-  if (b < a.batch) sums[b] = (int)before;
-  __syncthreads();
-  for (int i = warp; i < a.batch; i += THREADS / 32) entries<true>(a, i, cuts[i], (long long)count + sums[i], bad);
+  long long to = count + block_sum(n, all, warps);
+  sums[b] = (int)(to - count);
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < FEW; ++i)
+    if (x[i] >= 0) {
+      if (to < a.capacity) a.free_pages[to] = x[i];
+      ++to;
+    }
+  bool seen = false;  // reported by the count
+  for (uint32_t m = many; m; m &= m - 1) {
+    const int i = 32 * warp + __ffs(m) - 1;
+    entries<true>(a, i, cuts[i], (long long)count + sums[i], seen);
+  }
   bad |= count + all > a.capacity;
   if (threadIdx.x == 0) *a.count_out = (int)min(count + all, (long long)a.capacity);
   if (bad) report(a.status);
 }
 
-// In two launches: a warp counts a sequence's entries, then puts them.
+// In two launches, a block a sequence: a warp counts a piece of its entries, then puts them.
+constexpr int PIECES = WIDE / 32;
 struct Back {
-  Cut cut;
-  int n;
+  int n[PIECES];
 };
+__device__ __forceinline__ Cut piece_of(Cut c, int warp) {
+  const int step = ((c.last - c.first + PIECES - 1) / PIECES + 31) & ~31;
+  const int first = min(c.first + warp * step, c.last);
+  return Cut{first, min(first + step, c.last)};
+}
+// The workspace: the count, the cut and the entries of each sequence, and those of its pieces.
+struct TrimSpace {
+  int *count, *sums;
+  Cut *cuts;
+  Back *pieces;
+};
+__host__ __device__ inline TrimSpace trim_space(void *p, int batch) {
+  TrimSpace s;
+  s.pieces = static_cast<Back *>(p);
+  s.cuts = reinterpret_cast<Cut *>(s.pieces + batch);
+  s.sums = reinterpret_cast<int *>(s.cuts + batch);
+  s.count = s.sums + batch;
+  return s;
+}
 
 __global__ void __launch_bounds__(WIDE) trim_count_kernel(const PageTrimArgs a) {
-  const int b = blockIdx.x * (WIDE / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  Back *ws = static_cast<Back *>(a.workspace);
+  __shared__ int sum;
+  const int b = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const TrimSpace ws = trim_space(a.workspace, a.batch);
   bool bad = false;
-  if (b == 0 && lane == 0) ws[0].n = count_of(a.free_count, a.capacity, bad);
-  if (b < a.batch) {
-    int left;
-    Back x;
-    x.cut = cut_of(a, b, left, bad);
-    x.n = entries<false>(a, b, x.cut, 0, bad);
-    if (lane == 0) {
-      ws[1 + b] = x;
-      a.kv_out[b] = left;
-    }
+  if (threadIdx.x == 0) sum = 0;
+  if (threadIdx.x == 0 && b == 0) *ws.count = count_of(a.free_count, a.capacity, bad);
+  int left;
+  const Cut c = cut_of(a, b, left, bad);
+  __syncthreads();
+  const int n = entries<false>(a, b, piece_of(c, warp), 0, bad);
+  if (lane == 0) {
+    ws.pieces[b].n[warp] = n;
+    atomicAdd(&sum, n);
+  }
+  __syncthreads();  // kv_out may be kv_lens, which every warp has read
+  if (threadIdx.x == 0) {
+    ws.cuts[b] = c;
+    ws.sums[b] = sum;
+    a.kv_out[b] = left;
   }
   if (bad) report(a.status);
   pdl_launch_dependents();
@@ -293,26 +360,25 @@ __global__ void __launch_bounds__(WIDE) trim_count_kernel(const PageTrimArgs a) 
 __global__ void __launch_bounds__(WIDE) trim_put_kernel(const PageTrimArgs a) {
   __shared__ long long warps[32];
   pdl_wait();
-  const Back *ws = static_cast<const Back *>(a.workspace);
-  const int b0 = blockIdx.x * (WIDE / 32), b = b0 + (threadIdx.x >> 5);
-  const int count = ws[0].n;
-  // entries of the sequences before the block's; block 0 takes all, for the new count
+  const TrimSpace ws = trim_space(a.workspace, a.batch);
+  const int b = blockIdx.x, warp = threadIdx.x >> 5;
+  const int count = *ws.count;
+  // entries of the sequences before; block 0 takes all, for the new count
   long long n = 0, all;
-  for (int i = threadIdx.x; i < (blockIdx.x ? b0 : a.batch); i += WIDE) n += ws[1 + i].n;
+  for (int i = threadIdx.x; i < (b ? b : a.batch); i += WIDE) n += ws.sums[i];
+  const Cut c = ws.cuts[b];
+  const Back back = ws.pieces[b];
   block_sum(n, all, warps);
-  bool bad = false;
-  if (blockIdx.x == 0) {
-    bad = count + all > a.capacity;
+  if (b == 0) {
+    if (count + all > a.capacity) report(a.status);
     if (threadIdx.x == 0) *a.count_out = (int)min(count + all, (long long)a.capacity);
     all = 0;
   }
-  if (b < a.batch) {
-    long long to = count + all;
-    for (int i = b0; i < b; ++i) to += ws[1 + i].n;
-    bool seen = false;  // reported by the count
-    entries<true>(a, b, ws[1 + b].cut, to, seen);
-  }
-  if (bad) report(a.status);
+  long long to = count + all;
+#pragma unroll
+  for (int i = 0; i < PIECES; ++i) to += i < warp ? back.n[i] : 0;
+  bool seen = false;  // reported by the count
+  entries<true>(a, b, piece_of(c, warp), to, seen);
 }
 
 template <typename A>
@@ -332,14 +398,17 @@ cudaError_t after(void (*kernel)(A), unsigned grid, int threads, const A &a, cud
 }  // namespace
 
 size_t page_plan_workspace(int batch) { return (size_t)(batch + 1) * sizeof(Grown); }
-size_t page_trim_workspace(int batch) { return (size_t)(batch + 1) * sizeof(Back); }
+size_t page_trim_workspace(int batch) { return (size_t)batch * (sizeof(Back) + sizeof(Cut) + sizeof(int)) + 16; }
 
 cudaError_t launch_page_plan(const PagePlanArgs &a, cudaStream_t st) {
   if (a.batch <= ONE_BATCH && a.rows <= ONE_ROWS) {
-    plan_kernel<true><<<1, THREADS, 0, st>>>(a);
+    plan_kernel<true, 1><<<1, THREADS, 0, st>>>(a);
     return cudaGetLastError();
   }
-  plan_kernel<false><<<1, THREADS, 0, st>>>(a);
+  if (a.batch <= THREADS)
+    plan_kernel<false, 1><<<1, THREADS, 0, st>>>(a);
+  else
+    plan_kernel<false, kMaxPagedBatch / THREADS><<<1, THREADS, 0, st>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || a.rows == 0) return e;
   return after(rows_kernel, (unsigned)((a.rows + 4 * WIDE - 1) / (4 * WIDE)), WIDE, a, st);
@@ -350,10 +419,9 @@ cudaError_t launch_page_trim(const PageTrimArgs &a, cudaStream_t st) {
     trim_kernel<<<1, THREADS, 0, st>>>(a);
     return cudaGetLastError();
   }
-  const unsigned grid = (a.batch + WIDE / 32 - 1) / (WIDE / 32);
-  trim_count_kernel<<<grid, WIDE, 0, st>>>(a);
+  trim_count_kernel<<<a.batch, WIDE, 0, st>>>(a);
   const cudaError_t e = cudaGetLastError();
-  return e != cudaSuccess ? e : after(trim_put_kernel, grid, WIDE, a, st);
+  return e != cudaSuccess ? e : after(trim_put_kernel, a.batch, WIDE, a, st);
 }
 
 }  // namespace chain

@@ -1623,19 +1623,12 @@ __global__ void __launch_bounds__(256, 2) shared_join_kernel(const Params p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = lane / ROWS;
   const long long end = bd.u0 + p.overhead + (long long)bd.w * bd.nt;
   auto tile_of = [&](int k) { return tile_at(p, run_start<RUNS>(bd.total, k) - bd.u0, bd.w); };
-  auto in_unit = [&](int k) { return k < RUNS && run_start<RUNS>(bd.total, k) < end; };
-  auto cuts = [&](int k) { return k > 0 && run_start<RUNS>(bd.total, k) > bd.u0 && tile_of(k) > 0; };
-  int before = 0, last = (int)blockIdx.x + 2;  // the unit's boundaries before this one, and the end of its parts
-  for (uint32_t in = ~0u; in == ~0u;) {
-    in = __ballot_sync(0xffffffffu, cuts((int)blockIdx.x - before - lane));
-    before += in == ~0u ? 32 : __ffs(~in) - 1;
-  }
+  // The first run that begins at cost x or behind it.
+  auto run_from = [&](long long x) { return (int)min(quotient(x * RUNS + bd.total - 1, bd.total), (long long)RUNS); };
+  const int c = run_from(bd.u0 + p.overhead + bd.w);  // the unit's first boundary; its first part is run c - 1's
+  const int last = run_from(end);                     // the end of its parts
+  const int before = (int)blockIdx.x + 1 - c;
   if (before >= CHUNKS) return;
-  for (uint32_t in = ~0u; in == ~0u;) {
-    in = __ballot_sync(0xffffffffu, in_unit(last + lane));
-    last += in == ~0u ? 32 : __ffs(~in) - 1;
-  }
-  const int c = (int)blockIdx.x + 1 - before;  // the unit's first boundary; its first part is run c - 1's
   const bool few = last - c + 1 <= FEW;
   if (few && before > 0) return;
   // a run shorter than a key tile may hold none of the unit, and then no part
@@ -1661,7 +1654,7 @@ __global__ void __launch_bounds__(256, 2) shared_join_kernel(const Params p) {
   float4 o[COLS];
   if (few) {
     for (int col0 = (warp * HALVES + half) * COLS; col0 < D / 4; col0 += 8 * HALVES * COLS) {
-      join_parts<D, SLOT, 4, COLS>(p, c, c - 1, 1, last, r, col0, has_part, m, l, o);
+      join_parts<D, SLOT, 2, COLS>(p, c, c - 1, 1, last, r, col0, has_part, m, l, o);
       if (!valid) continue;
 #pragma unroll
       for (int q = 0; q < COLS; ++q) put(r, tok, col0 + q, o[q], m, l);
