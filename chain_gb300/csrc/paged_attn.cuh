@@ -1070,12 +1070,13 @@ struct TokenLayout {
   static constexpr int KS = KEYS < 2048 / D ? KEYS : 2048 / D;  // of a stage: 8 KB of K and V at most
   static constexpr int STAGES = 2;
   static constexpr uint32_t HALF = KS * D * 2, STAGE = 2 * HALF;
-  static constexpr uint32_t WARP = STAGES * STAGE;  // a warp's ring; then its share of O
-  static constexpr uint32_t ALLOC = WARPS * WARP;
+  static constexpr uint32_t WARP = STAGES * STAGE;  // a warp's ring
   static constexpr int OPITCH = D + 4;
+  static constexpr uint32_t SHARE = TOK_ROWS * OPITCH * 4;  // a warp's O, beside the rings: the next unit's keys are
+                                                            // under way while a unit is joined
+  static constexpr uint32_t ALLOC = WARPS * (WARP + SHARE);
   static constexpr int COST = 4, OVERHEAD = D == 128 ? 4 : 8;
   static_assert(MAX_BATCH * 8 <= ALLOC, "the schedule's sums use the rings");
-  static_assert(TOK_ROWS * OPITCH * 4 <= WARP, "O in the ring");
   static_assert(KEYS % KS == 0 && KS % 16 == 0, "keys");
 };
 
@@ -1110,7 +1111,7 @@ __global__ void __launch_bounds__(32 * WARPS, TokenLayout<D, WARPS>::BLOCKS) pag
   constexpr int RPC = 32 / CH;          // rows that a copy of the warp covers
   constexpr int PER = L::KEYS / L::KS;  // stages of a key tile
   extern __shared__ uint8_t smem_raw[];
-  __shared__ Unit next;
+  __shared__ Unit next[2];
   __shared__ float2 ml[WARPS][TOK_ROWS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   long long *sums = reinterpret_cast<long long *>(smem_raw);
@@ -1122,15 +1123,18 @@ __global__ void __launch_bounds__(32 * WARPS, TokenLayout<D, WARPS>::BLOCKS) pag
   if (warp == 0) begin_run<L::RUNS, MODE>(p, sums, run, lane);
   const uint32_t ring = smem_u32(smem_raw) + warp * L::WARP;
   const int page = 1 << p.s.page_shift, pool = (int)p.s.num_pages;
-  while (true) {
-    if (warp == 0) {
-      const Unit u = next_of<MODE>(p, run, lane);
-      if (lane == 0) next = u;
-    }
-    __syncthreads();
-    const Unit u = next;
-    if (u.head < 0) break;
-    const int steps = (u.j1 - u.j0) * PER;
+  float *mine = reinterpret_cast<float *>(smem_raw + WARPS * L::WARP + warp * L::SHARE);
+  auto publish = [&](Unit &to) {  // by warp 0
+    const Unit n = next_of<MODE>(p, run, lane);
+    if (lane == 0) to = n;
+  };
+  if (warp == 0) publish(next[0]);
+  __syncthreads();
+  Unit u = next[0], done = {};
+  bool first = true;
+  for (int turn = 0;; turn ^= 1) {
+    // What the unit needs first: its first stage and Q, asked for while the unit before is joined.
+    const int steps = u.head < 0 ? 0 : (u.j1 - u.j0) * PER;
     const int *table = p.s.table + u.b * p.s.table_stride;
     const __nv_bfloat16 *kc = static_cast<const __nv_bfloat16 *>(p.kc.ptr) + u.head * p.kc.s_head;
     const __nv_bfloat16 *vc = static_cast<const __nv_bfloat16 *>(p.vc.ptr) + u.head * p.vc.s_head;
@@ -1191,6 +1195,80 @@ __global__ void __launch_bounds__(32 * WARPS, TokenLayout<D, WARPS>::BLOCKS) pag
         q[kk][2 + h] = valid ? *reinterpret_cast<const uint32_t *>(src + kk * 16 + 8) : 0u;
       }
     }
+    if (!first) {  // joins the warps' shares of the unit before
+      constexpr int COLS = D / 8;  // a thread's, of row threadIdx.x / 8
+      const int row = threadIdx.x >> 3, c0 = (threadIdx.x & 7) * COLS, tok = row / p.G;
+      if (row < TOK_ROWS && tok < done.ntok && tok < p.tpt) {
+        float top = -INFINITY, sum = 0.0f, x[COLS];
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) top = fmaxf(top, ml[w][row].x);
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) x[c] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+          const float2 v = ml[w][row];
+          const float f = v.x == -INFINITY ? 0.0f : ex2(v.x - top);
+          sum = fmaf(v.y, f, sum);
+          const float4 *src =
+              reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(smem_raw + WARPS * L::WARP + w * L::SHARE) + row * L::OPITCH + c0);
+#pragma unroll
+          for (int c = 0; c < COLS / 4; ++c) {
+            const float4 y = src[c];
+            x[4 * c] = fmaf(y.x, f, x[4 * c]);
+            x[4 * c + 1] = fmaf(y.y, f, x[4 * c + 1]);
+            x[4 * c + 2] = fmaf(y.z, f, x[4 * c + 2]);
+            x[4 * c + 3] = fmaf(y.w, f, x[4 * c + 3]);
+          }
+        }
+        const int64_t pre_pitch = (int64_t)p.total * p.G, pre_row = (int64_t)done.tok0 * p.G + row;
+        float4 *pre = reinterpret_cast<float4 *>(p.pre_o) + (done.head * (D / 4) + c0 / 4) * pre_pitch + pre_row;
+        if (MODE == OWN && done.slot < 0 && done.pre) {  // the row's sums over its group's prefix
+          pdl_wait();
+          const float2 v = p.pre_ml[done.head * pre_pitch + pre_row];
+          const float high = fmaxf(top, v.x), f = high == -INFINITY ? 0.0f : ex2(top - high);
+          const float g = high == -INFINITY ? 0.0f : ex2(v.x - high);
+          top = high;
+          sum = fmaf(sum, f, v.y * g);
+#pragma unroll
+          for (int c = 0; c < COLS / 4; ++c) {
+            const float4 y = pre[c * pre_pitch];
+            x[4 * c] = fmaf(x[4 * c], f, y.x * g);
+            x[4 * c + 1] = fmaf(x[4 * c + 1], f, y.y * g);
+            x[4 * c + 2] = fmaf(x[4 * c + 2], f, y.z * g);
+            x[4 * c + 3] = fmaf(x[4 * c + 3], f, y.w * g);
+          }
+        }
+        if (MODE == SHARED && done.slot < 0) {
+#pragma unroll
+          for (int c = 0; c < COLS / 4; ++c)
+            pre[c * pre_pitch] = make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+          if ((threadIdx.x & 7) == 0) p.pre_ml[done.head * pre_pitch + pre_row] = make_float2(top, sum);
+        } else if (done.slot < 0) {
+          const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+          const int64_t qhead = (int64_t)done.head * p.G + row - tok * p.G;
+          uint4 *dst = reinterpret_cast<uint4 *>(p.O + ((int64_t)done.tok0 + tok) * p.o_stok + qhead * p.o_shead + c0);
+#pragma unroll
+          for (int c = 0; c < COLS / 8; ++c)
+            dst[c] = make_uint4(pack_bf16(x[8 * c] * inv, x[8 * c + 1] * inv), pack_bf16(x[8 * c + 2] * inv, x[8 * c + 3] * inv),
+                                pack_bf16(x[8 * c + 4] * inv, x[8 * c + 5] * inv),
+                                pack_bf16(x[8 * c + 6] * inv, x[8 * c + 7] * inv));
+          if ((threadIdx.x & 7) == 0)
+            p.LSE[qhead * p.lse_shead + done.tok0 + tok] =
+                sum > 0.0f ? (top + lg2(sum)) * 0.69314718055994531f : -INFINITY;
+        } else {
+          const int64_t slot = (int64_t)blockIdx.x * 2 + done.slot;
+          float4 *dst = reinterpret_cast<float4 *>(p.part_o) + slot * (TOK_ROWS * D / 4) + row;
+#pragma unroll
+          for (int c = 0; c < COLS / 4; ++c)
+            dst[(c0 / 4 + c) * TOK_ROWS] = make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+          if ((threadIdx.x & 7) == 0) p.part_ml[slot * TOK_ROWS + row] = make_float2(top, sum);
+        }
+      }
+      __syncthreads();  // the shares and ml are free
+    }
+    first = false;
+    if (u.head < 0) break;
+    if (warp == 0) publish(next[turn ^ 1]);
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, o[D / 8][4];
 #pragma unroll
     for (int n = 0; n < D / 8; ++n)
@@ -1277,8 +1355,7 @@ __global__ void __launch_bounds__(32 * WARPS, TokenLayout<D, WARPS>::BLOCKS) pag
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncwarp();
-    // the warps' shares: O over the warp's own ring
-    float *mine = reinterpret_cast<float *>(smem_raw + warp * L::WARP);
+    // the warps' shares
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int row = lane / 4 + 8 * h;
@@ -1291,77 +1368,8 @@ __global__ void __launch_bounds__(32 * WARPS, TokenLayout<D, WARPS>::BLOCKS) pag
             make_float2(o[n][2 * h], o[n][2 * h + 1]);
     }
     __syncthreads();
-    {
-      constexpr int COLS = D / 8;  // a thread's, of row threadIdx.x / 8
-      const int row = threadIdx.x >> 3, c0 = (threadIdx.x & 7) * COLS, tok = row / p.G;
-      if (row < TOK_ROWS && tok < u.ntok && tok < p.tpt) {
-        float top = -INFINITY, sum = 0.0f, x[COLS];
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) top = fmaxf(top, ml[w][row].x);
-#pragma unroll
-        for (int c = 0; c < COLS; ++c) x[c] = 0.0f;
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) {
-          const float2 v = ml[w][row];
-          const float f = v.x == -INFINITY ? 0.0f : ex2(v.x - top);
-          sum = fmaf(v.y, f, sum);
-          const float4 *src =
-              reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(smem_raw + w * L::WARP) + row * L::OPITCH + c0);
-#pragma unroll
-          for (int c = 0; c < COLS / 4; ++c) {
-            const float4 y = src[c];
-            x[4 * c] = fmaf(y.x, f, x[4 * c]);
-            x[4 * c + 1] = fmaf(y.y, f, x[4 * c + 1]);
-            x[4 * c + 2] = fmaf(y.z, f, x[4 * c + 2]);
-            x[4 * c + 3] = fmaf(y.w, f, x[4 * c + 3]);
-          }
-        }
-        const int64_t pre_pitch = (int64_t)p.total * p.G, pre_row = (int64_t)u.tok0 * p.G + row;
-        float4 *pre = reinterpret_cast<float4 *>(p.pre_o) + (u.head * (D / 4) + c0 / 4) * pre_pitch + pre_row;
-        if (MODE == OWN && u.slot < 0 && u.pre) {  // the row's sums over its group's prefix
-          pdl_wait();
-          const float2 v = p.pre_ml[u.head * pre_pitch + pre_row];
-          const float high = fmaxf(top, v.x), f = high == -INFINITY ? 0.0f : ex2(top - high);
-          const float g = high == -INFINITY ? 0.0f : ex2(v.x - high);
-          top = high;
-          sum = fmaf(sum, f, v.y * g);
-#pragma unroll
-          for (int c = 0; c < COLS / 4; ++c) {
-            const float4 y = pre[c * pre_pitch];
-            x[4 * c] = fmaf(x[4 * c], f, y.x * g);
-            x[4 * c + 1] = fmaf(x[4 * c + 1], f, y.y * g);
-            x[4 * c + 2] = fmaf(x[4 * c + 2], f, y.z * g);
-            x[4 * c + 3] = fmaf(x[4 * c + 3], f, y.w * g);
-          }
-        }
-        if (MODE == SHARED && u.slot < 0) {
-#pragma unroll
-          for (int c = 0; c < COLS / 4; ++c)
-            pre[c * pre_pitch] = make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
-          if ((threadIdx.x & 7) == 0) p.pre_ml[u.head * pre_pitch + pre_row] = make_float2(top, sum);
-        } else if (u.slot < 0) {
-          const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-          const int64_t qhead = (int64_t)u.head * p.G + row - tok * p.G;
-          uint4 *dst = reinterpret_cast<uint4 *>(p.O + ((int64_t)u.tok0 + tok) * p.o_stok + qhead * p.o_shead + c0);
-#pragma unroll
-          for (int c = 0; c < COLS / 8; ++c)
-            dst[c] = make_uint4(pack_bf16(x[8 * c] * inv, x[8 * c + 1] * inv), pack_bf16(x[8 * c + 2] * inv, x[8 * c + 3] * inv),
-                                pack_bf16(x[8 * c + 4] * inv, x[8 * c + 5] * inv),
-                                pack_bf16(x[8 * c + 6] * inv, x[8 * c + 7] * inv));
-          if ((threadIdx.x & 7) == 0)
-            p.LSE[qhead * p.lse_shead + u.tok0 + tok] =
-                sum > 0.0f ? (top + lg2(sum)) * 0.69314718055994531f : -INFINITY;
-        } else {
-          const int64_t slot = (int64_t)blockIdx.x * 2 + u.slot;
-          float4 *dst = reinterpret_cast<float4 *>(p.part_o) + slot * (TOK_ROWS * D / 4) + row;
-#pragma unroll
-          for (int c = 0; c < COLS / 4; ++c)
-            dst[(c0 / 4 + c) * TOK_ROWS] = make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
-          if ((threadIdx.x & 7) == 0) p.part_ml[slot * TOK_ROWS + row] = make_float2(top, sum);
-        }
-      }
-    }
-    __syncthreads();  // the rings, ml and `next` are free
+    done = u;
+    u = next[turn ^ 1];
   }
   if (MODE == OWN) pdl_wait();  // as above
 }

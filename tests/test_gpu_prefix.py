@@ -152,6 +152,30 @@ def test_large_scores_on_either_side(cg, news, rise):
     check(c, q, o, lse, True, 0.5)
 
 
+# V's factor in each 32 positions in turn
+FACTORS = {"large": [2.0 ** 12], "small": [2.0 ** -12], "tiny": [2.0 ** -100], "huge": [2.0 ** 100], "zeros": [0.0],
+           "in turn": [1.0, 2.0 ** 10, 2.0 ** -30, 0.0, 300.0, 2.0 ** -9, 1.0]}
+
+
+@pytest.mark.parametrize("d,H,Hkv,count", [(128, 16, 4, 40), (64, 16, 2, 20), (128, 8, 4, 3)])
+@pytest.mark.parametrize("name", FACTORS)
+def test_values_of_every_size(cg, name, d, H, Hkv, count):
+    P, page = 1152, 32
+    c = Shared([(count, P)], behind(P, [1 + 3 * i for i in range(count)], page), [1] * count, Hkv, d, page, 48)
+    f = FACTORS[name]
+    for i, x in enumerate(c.v):
+        f_at = torch.tensor([f[(j // 32) % len(f)] for j in range(len(x))])[:, None, None]
+        c.v[i] = (x.float() * f_at).bfloat16()
+    c.fill().cuda()
+    q = cs.normal((c.total, H, d), 49)
+    o, lse = cg.attention_fwd_paged_prefix(q.cuda(), c.kcd, c.vcd, *c.args, causal=True)
+    assert cg.chain_check()[0] == 0
+    check(c, q, o, lse, True, d ** -0.5)
+    if f != [0.0]:
+        ref = [reference(c, q, b, True, d ** -0.5) for b in range(count)]
+        assert_fwd_close(o.float() / max(f), torch.cat([r[0] for r in ref]) / max(f))
+
+
 @pytest.mark.parametrize("news", [[1, 1, 1], [33, 1, 5]])
 def test_strided_tensors_and_rows_behind_the_last_sequence(cg, news):
     H, d = 6, 128
