@@ -17,6 +17,10 @@
 namespace chain {
 namespace {
 
+// Two passes and one, 32 heads on 8, d = 128, second-level cache cold: single tokens, 64 sequences of 512
+// positions (128 MB in all) 44 us and 34, of 1,024 44 and 46, of 2,048 46 and 69; 16 of 2,048 35 and 31, of 4,096 37
+// and 43.  32 sequences of 1,024 (128 MB), 16 new tokens each 66 and 50, 64 each 98 and 70.  Query tiles that are
+// full: 4 sequences of 16,128 (252 MB), 128 new tokens each 177 and 151.
 constexpr int64_t ALONE_BYTES = int64_t(1) << 27;
 
 size_t rows_bytes(int64_t rows, int d) { return (size_t)rows * d * sizeof(float); }
@@ -28,11 +32,12 @@ cudaError_t launch(const PrefixAttnArgs &x, const WaitCfg &wc, cudaStream_t st) 
   own.group_cu = x.group_cu;
   own.group_lens = x.group_lens;
   own.groups = x.groups;
-  // So few keys that single tokens read them sooner each by itself than in two passes: the most that the table
-  // can name, since the lengths are on the device.
+  // One pass where two would not pay: with few keys (the most that the table can name, since the lengths are on
+  // the device), and with so many tokens a sequence that each fills its own query tiles: they are multiplied as
+  // often, and read from the second-level cache.
   const int64_t keys = (int64_t)a.seqs.batch * a.seqs.max_pages << a.seqs.page_shift;
-  if (few_rows(a, own.G) && keys * a.Hkv * D * 4 <= ALONE_BYTES)
-    return launch_pass<D, OWN>(a, own, a.seqs.batch, true, may_have_chunks(a, own.G), false, st);
+  if (keys * a.Hkv * D * 4 <= ALONE_BYTES || a.total >= 2 * (int64_t)own.utok * a.seqs.batch)
+    return launch_pass<D, OWN>(a, own, a.seqs.batch, few_rows(a, own.G), may_have_chunks(a, own.G), false, st);
   const int64_t rows = (int64_t)a.total * a.H;
   uint8_t *ws = static_cast<uint8_t *>(a.workspace) + 2 * pass_workspace(D);
   own.pre_o = reinterpret_cast<float *>(ws);

@@ -89,6 +89,7 @@ CASES = {
                                   [9 * i + 9 for i in range(12)], 16, 4, 128, 128),
     "chunks of groups": ([(2, 300), (3, 1000)], behind(300, [40, 3]) + behind(1000, [70, 5, 1]), [30, 3, 70, 5, 1],
                          14, 2, 128, 16),
+    "full query tiles": ([(3, 500)], behind(500, [200, 150, 150], 32), [200, 130, 100], 8, 2, 128, 32),
     "one head for all": ([(30, 700)], behind(700, range(1, 31), 64), [1] * 30, 64, 1, 64, 64),
     "a head for each": ([(30, 700)], behind(700, range(1, 31), 64), [1] * 30, 4, 4, 128, 64),
     "padded with empty sequences": ([(40, 400)], [0, 0] + behind(400, [5, 1, 90]) + [0] * 35, [0, 0, 1, 1, 1] + [0] * 35,
