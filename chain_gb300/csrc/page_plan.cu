@@ -280,17 +280,22 @@ __global__ void __launch_bounds__(THREADS, 1) trim_kernel(const PageTrimArgs a) 
     if (!is) x[i] = -1;
     n += is;
   }
-  uint32_t many = __ballot_sync(0xffffffffu, !few);
   cuts[b] = c;
-  __syncwarp();
-  for (uint32_t m = many; m; m &= m - 1) {
-    const int i = __ffs(m) - 1, got = entries<false>(a, 32 * warp + i, cuts[32 * warp + i], 0, bad);
-    if (lane == i) n = got;
-  }
+  const bool many = __syncthreads_or(!few);
+  auto each = [&](auto &&f) {  // the sequences that a warp takes
+    for (int i = warp; many && i < a.batch; i += THREADS / 32)
+      if (cuts[i].last - cuts[i].first > FEW) f(i);
+  };
+  each([&](int i) {
+    const int got = entries<false>(a, i, cuts[i], 0, bad);
+    if (lane == 0) sums[i] = got;
+  });
+  __syncthreads();
+  if (!few) n = sums[b];
   long long all;
   long long to = count + block_sum(n, all, warps);
   sums[b] = (int)(to - count);
-  __syncwarp();
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < FEW; ++i)
     if (x[i] >= 0) {
@@ -298,10 +303,7 @@ __global__ void __launch_bounds__(THREADS, 1) trim_kernel(const PageTrimArgs a) 
       ++to;
     }
   bool seen = false;  // reported by the count
-  for (uint32_t m = many; m; m &= m - 1) {
-    const int i = 32 * warp + __ffs(m) - 1;
-    entries<true>(a, i, cuts[i], (long long)count + sums[i], seen);
-  }
+  each([&](int i) { entries<true>(a, i, cuts[i], (long long)count + sums[i], seen); });
   bad |= count + all > a.capacity;
   if (threadIdx.x == 0) *a.count_out = (int)min(count + all, (long long)a.capacity);
   if (bad) report(a.status);
