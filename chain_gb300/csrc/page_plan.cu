@@ -12,9 +12,11 @@
 // Giving back is one prefix sum, of the entries of each sequence that name a page, and a
 // copy of those entries.
 //
-// Small calls are one block, whose time is its dependent loads (lengths, then entries, then stores:
-// 3 us): a second launch would cost as much again.  Large ones are memory's: the sums in one block (or, for what
-// goes back, the counts in all), and a second launch that expands with every SM.
+// Small calls are one block, whose time is its dependent loads (lengths, sums, entries, stores): one step of
+// 512 requests 3.9 us, of one 2.7 (again and again in a graph; 9.4 and 7.3 with the second-level cache cold and a
+// graph's start).  Large ones take two launches, the sums in one block (or, for what goes back, the counts in all) and
+// the expansion by every SM: 64 prompts of 951,000 rows 10 us, 12 MB; 366,000 pages of 512 sequences given back 10 us
+// (28 with one warp to a sequence).
 #include "internal.h"
 
 namespace chain {
@@ -23,8 +25,11 @@ namespace {
 constexpr int THREADS = 1024;     // of a block that sums
 constexpr int ONE_BATCH = 1024;   // most sequences of a one-block plan: their sums lie in shared memory
 constexpr int WIDE = 256;         // threads of a block that expands
-constexpr int64_t ONE_ROWS = 8192;
-constexpr int64_t ONE_ENTRIES = 1 << 17;
+// Most rows, and most entries of a table, that one block takes.  Rows, one block and two launches: 1,024 3.5 us and
+// 6.8, 4,096 6.2 and 7.1, 8,192 9.4 and 6.8.  Entries: where a few tokens go back 2.9 us and 4.3 at any size of the table;
+// where whole sequences do, 15,600 entries 9.9 and 4.6, 64,000 20.7 and 4.1.
+constexpr int64_t ONE_ROWS = 4096;
+constexpr int64_t ONE_ENTRIES = 1 << 15;
 
 __device__ __forceinline__ void report(DevStatus *s) { atomicExch(&s->reserved[0], 1); }
 
@@ -403,27 +408,40 @@ size_t page_plan_workspace(int batch) { return (size_t)(batch + 1) * sizeof(Grow
 size_t page_trim_workspace(int batch) { return (size_t)batch * (sizeof(Back) + sizeof(Cut) + sizeof(int)) + 16; }
 
 cudaError_t launch_page_plan(const PagePlanArgs &a, cudaStream_t st) {
+  timing_mark(st, 0);
   if (a.batch <= ONE_BATCH && a.rows <= ONE_ROWS) {
     plan_kernel<true, 1><<<1, THREADS, 0, st>>>(a);
-    return cudaGetLastError();
+    const cudaError_t e = cudaGetLastError();
+    timing_mark(st, 1);
+    return e;
   }
   if (a.batch <= THREADS)
     plan_kernel<false, 1><<<1, THREADS, 0, st>>>(a);
   else
     plan_kernel<false, kMaxPagedBatch / THREADS><<<1, THREADS, 0, st>>>(a);
   cudaError_t e = cudaGetLastError();
+  timing_mark(st, 1);
   if (e != cudaSuccess || a.rows == 0) return e;
-  return after(rows_kernel, (unsigned)((a.rows + 4 * WIDE - 1) / (4 * WIDE)), WIDE, a, st);
+  e = after(rows_kernel, (unsigned)((a.rows + 4 * WIDE - 1) / (4 * WIDE)), WIDE, a, st);
+  timing_mark(st, 2);
+  return e;
 }
 
 cudaError_t launch_page_trim(const PageTrimArgs &a, cudaStream_t st) {
+  timing_mark(st, 0);
   if (a.batch <= ONE_BATCH && (int64_t)a.batch * a.max_pages <= ONE_ENTRIES) {
     trim_kernel<<<1, THREADS, 0, st>>>(a);
-    return cudaGetLastError();
+    const cudaError_t e = cudaGetLastError();
+    timing_mark(st, 1);
+    return e;
   }
   trim_count_kernel<<<a.batch, WIDE, 0, st>>>(a);
-  const cudaError_t e = cudaGetLastError();
-  return e != cudaSuccess ? e : after(trim_put_kernel, a.batch, WIDE, a, st);
+  cudaError_t e = cudaGetLastError();
+  timing_mark(st, 1);
+  if (e != cudaSuccess) return e;
+  e = after(trim_put_kernel, a.batch, WIDE, a, st);
+  timing_mark(st, 2);
+  return e;
 }
 
 }  // namespace chain

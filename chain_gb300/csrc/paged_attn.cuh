@@ -43,13 +43,14 @@
 // Calls of single tokens go to paged_token_kernel, further down, which shares the split.
 //
 // Bounds, and what was measured (32 heads on 8, pages of 64 to 128):
-//   chunks: the chain of softmax and products.  d = 128, 2,048 tokens over 32,768: 1,090 us,
-//   980 TFLOP/s (P_lo's product not counted; 775 us with one bf16 of P), the tensor pipe 61% busy: a
+//   chunks: the chain of softmax and products.  d = 128, 2,048 tokens over 32,768: 1,030 us,
+//   1,035 TFLOP/s (P_lo's product not counted; 775 us with one bf16 of P, before the softmax was rolled): a
 //   stream's softmax and its three products follow each other, since P shares S's columns; two
-//   streams overlap them.  d = 64: 765 us, 700 TFLOP/s, the tensor pipe 39% busy.
-//   single tokens: memory.  d = 128, 64 sequences of 8,192: 363 us, 2.15 GB at 5.9 TB/s;
-//   d = 64: 196 us, 1.07 GB at 5.5 TB/s.  One sequence of 131,072: 99 us, 5.4 TB/s, with
-//   the start, the join and the ends of the runs; of 100: 6.4 us, all latency.
+//   streams overlap them.  A step of both takes 2.3 us: a softmax 1.0, its products 0.8, and what passes
+//   between the barriers' two sides 0.5.  d = 64: 760 us, 700 TFLOP/s.
+//   single tokens: memory.  d = 128, 64 sequences of 8,192: 324 us, 2.15 GB at 6.6 TB/s;
+//   d = 64: 184 us, 1.07 GB at 5.9 TB/s.  One sequence of 131,072: 89 us, 6.0 TB/s, with
+//   the start, the join and the ends of the runs; of 100: 6.7 us, all latency.
 #pragma once
 #include <atomic>
 
@@ -109,7 +110,7 @@ struct Layout {
   static constexpr int NS = D == 128 ? 5 : 12;  // 160 or 192 KB of K and V in flight
   // Costs, in quarters of a key tile against one query tile, chosen by time over mixed batches (24
   // chunks and tokens of up to 300 over up to 5,000 keys, 32 heads of 128 on 8 / 15 of 64 on 5: 278 us /
-  // 123 us; with 5, 14 / 6, 20 for the last two 296 / 125, with 6, 9 / 7, 12 284 / 130).  The last is a
+  // 123 us then, 251 / 109 now; with 5, 14 / 6, 20 for the last two 296 / 125 then, with 6, 9 / 7, 12 284 / 130).  The last is a
   // unit's start and end, raised, as dearer units leave fewer of them cut and joined.
   static constexpr int COST1 = 4, COST2 = D == 128 ? 6 : 7, OVERHEAD = D == 128 ? 20 : 28;
   // Tensor memory: S0 [0,128), S1 [128,256), O0 [256,384), O1 [384,512).  P overwrites S: keys
@@ -673,7 +674,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   // d = 128 single tokens took 389 us that take 336, at d = 64 a chunk over 32,768 positions 1,131
   // and 770.)  Measured at d = 64 and dropped: columns of P_hi's own and P_lo in shared memory, so
   // that a stream's next S is computed while its softmax still runs, with two issuers: the chunk 750 us, 24
-  // mixed sequences no faster, and every buffer freed by two warps that run apart.
+  // mixed sequences no faster, and every buffer freed by two warps that run apart.  At d = 128: halves of 64 keys, a
+  // half's next S behind its product, while the softmax is at the other half: twice the exchanges, 1,030 us -> 1,450.
   auto role_mma = [&]() {
     const uint32_t idS = idesc_bf16_f32(BM, BN, 0, 0), idO = idesc_bf16_f32(BM, D, 0, 1);
     const SDesc dQ = sdesc_make(smem_u32(smem + L::OFF_Q), 16, 1024);
@@ -822,6 +824,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc_fence_after();
         if (active) {
           const int kv0 = (u.j0 + (two ? i : 2 * i + t)) * BN;
+          // In loops, S read twice from tensor memory: straight through the 128 columns the instructions came from
+          // memory at a launch's start (9 us before the first product P V, 5 now) and not all of them stayed
+          // beside the other stream's (the chunk 1,090 us; other loops of 16 to 128 columns, or with the next
+          // load under way, 0 to 3% slower than these).
           float mx4[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) mx4[e] = -INFINITY;
@@ -1066,8 +1072,9 @@ __global__ void __launch_bounds__(THREADS, 1)
 // tensor cores' rate does not matter), and eight warps an SM work for themselves: a warp
 // takes its share of a tile's 128 keys, copies them, keeps its own running (m, l, O), and the
 // block joins its warps' at the end of a unit.  Units, runs and partial results are those of
-// the kernel above.  Two stages of 8 KB a warp; a third, or more blocks, made the memory
-// slower (64 sequences of 16,384: 356 us with two stages, 374 with three).
+// the kernel above.  Two stages of 8 KB a warp; a third, or more blocks, made the memory slower (64 sequences
+// of up to 16,384: 356 us with two stages, 374 with three).  A unit is joined while the next one's first stage and Q
+// are under way, through shared memory of its own (that batch 364 -> 329 us, one sequence of 131,072 102 -> 92).
 constexpr int TOK_ROWS = 16;
 template <int D, int WARPS>
 struct TokenLayout {
@@ -1382,9 +1389,9 @@ __global__ void __launch_bounds__(32 * WARPS, TokenLayout<D, WARPS>::BLOCKS) pag
 
 // Whether a call's rows may be few: with a query head's group that fits 16 rows, no more new
 // tokens than sequences, or so few that they fit one tile.  Single tokens, 32 heads on 8, this kernel
-// and the one above: 64 sequences of 300 at d = 64 19.5 us and 44.1, at d = 128 27.2 and 53.3; of
-// 1,000 57 and 90, of 4,000 190 and 212, of 8,192 366 and 369 (d = 64 206 and 252); 200 of 300 62 and 140.
-// One sequence of 100: 6.4 and 11.9, of 4,096: 14.6 and 19.7, of 131,072: 101 and 107.
+// and the one above: 64 sequences of 300 at d = 64 16.2 us and 36.3, at d = 128 22.6 and 42.6; of
+// 1,000 53 and 70, of 4,000 167 and 191, of 8,192 324 and 355 (d = 64 184 and 215); 200 of 300 59 and 110.
+// One sequence of 100: 6.7 and 11.5, of 4,096: 13.1 and 16.6, of 131,072: 89 and 102.
 bool few_rows(const PagedAttnArgs &a, int G) {
   return G <= TOK_ROWS && (a.total <= a.seqs.batch || (int64_t)a.total * G <= TOK_ROWS);
 }
@@ -1392,8 +1399,8 @@ bool few_rows(const PagedAttnArgs &a, int G) {
 // coincidence; fewer may be a chunk in a batch that is padded with empty sequences, whose keys 16-row
 // tiles would read once for every 16 rows.  Then sequences of more than two tiles are left to a launch
 // of the kernel above, which finds nothing to do where there are none (32 heads on 8, d = 128, a batch
-// of 256 padded with empty sequences: 200 tokens over 8,192 keys 61 us, 217 without that launch; 64 single
-// tokens over 300 keys 33 and 28).
+// of 256 padded with empty sequences: 200 tokens over 8,192 keys 52 us, 158 without that launch; 64 single
+// tokens over 300 keys 27 and 23).
 bool may_have_chunks(const PagedAttnArgs &a, int G) {
   return a.total < a.seqs.batch && (int64_t)a.total * G > 2 * TOK_ROWS;
 }
@@ -1572,7 +1579,9 @@ __global__ void __launch_bounds__(256, 4) paged_combine_kernel(const Params p) {
 // A block takes ROWS rows, a lane a row, as in the parts (with 16 rows, half a warp's lanes take other parts).  Of a few
 // parts a warp takes COLS float4 of every row, and the unit's first boundary all columns; many parts are dealt to the
 // warps, PB loaded at once, and the unit's boundaries share its columns out.  The groups' sums are joined
-// through shared memory.
+// through shared memory.  With a warp to each D / 8 columns and the parts one after another, as above, 48 rows of 76 parts
+// took 38 us, 8 now; 256 rows of 19 parts 13.7, 10 now (each launch by itself, second-level cache cold).  As one block an SM
+// that loops, so that OWN's first blocks run beside it, the whole call was 3% slower.
 template <int ROWS>
 struct JoinShared {
   static constexpr int COLS = 4, GROUPS = 8 * (32 / ROWS);
@@ -1819,8 +1828,8 @@ template <int D, int MODE>
 cudaError_t launch_pass(const PagedAttnArgs &a, Params p, int seqs, bool few, bool chunks, bool early, cudaStream_t st) {
   using L = Layout<D>;
   // Few units are spread over the warps of one block an SM, more over two blocks, whose starts and
-  // ends overlap (1,000 keys a sequence, 8 K/V heads: 2 sequences 10.8 us, 13.5 with two blocks;
-  // 4 sequences 11.8 and 12.3; 8 15.6 and 14.2; 16 21.5 and 19.2)
+  // ends overlap (1,000 keys a sequence, 8 K/V heads: 2 sequences 11.4 us, 13.3 with two blocks;
+  // 4 sequences 11.8 and 12.3; 8 15.0 and 13.5; 16 19.7 and 17.6)
   cudaError_t e;
   int mark = 0;  // kernel boundaries so far
   if (few) {
@@ -1847,7 +1856,7 @@ cudaError_t launch_pass(const PagedAttnArgs &a, Params p, int seqs, bool few, bo
   const uint32_t bk[4] = {64, (uint32_t)(page < BN ? page : BN), 1, 1};
   // A token's row of one K/V head is 128 bytes at d = 64, and the bytes after it belong to
   // another head, which another unit reads much later: fetched 256 at a time, they are read for
-  // nothing (single tokens of 64 sequences of 8,192 keys, 64 heads on 2: 75 us, 79 with 256).  At
+  // nothing (single tokens of 64 sequences of 8,192 keys, 64 heads on 2: 75 us, 79 with 256, by tiles of 128 rows).  At
   // d = 128 the row is the 256 bytes.
   const CUtensorMapL2promotion promote =
       D == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;

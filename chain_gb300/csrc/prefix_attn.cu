@@ -12,6 +12,19 @@
 // lanes side by side as in the parts of a cut unit; OWN joins them where it would have
 // written O, in a unit's end or in the join of a cut one, so that O is rounded once.  Each pass deals its work as a
 // call alone does.  OWN begins while SHARED ends, and waits for it only where it joins.
+//
+// Bounds, and what was measured (in a graph, again and again; by itself, second-level cache cold, in brackets):
+//   64 tokens, 32 heads on 8, d = 128, behind 8,192 positions, up to 512 of their own: 62 us [SHARED 26, its join 10,
+//   OWN 24, its join 6], of which 16 are its bytes.  SHARED is a start (8 us to the first S, 5 to the first softmax's
+//   end, both instructions and tables from memory), three steps of 2.3 us and 128 KB of sums a block;
+//   128 tokens behind 32,768, up to 1,024 of their own: 152 us [80, 13, 53, 6], bytes 60, operations 37: the
+//   chain of the 128-row tiles, then memory;
+//   6 tokens of 8 heads to a K/V head behind 131,072: 61 us [37, 8, 10, 7], bytes 20: the chain of copies
+//   and products at one query tile, and three starts;
+//   32 chunks of up to 64 tokens behind 16,384: 368 us [322, 14, 32, 3], operations 181: the chain.
+// Measured for SHARED and dropped, each right: V turned into f16 in shared memory by warps of its own, so that P
+// enters as one f16 (322 us -> 336: what passes between the warps counts, not the products); 32- and 64-row tiles in
+// the kernel of few rows (one group of 32 rows 57 us -> 53, eight 61 -> 65, 48 rows 60 -> 72).
 #include "paged_attn.cuh"
 
 namespace chain {
@@ -36,8 +49,13 @@ cudaError_t launch(const PrefixAttnArgs &x, const WaitCfg &wc, cudaStream_t st) 
   // the device), and with so many tokens a sequence that each fills its own query tiles: they are multiplied as
   // often, and read from the second-level cache.
   const int64_t keys = (int64_t)a.seqs.batch * a.seqs.max_pages << a.seqs.page_shift;
-  if (keys * a.Hkv * D * 4 <= ALONE_BYTES || a.total >= 2 * (int64_t)own.utok * a.seqs.batch)
-    return launch_pass<D, OWN>(a, own, a.seqs.batch, few_rows(a, own.G), may_have_chunks(a, own.G), false, st);
+  if (keys * a.Hkv * D * 4 <= ALONE_BYTES || a.total >= 2 * (int64_t)own.utok * a.seqs.batch) {
+    timing_mark(st, 0);
+    const cudaError_t e = launch_pass<D, OWN>(a, own, a.seqs.batch, few_rows(a, own.G), may_have_chunks(a, own.G), false, st);
+    timing_mark(st, 1);
+    return e;
+  }
+  timing_mark(st, 0);
   const int64_t rows = (int64_t)a.total * a.H;
   uint8_t *ws = static_cast<uint8_t *>(a.workspace) + 2 * pass_workspace(D);
   own.pre_o = reinterpret_cast<float *>(ws);
@@ -50,12 +68,16 @@ cudaError_t launch(const PrefixAttnArgs &x, const WaitCfg &wc, cudaStream_t st) 
   shared.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(b.workspace) + part_bytes(D));
   shared.bounds = reinterpret_cast<Boundary *>(static_cast<uint8_t *>(b.workspace) + part_bytes(D) + ml_bytes());
   // Tiles of 16 rows where the groups' rows fit one on the average; what is longer than two of them then goes to a launch
-  // of its own, as with single tokens.
+  // of its own, as with single tokens.  (Two tiles to a group: 16 groups of 24 rows at d = 64 62 us, 59 with tiles of
+  // 128; one of 32 behind 32,768 73 and 58.)
   const int64_t group_rows = (int64_t)a.total * own.G;
   const bool few = own.G <= TOK_ROWS && group_rows <= (int64_t)TOK_ROWS * x.groups;
   cudaError_t e = launch_pass<D, SHARED>(b, shared, x.groups, few, x.groups > 1 && group_rows > 2 * TOK_ROWS, false, st);
   if (e != cudaSuccess) return e;
-  return launch_pass<D, OWN>(a, own, a.seqs.batch, few_rows(a, own.G), may_have_chunks(a, own.G), true, st);
+  timing_mark(st, 1);
+  e = launch_pass<D, OWN>(a, own, a.seqs.batch, few_rows(a, own.G), may_have_chunks(a, own.G), true, st);
+  timing_mark(st, 2);
+  return e;
 }
 
 }  // namespace

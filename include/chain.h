@@ -598,9 +598,9 @@ int chain_fwd_paged(const chain_tensor_t *Q, const chain_tensor_t *Kc, const cha
  *   workspace    at least chain_fwd_paged_prefix_workspace_size(Q, Kc) bytes, 16-byte aligned,
  *                contents ignored on entry; calls that may overlap on the GPU need one each.
  * Every new token must see its group's whole prefix: prefix_lens[g] at most kv_lens[b] - n_b
- * with CAUSAL, kv_lens[b] with NONE.  A sequence with new tokens for which it is not so is
- * reported by the next chain_check() as CHAIN_ERR_ARG and its rows are not valid; a prefix_lens[g]
- * below 0 or above max_pages * page of a group with new tokens is reported and taken as the nearer end.
+ * with CAUSAL, kv_lens[b] with NONE.  A sequence with new tokens for which it is not so, or
+ * a negative prefix_lens[g] (taken as 0), is reported by the next chain_check() as CHAIN_ERR_ARG, and the
+ * rows of a group that a prefix is too long for are not valid; nothing outside the pool or the table is accessed.
  * Arithmetic: as chain_fwd_paged; a row's sums over the prefix (whole tiles of 128 keys of it) and over
  * what its sequence has behind are held in fp32 and joined before the rounding of O.  Results are
  * deterministic, but not the bits of chain_fwd_paged.  Asynchronous on `stream`.
