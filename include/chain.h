@@ -17,8 +17,8 @@
  * attention ("Ulysses Sequence Parallelism", "Contexte Technique") and its
  * inverse (the second exchange of "Analyse et Implications"); and, beside the
  * attention of a model that is trained or answers with it, the norm and
- * position rotation of its queries and keys, and a paged K/V cache: its write
- * and the attention of a chunk of new tokens over it.
+ * position rotation of its queries and keys, and a paged K/V cache: its pages, its write
+ * and the attention of a chunk of new tokens over it, behind shared prefixes too.
  *
  * Conventions common to every entry point
  *  - Tensors are described by chain_tensor_t: a DEVICE pointer, an element
