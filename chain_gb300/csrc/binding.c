@@ -419,6 +419,12 @@ static int pages(PyObject *lens, const char *what, PyObject *kv, PyObject *table
   return 0;
 }
 
+/* One that does not fit an int is no page size either. */
+static int page_size(PyObject *o) {
+  const long x = PyLong_AsLong(o);
+  return x < 0 || x > 1 << 20 ? 0 : (int)x;
+}
+
 static PyObject *page_plan(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   (void)self;
   if (count(n, 15, "chain_page_plan")) return NULL;
@@ -431,12 +437,12 @@ static PyObject *page_plan(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   if (row_of(a[6], dev, "cu_seqlens", 0, &ends, &cu) || row_of(a[9], dev, "positions", 0, &rows, &positions_) ||
       row_of(a[10], dev, "slots", 1, &rows, &slots))
     return NULL;
-  const long page = PyLong_AsLong(a[5]);
+  const int page = page_size(a[5]);
   const size_t bytes = PyLong_AsSize_t(a[12]);
   if (PyErr_Occurred()) return NULL;
   int rc;
   Py_BEGIN_ALLOW_THREADS
-  rc = chain_page_plan(p.lens, p.kv, p.table, p.stride, (int)p.batch, p.max_pages, (int)page, p.free, p.capacity,
+  rc = chain_page_plan(p.lens, p.kv, p.table, p.stride, (int)p.batch, p.max_pages, page, p.free, p.capacity,
                        p.count, cu, p.kv_out, p.count_out, positions_, slots, rows, p.ws, bytes, stream);
   Py_END_ALLOW_THREADS
   return done(rc, "chain_page_plan");
@@ -448,13 +454,13 @@ static PyObject *page_trim(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   DEV_STREAM(11);
   pages_t p;
   if (pages(a[0], "keep_lens", a[1], a[2], a[3], a[4], a[7], a[8], a[9], dev, &p)) return NULL;
-  const long page = PyLong_AsLong(a[5]);
+  const int page = page_size(a[5]);
   const long long pool = PyLong_AsLongLong(a[6]);
   const size_t bytes = PyLong_AsSize_t(a[10]);
   if (PyErr_Occurred()) return NULL;
   int rc;
   Py_BEGIN_ALLOW_THREADS
-  rc = chain_page_trim(p.lens, p.kv, p.table, p.stride, (int)p.batch, p.max_pages, (int)page, pool, p.free,
+  rc = chain_page_trim(p.lens, p.kv, p.table, p.stride, (int)p.batch, p.max_pages, page, pool, p.free,
                        p.capacity, p.count, p.kv_out, p.count_out, p.ws, bytes, stream);
   Py_END_ALLOW_THREADS
   return done(rc, "chain_page_trim");

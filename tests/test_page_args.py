@@ -91,6 +91,10 @@ def test_the_native_modules_own_checks(cg):
             call(**bad)
     with pytest.raises(cg.ChainError):  # a row stride below max_pages
         call(table=ints(1, 4).expand(3, 4))
+    for page in (2 ** 32 + 16, -16, 0):
+        with pytest.raises(cg.ChainError) as e:
+            call(page=page)
+        assert e.value.status == cg.ERR_UNSUPPORTED
 
     def trim_call(**over):
         a = dict(keep=ints(3), kv=ints(3), table=ints(3, 4), free=ints(8), count=ints(1), page=16, pool=9,
