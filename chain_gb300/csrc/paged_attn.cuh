@@ -676,6 +676,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   // that a stream's next S is computed while its softmax still runs, with two issuers: the chunk 750 us, 24
   // mixed sequences no faster, and every buffer freed by two warps that run apart.  At d = 128: halves of 64 keys, a
   // half's next S behind its product, while the softmax is at the other half: twice the exchanges, 1,030 us -> 1,450.
+  // One elected lane goes through a unit's steps by itself: the pipe holds few products, so that what lies between a
+  // step's last and the next one's first shows whole.  (Elected step by step, the waits by a lane and their outcome
+  // exchanged, the chunk at d = 128 959 us that takes 867.)
   auto role_mma = [&]() {
     const uint32_t idS = idesc_bf16_f32(BM, BN, 0, 0), idO = idesc_bf16_f32(BM, D, 0, 1);
     const SDesc dQ = sdesc_make(smem_u32(smem + L::OFF_Q), 16, 1024);
@@ -685,23 +688,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     int k = 0;
     uint32_t q_uses[2] = {0, 0}, qsel = 0;
     uint32_t base = 0;             // ring number of the unit's first K tile
-    uint32_t steps[2] = {0, 0};    // P V products of each stream so far
+    uint32_t steps[2] = {0, 0};    // P V products of each stream before the unit
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
       return mbar_wait_warp(bar, parity, p.wc, abort_flag, SITE_PAGED_MMA);
-    };
-    // Two barriers in one go, and whether a third is there already: lane 0 polls, as in
-    // mbar_wait_warp, and one exchange tells the others.  Returns bit 0: both over, bit 1: the third.
-    auto wait_pair = [&](uint64_t *b0, uint32_t p0, uint64_t *b1, uint32_t p1, uint64_t *b2, uint32_t p2) -> int {
-      int r = 0;
-      if (lane == 0) {
-        const uint32_t a0 = smem_u32(b0), a1 = smem_u32(b1);
-        const bool r0 = mbar_try_wait(a0, p0), r1 = mbar_try_wait(a1, p1);
-        r = (r0 || mbar_wait(b0, p0, p.wc, abort_flag, SITE_PAGED_MMA)) &&
-            (r1 || mbar_wait(b1, p1, p.wc, abort_flag, SITE_PAGED_MMA));
-        if (r && b2 && mbar_try_wait(smem_u32(b2), p2)) r |= 2;
-      }
-      return __shfl_sync(0xffffffffu, r, 0);
     };
     while (ok && next_unit(k, u, SITE_PAGED_MMA)) {
       const bool two = u.ntok > p.tpt;
@@ -734,27 +724,19 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (last_reader(t)) umma_commit(&empty[st]);
         if (two ? i == ns[t] - 1 : 2 * i + t == n - 1) umma_commit(&q_empty[two ? t : single]);
       };
-      auto issue_s = [&](int t, int i) -> bool {
-        const uint32_t seq = k_seq(t, i);
-        if (!wait(&full[seq % NS], (seq / NS) & 1)) return false;
-        tc_fence_after();
-        if (elect_one()) put_s(t, i);
-        __syncwarp();
-        return true;
+      auto there = [&](uint32_t seq) {
+        return mbar_wait(&full[seq % NS], (seq / NS) & 1, p.wc, abort_flag, SITE_PAGED_MMA);
       };
-      // O_t += P_hi V + P_lo V of step i, with S of the stream's next step right behind it if its K
-      // tile is there
-      auto issue_pv = [&](int t, int i) -> bool {
-        const uint32_t seq = k_seq(t, i) + 1, st = seq % NS;
-        const bool next_s = i + 1 < ns[t];
-        const uint32_t nseq = k_seq(t, i + 1);
-        const int got = wait_pair(&full[st], (seq / NS) & 1, &p_ready[t], steps[t] & 1,
-                                  next_s ? &full[nseq % NS] : nullptr, (nseq / NS) & 1);
-        if (!(got & 1)) return false;
-        // The last page may hold anything behind the sequence's end, and 0 times a NaN
-        // is not 0: those rows of V become zeros (twice, where both streams read them).
-        const int valid = u.len - (u.j0 + (two ? i : 2 * i + t)) * BN;
-        if (valid > 0 && valid < BN) {
+      // The last page may hold anything behind the sequence's end, and 0 times a NaN is not 0: those rows of the
+      // last tile's V become zeros, by the warp, before the unit's last steps.
+      const int valid = u.len - (u.j1 - 1) * BN, count = two ? n : (n + 1) / 2;
+      const bool tail = valid > 0 && valid < BN;
+#pragma unroll 1
+      for (int last = 0; ok && last < (tail ? 2 : 1); ++last) {
+        if (last) {
+          const uint32_t seq = base + 2 * n - 1, st = seq % NS;
+          ok = wait(&full[st], (seq / NS) & 1);
+          if (!ok) break;
           const int page = 1 << p.s.page_shift;
           const int upto = min(BN, (valid + page - 1) & ~(page - 1));
           for (int c = lane; c < (upto - valid) * (D / 8); c += 32) {
@@ -765,28 +747,46 @@ __global__ void __launch_bounds__(THREADS, 1)
           fence_proxy_async_smem();
           __syncwarp();
         }
-        ++steps[t];
-        tc_fence_after();
         if (elect_one()) {
-          const uint32_t vo = st * L::TILE;
+          if (!last)
 #pragma unroll
-          for (int part = 0; part < 2; ++part)
+            for (int t = 0; t < 2; ++t)
+              if (ok && ns[t] > 0 && (ok = there(k_seq(t, 0)))) {
+                tc_fence_after();
+                put_s(t, 0);
+              }
+          const int end = tail && !last ? count - 1 : count;
+#pragma unroll 1
+          for (int i = last ? count - 1 : 0; ok && i < end; ++i)
 #pragma unroll
-            for (int kk = 0; kk < BN / 16; ++kk)
-              umma_f16_ts(tmem + L::o_col(t), tmem + t * BN + kk * 16 + part * 8, sdesc_at(dV, vo + kk * 2048), idO,
-                          i > 0 || part > 0 || kk > 0);
-          umma_commit(&pv_done[t]);
-          if (last_reader(t)) umma_commit(&empty[st]);
-          if (got & 2) put_s(t, i + 1);
+            for (int t = 0; t < 2; ++t) {
+              if (!ok || i >= ns[t]) continue;
+              // O_t += P_hi V + P_lo V of step i; stream 1 finds the tiles there that stream 0 has waited for
+              const uint32_t seq = k_seq(t, i) + 1, st = seq % NS, vo = st * L::TILE;
+              const bool seen = two && t == 1 && i < ns[0];
+              ok = (seen || there(seq)) &&
+                   mbar_wait(&p_ready[t], (steps[t] + i) & 1, p.wc, abort_flag, SITE_PAGED_MMA);
+              if (!ok) continue;
+              tc_fence_after();
+#pragma unroll
+              for (int part = 0; part < 2; ++part)
+#pragma unroll
+                for (int kk = 0; kk < BN / 16; ++kk)
+                  umma_f16_ts(tmem + L::o_col(t), tmem + t * BN + kk * 16 + part * 8, sdesc_at(dV, vo + kk * 2048), idO,
+                              i > 0 || part > 0 || kk > 0);
+              umma_commit(&pv_done[t]);
+              if (last_reader(t)) umma_commit(&empty[st]);
+              if (i + 1 < ns[t] && (ok = (seen && i + 1 < ns[0]) || there(k_seq(t, i + 1)))) {
+                tc_fence_after();
+                put_s(t, i + 1);
+              }
+            }
         }
         __syncwarp();
-        return !next_s || (got & 2) || issue_s(t, i + 1);
-      };
-      for (int t = 0; ok && t < 2; ++t)
-        if (ns[t] > 0) ok = issue_s(t, 0);
-      for (int i = 0; ok && i < max(ns[0], ns[1]); ++i)
-        for (int t = 0; ok && t < 2; ++t)
-          if (i < ns[t]) ok = issue_pv(t, i);
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      steps[0] += ns[0];
+      steps[1] += ns[1];
       base += 2 * n;
     }
     // no MMA may still be running when tensor memory is released
