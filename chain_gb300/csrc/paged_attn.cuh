@@ -173,6 +173,29 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 
+// tmem_ld32, and the largest of the lane's 32 columns as fp32.
+__device__ __forceinline__ float tmem_ld32_max(uint32_t taddr, uint32_t (&r)[32]) {
+  float top;
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, "
+      "%8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, "
+      "%24, %25, %26, %27, %28, %29, %30, %31}, %32, [%33];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]),
+        "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+        "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=f"(top)
+      : "r"(taddr)
+      : "memory");
+  return top;
+}
+
 // Each lane holds 64 bytes of its own row and `at`, their place in memory.
 // Four lanes exchange 16-byte chunks, so that one store writes 64 bytes of each of
 // eight rows: a lane storing its own row would touch 32 lines an instruction,
@@ -824,34 +847,33 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc_fence_after();
         if (active) {
           const int kv0 = (u.j0 + (two ? i : 2 * i + t)) * BN;
-          // In loops, S read twice from tensor memory: straight through the 128 columns the instructions came from
-          // memory at a launch's start (9 us before the first product P V, 5 now) and not all of them stayed
-          // beside the other stream's (the chunk 1,090 us; other loops of 16 to 128 columns, or with the next
-          // load under way, 0 to 3% slower than these).
-          float mx4[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) mx4[e] = -INFINITY;
+          // In loops, S read twice from tensor memory, the first time for its maximum, which the load brings (the
+          // chunk 868 us, 858 so; 32 chunks behind 16,384 shared positions 333 and 324): straight through the 128
+          // columns the instructions came from memory at a launch's start and not all of them stayed beside the other
+          // stream's.  Other loops of 32 to 128 columns, or with the next load under way: 2% slower to 2% faster on
+          // long runs, 2 to 6% slower on 24 mixed sequences.
+          float mx = -INFINITY;
 #pragma unroll 1
           for (int c = 0; c < BN; c += 64) {
-            uint32_t s[64];
-            tmem_ld32(tS + c, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
-            tmem_ld32(tS + c + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
-            tmem_wait_ld();
             if (__any_sync(0xffffffffu, kv0 + c + 64 > lim)) {
+#pragma unroll 1
+              for (int d = c; d < c + 64; d += 32) {
+                uint32_t s[32];
+                tmem_ld32(tS + d, s);
+                tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 64; ++e)
-                if (kv0 + c + e >= lim) s[e] = __float_as_uint(-INFINITY);
-              tmem_st32(tS + c, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
-              tmem_st32(tS + c + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+                for (int e = 0; e < 32; ++e)
+                  if (kv0 + d + e >= lim) s[e] = __float_as_uint(-INFINITY);
+                tmem_st32(tS + d, s);
+              }
               tmem_wait_st();
             }
-#pragma unroll
-            for (int i = 0; i < 64; i += 8)
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                mx4[e] = fmax3(mx4[e], __uint_as_float(s[i + 2 * e]), __uint_as_float(s[i + 2 * e + 1]));
+            uint32_t s[2][32];
+            const float a = tmem_ld32_max(tS + c, s[0]), b = tmem_ld32_max(tS + c + 32, s[1]);
+            tmem_wait_ld();
+            mx = fmax3(mx, a, b);
           }
-          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.scale_log2;
+          mx *= p.scale_log2;
           float alpha = 1.0f;
           bool rescale = false;
           if (i == 0) {
@@ -884,7 +906,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 rs2[(e >> 1) & 3] = add_f32x2(rs2[(e >> 1) & 3], f32x2(p0, p1));
                 const uint32_t h = pack_bf16(p0, p1);
                 pk[e >> 1] = h;
-                pk[8 + (e >> 1)] = pack_bf16(p0 - __uint_as_float(h << 16), p1 - __uint_as_float(h & 0xffff0000u));
+                float y0, y1;
+                f32x2_split(fma_f32x2(f32x2(__uint_as_float(h << 16), __uint_as_float(h & 0xffff0000u)), f32x2(-1.0f, -1.0f), f32x2(p0, p1)), y0, y1);
+                pk[8 + (e >> 1)] = pack_bf16(y0, y1);
               }
               tmem_st16(tS + c + g * 16, pk);
             }
