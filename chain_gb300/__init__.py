@@ -366,14 +366,14 @@ def _small():
 
 def _where(stream):
     """The current device, and the handle of `stream` or of its current stream."""
-    dev = torch.cuda.current_device()
+    dev = torch._C._cuda_getDevice()  # torch.cuda.current_device() less its check for a first use
     if stream is None:
         return dev, torch._C._cuda_getCurrentRawStream(dev)
     return dev, _stream(stream).value or 0
 
 
 def _bytes(t):
-    return t.numel() * t.element_size()
+    return t.nbytes
 
 
 def chain_qk_norm_rope(Q, K, gq, gk, inv_freq, positions, eps, pairs, Qo, Ko, stream=None):

@@ -89,7 +89,17 @@ static int tensor(PyObject *t, long dev, int optional, chain_tensor_t *d, chain_
   return 0;
 }
 
-/* Index array of `nd` dimensions, innermost contiguous: int32, or int64 where `wide` */
+/* 1 or 0; -1 on error */
+static int is_dense(PyObject *t) {
+  PyObject *c = PyObject_CallMethodNoArgs(t, s_is_contiguous);
+  if (!c) return -1;
+  const int dense = PyObject_IsTrue(c);
+  Py_DECREF(c);
+  return dense;
+}
+
+/* Index array of `nd` dimensions, innermost contiguous: int32, or int64 where `wide`.  `stride` is of more
+ * than one dimension only: a tuple of one costs half as much again as asking whether the array is contiguous. */
 static int index_array(PyObject *t, long dev, const char *what, int wide, int nd, void **ptr, int64_t *shape,
                        int64_t *stride) {
   PyObject *dt = PyObject_GetAttr(t, s_dtype);
@@ -98,17 +108,21 @@ static int index_array(PyObject *t, long dev, const char *what, int wide, int nd
   Py_DECREF(dt);
   if (on_device(t, dev) || address(t, ptr)) return -1;
   const int n = read_sizes(PyObject_GetAttr(t, s_shape), shape, nd);
-  if (n < 0 || read_sizes(PyObject_CallMethodNoArgs(t, s_stride), stride, nd) < 0) return -1;
+  if (n < 0) return -1;
   if (!ok || n != nd) {
     PyErr_Format(PyExc_ValueError, "%s must be a CUDA %s tensor of %d dimension%s", what, wide ? "int64" : "int32", nd,
                  nd > 1 ? "s" : "");
     return -1;
   }
-  if (shape[nd - 1] > 1 && stride[nd - 1] != 1) {
-    PyErr_Format(PyExc_ValueError, "%s must be contiguous", what);
-    return -1;
+  int dense;
+  if (nd == 1) {
+    dense = is_dense(t);
+  } else {
+    if (read_sizes(PyObject_CallMethodNoArgs(t, s_stride), stride, nd) < 0) return -1;
+    dense = shape[nd - 1] <= 1 || stride[nd - 1] == 1;
   }
-  return 0;
+  if (dense == 0) PyErr_Format(PyExc_ValueError, "%s must be contiguous", what);
+  return dense == 1 ? 0 : -1;
 }
 
 static int indices(PyObject *t, long dev, const char *what, int nd, void **ptr, int64_t *shape, int64_t *stride) {
@@ -117,23 +131,14 @@ static int indices(PyObject *t, long dev, const char *what, int nd, void **ptr, 
 
 /* One dimension of `len` entries, or of any number of them where it is -1, which is then returned in it. */
 static int row_of(PyObject *t, long dev, const char *what, int wide, int64_t *len, void **ptr) {
-  int64_t shape[1], stride[1];
-  if (index_array(t, dev, what, wide, 1, ptr, shape, stride)) return -1;
+  int64_t shape[1];
+  if (index_array(t, dev, what, wide, 1, ptr, shape, NULL)) return -1;
   if (*len >= 0 && shape[0] != *len) {
     PyErr_Format(PyExc_ValueError, "%s must have %lld entries, not %lld", what, (long long)*len, (long long)shape[0]);
     return -1;
   }
   *len = shape[0];
   return 0;
-}
-
-/* 1 or 0; -1 on error */
-static int is_dense(PyObject *t) {
-  PyObject *c = PyObject_CallMethodNoArgs(t, s_is_contiguous);
-  if (!c) return -1;
-  const int dense = PyObject_IsTrue(c);
-  Py_DECREF(c);
-  return dense;
 }
 
 /* positions: one int32 for each of `tokens`, any shape, or None */
@@ -174,8 +179,8 @@ typedef struct {
 } paged_t;
 
 static int paged(PyObject *cu, PyObject *lens, PyObject *table, long dev, paged_t *p) {
-  int64_t sc[2], sl[2], st[2], tc[2], tl[2], tt[2];
-  if (indices(cu, dev, "cu_seqlens", 1, &p->cu, sc, tc) || indices(lens, dev, "kv_lens", 1, &p->lens, sl, tl) ||
+  int64_t sc[1], sl[1], st[2], tt[2];
+  if (indices(cu, dev, "cu_seqlens", 1, &p->cu, sc, NULL) || indices(lens, dev, "kv_lens", 1, &p->lens, sl, NULL) ||
       indices(table, dev, "page_table", 2, &p->table, st, tt))
     return -1;
   if (sc[0] != sl[0] + 1 || st[0] != sl[0] || sl[0] > 0x7fffffff || st[1] > 0x7fffffff) {
