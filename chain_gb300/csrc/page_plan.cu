@@ -14,9 +14,10 @@
 //
 // Small calls are one block, whose time is its dependent loads (lengths, sums, entries, stores): one step of
 // 512 requests 3.9 us, of one 2.7 (again and again in a graph; 9.4 and 7.3 with the second-level cache cold and a
-// graph's start).  Large ones take two launches, the sums in one block (or, for what goes back, the counts in all) and
-// the expansion by every SM: 64 prompts of 951,000 rows 10 us, 12 MB; 366,000 pages of 512 sequences given back 10 us
-// (28 with one warp to a sequence).
+// graph's start).  Large plans take two launches, the sums in one block and the expansion by every SM: 64 prompts of
+// 951,000 rows 10 us, 12 MB.  Trims of larger tables are a cluster's, and of the largest two launches, the counts by a
+// block a sequence and then the copies: 300 sequences that give back a page or none 4.9 us, 512 that give back 366,000
+// pages 5.5.
 #include "internal.h"
 
 namespace chain {
@@ -25,11 +26,16 @@ namespace {
 constexpr int THREADS = 1024;     // of a block that sums
 constexpr int ONE_BATCH = 1024;   // most sequences of a one-block plan: their sums lie in shared memory
 constexpr int WIDE = 256;         // threads of a block that expands
-// Most rows, and most entries of a table, that one block takes.  Rows, one block and two launches: 1,024 3.5 us and
-// 6.8, 4,096 6.2 and 7.1, 8,192 9.4 and 6.8.  Entries: where a few tokens go back 2.9 us and 4.3 at any size of the table;
-// where whole sequences do, 15,600 entries 9.9 and 4.6, 64,000 20.7 and 4.1.
+// Most rows that one block takes: one block and two launches, 1,024 rows 3.5 us and 6.8, 4,096 6.2 and 7.1, 8,192 9.4 and 6.8.
 constexpr int64_t ONE_ROWS = 4096;
-constexpr int64_t ONE_ENTRIES = 1 << 15;
+// Entries of a table whose trim one block, a cluster, or two launches take, by what goes back in a graph, a few pages
+// and all of them: 4,096 entries 3.5 and 6.1, 4.8 and 6.3, 3.6 and 3.7 us; 8,192 3.5 and 6.0, 4.8 and 6.2; 31,500 3.5 and 18.8,
+// 4.8 and 6.8, 4.2 and 4.3; 128,000 3.6 and 58.8, 4.9 and 13.3, 4.8 and 5.4; 366,000 the last 3.7 and 152, 5.0 and
+// 26.4, 4.8 and 5.5.  Called one by one a second launch takes 2.5 us of the host's time (5.7 and 8.2 us a call), so that
+// one is preferred as long as a call that gives everything back, which is rare, stays near that.
+constexpr int64_t ONE_ENTRIES = 1 << 13;
+constexpr int CLUSTER = 8;  // blocks
+constexpr int64_t CLUSTER_ENTRIES = 1 << 17;
 
 __device__ __forceinline__ void report(DevStatus *s) { atomicExch(&s->reserved[0], 1); }
 
@@ -260,57 +266,90 @@ __device__ __forceinline__ int entries(const PageTrimArgs &a, int b, Cut c, long
   return n;
 }
 
-// All in one block: a thread takes a sequence that gives back few pages, a warp one that gives back many.
+// All in one launch, of one block or a cluster of C.  A thread takes a sequence, and their entries, laid end to end, are cut
+// into one piece for each warp: whatever the mix of sequences, the warps have as much to do.  A lane finds its entry's
+// sequence among the sums by bisection, and keeps it for its next entry.  Every block finds the cuts and sums by itself; what
+// its piece puts on the stack it tells the others through their shared memory.
+template <int C>
 __global__ void __launch_bounds__(THREADS, 1) trim_kernel(const PageTrimArgs a) {
-  constexpr int FEW = 4;
+  constexpr int BATCH = 8;  // loads under way
   __shared__ long long warps[32];
-  __shared__ Cut cuts[ONE_BATCH];
-  __shared__ int sums[ONE_BATCH];
+  __shared__ int off[ONE_BATCH + 1], shift[ONE_BATCH];  // entries before a sequence's; an entry's place less its number
+  __shared__ int puts[32], totals[C];                   // entries that name a page: of the warps, of the blocks
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = threadIdx.x;
+  const int rank = C > 1 ? (int)cluster_ctarank() : 0;
   bool bad = false;
   const int count = count_of(a.free_count, a.capacity, bad);
   Cut c = {0, 0};
-  int x[FEW], n = 0;
-  if (b < a.batch) {
-    int left;
-    c = cut_of(a, b, left, bad);
-    a.kv_out[b] = left;
-  }
-  const bool few = c.last - c.first <= FEW;
-#pragma unroll
-  for (int i = 0; i < FEW; ++i) {
-    x[i] = few && c.first + i < c.last ? a.table[(int64_t)b * a.table_stride + c.first + i] : -1;
-    const bool is = x[i] >= 0 && x[i] < a.num_pages;
-    bad |= few && c.first + i < c.last && !is;
-    if (!is) x[i] = -1;
-    n += is;
-  }
-  cuts[b] = c;
-  const bool many = __syncthreads_or(!few);
-  auto each = [&](auto &&f) {  // the sequences that a warp takes
-    for (int i = warp; many && i < a.batch; i += THREADS / 32)
-      if (cuts[i].last - cuts[i].first > FEW) f(i);
-  };
-  each([&](int i) {
-    const int got = entries<false>(a, i, cuts[i], 0, bad);
-    if (lane == 0) sums[i] = got;
-  });
-  __syncthreads();
-  if (!few) n = sums[b];
+  int left = 0;
+  if (b < a.batch) c = cut_of(a, b, left, bad);
+  if (C > 1) cluster_sync_all();  // every block is there to be written to
   long long all;
-  long long to = count + block_sum(n, all, warps);
-  sums[b] = (int)(to - count);
+  const int at = (int)block_sum(c.last - c.first, all, warps), end = (int)all;
+  if (b < a.batch) {
+    off[b] = at;
+    shift[b] = c.first - at;
+  }
+  if (b == 0) off[a.batch] = end;
   __syncthreads();
+  const int step = ((end + 32 * C - 1) / (32 * C) + 31) & ~31;
+  const int lo = (int)min((long long)(rank * 32 + warp) * step, all), hi = (int)min((long long)lo + step, all);
+  int x[BATCH], seq = -1;
+  const int pool = (int)a.num_pages;
+  auto load = [&](int e0) {
 #pragma unroll
-  for (int i = 0; i < FEW; ++i)
-    if (x[i] >= 0) {
-      if (to < a.capacity) a.free_pages[to] = x[i];
-      ++to;
+    for (int i = 0; i < BATCH; ++i) {
+      const int e = e0 + 32 * i + lane;
+      x[i] = -1;
+      if (e < hi) {
+        if (seq < 0 || e >= off[seq + 1]) {  // most often the next one
+          if (seq < 0 || e >= off[++seq + 1]) seq = owner(max(seq, 0), a.batch, e, [&](int s) { return off[s]; });
+        }
+        x[i] = a.table[(int64_t)seq * a.table_stride + shift[seq] + e];
+      }
     }
-  bool seen = false;  // reported by the count
-  each([&](int i) { entries<true>(a, i, cuts[i], (long long)count + sums[i], seen); });
-  bad |= count + all > a.capacity;
-  if (threadIdx.x == 0) *a.count_out = (int)min(count + all, (long long)a.capacity);
+  };
+  auto is = [&](int i) { return x[i] >= 0 && x[i] < pool; };
+  int n = 0;
+  for (int e0 = lo; e0 < hi; e0 += 32 * BATCH) {
+    load(e0);
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      n += __popc(__ballot_sync(0xffffffffu, is(i)));
+      bad |= e0 + 32 * i + lane < hi && !is(i);
+    }
+  }
+  if (lane == 0) puts[warp] = n;
+  __syncthreads();
+  const int before = __reduce_add_sync(0xffffffffu, lane < warp ? puts[lane] : 0);
+  int total = __reduce_add_sync(0xffffffffu, puts[lane]), base = 0;
+  if (C > 1) {
+    if (b < C)
+      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(smem_u32(&totals[rank]), b)), "r"(total) : "memory");
+    cluster_sync_all();  // and every block has read the lengths and the count, which may be written in place
+    const int of = lane < C ? totals[lane] : 0;
+    base = __reduce_add_sync(0xffffffffu, lane < rank ? of : 0);
+    total = __reduce_add_sync(0xffffffffu, of);
+  }
+  long long to = (long long)count + base + before;
+  for (int e0 = lo; e0 < hi; e0 += 32 * BATCH) {
+    if (step > 32 * BATCH) {  // else they are still there
+      if (e0 == lo) seq = -1;
+      load(e0);
+    }
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const uint32_t in = __ballot_sync(0xffffffffu, is(i));
+      const long long place = to + __popc(in & ((1u << lane) - 1));
+      if (is(i) && place < a.capacity) a.free_pages[place] = x[i];
+      to += __popc(in);
+    }
+  }
+  bad |= (long long)count + total > a.capacity;
+  if (rank == 0) {
+    if (b < a.batch) a.kv_out[b] = left;
+    if (b == 0) *a.count_out = (int)min((long long)count + total, (long long)a.capacity);
+  }
   if (bad) report(a.status);
 }
 
@@ -429,9 +468,25 @@ cudaError_t launch_page_plan(const PagePlanArgs &a, cudaStream_t st) {
 
 cudaError_t launch_page_trim(const PageTrimArgs &a, cudaStream_t st) {
   timing_mark(st, 0);
-  if (a.batch <= ONE_BATCH && (int64_t)a.batch * a.max_pages <= ONE_ENTRIES) {
-    trim_kernel<<<1, THREADS, 0, st>>>(a);
-    const cudaError_t e = cudaGetLastError();
+  const int64_t entries = (int64_t)a.batch * a.max_pages;
+  if (a.batch <= ONE_BATCH && entries <= CLUSTER_ENTRIES) {
+    cudaError_t e;
+    if (entries <= ONE_ENTRIES) {
+      trim_kernel<1><<<1, THREADS, 0, st>>>(a);
+      e = cudaGetLastError();
+    } else {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(CLUSTER);
+      cfg.blockDim = dim3(THREADS);
+      cfg.stream = st;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = CLUSTER;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      e = cudaLaunchKernelEx(&cfg, trim_kernel<CLUSTER>, a);
+    }
     timing_mark(st, 1);
     return e;
   }

@@ -249,6 +249,36 @@ def test_what_a_trim_reports(cg, max_pages):
     s.same(kv, count, s.tabled, s.freed)
 
 
+LARGE_TRIMS = {
+    "one sequence, all of it": ([700000], [0], 16, 43760),
+    "one sequence, one page": ([700000], [699990], 16, 43760),
+    "every sequence, all of it": ([(331 * i) % 1100 for i in range(1024)], [0] * 1024, 16, 70),
+    "every sequence, some of it": ([(331 * i) % 1100 for i in range(1023)], [(77 * i) % 1100 for i in range(1023)], 16, 70),
+    "a long one among short ones": ([5] * 200 + [300000] + [17] * 300, [1] * 200 + [40] + [3] * 300, 16, 18800),
+    "one token each": ([16 * i + 1 for i in range(300)], [16 * i for i in range(300)], 16, 350),
+}
+
+
+@pytest.mark.parametrize("missing", [0, 7])
+@pytest.mark.parametrize("name", LARGE_TRIMS)
+def test_trim_of_a_large_table(cg, name, missing):
+    lens, keeps, page, max_pages = LARGE_TRIMS[name]
+    s = State(lens, page, max_pages, 3, len(name))
+    lost, k = 0, 0
+    for b, (L, keep) in enumerate(zip(lens, keeps)):  # every so often an entry that names no page
+        for e in range(-(-min(L, keep) // page), -(-L // page)):
+            k += 1
+            if missing and k % missing == 0:
+                s.table[b][e] = -1 if k % 2 else s.pool
+                lost += 1
+    s.cuda()
+    out = (s.lensd, s.countd)
+    kv, count = cg.page_trim(ints(keeps).cuda(), s.lensd, s.tabled, s.freed, s.countd, page, s.pool, out=out)
+    assert cg.chain_check()[0] == (cg.ERR_ARG if lost else 0)
+    s.trim(keeps)
+    s.same(kv, count, s.tabled, s.freed)
+
+
 def test_nothing_to_do(cg):
     s = State([], 16, 4, 5).cuda()
     cu, kv, count, positions, slots = plan(cg, s, [], 6)
