@@ -32,7 +32,7 @@
 //   warp 8     TMA producer: Q tiles, then K and V tiles through one ring of
 //              NS tile slots in the order K0 V0 K1 V1 ...; a tile of 128 keys is
 //              128 / page boxes, their pages looked up one tile ahead, one lane a box.
-//   warp 9     MMA issuer.
+//   warp 9     MMA issuer, one lane of it through a unit's steps.
 //   warp 10    scheduler: finds the run's units and hands them to the other
 //              warps through a small ring.
 // Two streams share the tensor core, so that one multiplies while the other
@@ -43,11 +43,11 @@
 // Calls of single tokens go to paged_token_kernel, further down, which shares the split.
 //
 // Bounds, and what was measured (32 heads on 8, pages of 64 to 128):
-//   chunks: the chain of softmax and products.  d = 128, 2,048 tokens over 32,768: 1,030 us,
-//   1,035 TFLOP/s (P_lo's product not counted; 775 us with one bf16 of P, before the softmax was rolled): a
-//   stream's softmax and its three products follow each other, since P shares S's columns; two
-//   streams overlap them.  A step of both takes 2.3 us: a softmax 1.0, its products 0.8, and what passes
-//   between the barriers' two sides 0.5.  d = 64: 760 us, 700 TFLOP/s.
+//   chunks: the tensor pipe, 77% busy at d = 128, and the chain that leaves the rest of it.  2,048 tokens over
+//   32,768: 877 us, 1,215 TFLOP/s (P_lo's product not counted): a stream's softmax and its three products
+//   follow each other, since P shares S's columns; two streams overlap them.  In copies made to be timed only, without any
+//   softmax it takes 733 us, without P_lo and its product 691, without the exponentials no less.  d = 64: 703 us,
+//   757 TFLOP/s.
 //   single tokens: memory.  d = 128, 64 sequences of 8,192: 324 us, 2.15 GB at 6.6 TB/s;
 //   d = 64: 184 us, 1.07 GB at 5.9 TB/s.  One sequence of 131,072: 89 us, 6.0 TB/s, with
 //   the start, the join and the ends of the runs; of 100: 6.7 us, all latency.

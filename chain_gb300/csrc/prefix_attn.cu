@@ -14,16 +14,17 @@
 // call alone does.  OWN begins while SHARED ends, and waits for it only where it joins.
 //
 // Bounds, and what was measured (in a graph, again and again; by itself, second-level cache cold, in brackets):
-//   64 tokens, 32 heads on 8, d = 128, behind 8,192 positions, up to 512 of their own: 62 us [SHARED 26, its join 10,
+//   64 tokens, 32 heads on 8, d = 128, behind 8,192 positions, up to 512 of their own: 60 us [SHARED 25, its join 10,
 //   OWN 24, its join 6], of which 16 are its bytes.  SHARED is a start (8 us to the first S, 5 to the first softmax's
-//   end, both instructions and tables from memory), three steps of 2.3 us and 128 KB of sums a block;
-//   128 tokens behind 32,768, up to 1,024 of their own: 152 us [80, 13, 53, 6], bytes 60, operations 37: the
-//   chain of the 128-row tiles, then memory;
-//   6 tokens of 8 heads to a K/V head behind 131,072: 61 us [37, 8, 10, 7], bytes 20: the chain of copies
+//   end, both instructions and tables from memory), three steps of 2 us and 128 KB of sums a block;
+//   128 tokens behind 32,768, up to 1,024 of their own: 143 us [72, 14, 55, 7], bytes 60, operations 37: the
+//   128-row tiles, whose tensor pipe is 66% busy, then memory;
+//   6 tokens of 8 heads to a K/V head behind 131,072: 58 us [34, 8, 10, 7], bytes 20: the chain of copies
 //   and products at one query tile, and three starts;
-//   32 chunks of up to 64 tokens behind 16,384: 368 us [322, 14, 32, 3], operations 181: the chain.
+//   32 chunks of up to 64 tokens behind 16,384: 325 us [280, 14, 32, 3], operations 181 and, with P's low part, 271.
 // Measured for SHARED and dropped, each right: V turned into f16 in shared memory by warps of its own, so that P
-// enters as one f16 (322 us -> 336: what passes between the warps counts, not the products); 32- and 64-row tiles in
+// enters as one f16 (322 us -> 336 then: what passes between the warps counts; without P's low part at all the 32
+// chunks would take 273 of 325 now); 32- and 64-row tiles in
 // the kernel of few rows (one group of 32 rows 57 us -> 53, eight 61 -> 65, 48 rows 60 -> 72).
 #include "paged_attn.cuh"
 
