@@ -171,8 +171,8 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
   return r;
 }
 
-// All threads of all CTAs of the cluster.  Used only at kernel start, where
-// every CTA of the cluster reaches it with nothing to wait for.
+// All threads of all CTAs of the cluster.  Used only where every CTA of the
+// cluster reaches it with nothing to wait for.
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile(
       "barrier.cluster.arrive.release.aligned;\n\t"
