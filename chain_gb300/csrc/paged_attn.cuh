@@ -665,7 +665,10 @@ __global__ void __launch_bounds__(THREADS, 1)
           pages = checked(ahead, first + lane);
           ahead = entry(first + 32 + lane);
         }
-        const int pg = __shfl_sync(0xffffffffu, pages, (e + part) & 31);
+        int pg = __shfl_sync(0xffffffffu, pages, (e + part) & 31);
+        // A sequence that has nothing behind its prefix still has one tile, and the page that the prefix ends in may hold
+        // anything there: such boxes are the pool's end too.  (A tile that `len` falls into: see `tail`.)
+        if (j * BN + part * rows >= u.len) pg = pool;
         const int at = page > BN ? (j * BN) & (page - 1) : 0;
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
