@@ -172,8 +172,10 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
 }
 
 // All threads of all CTAs of the cluster.  Used only where every CTA of the
-// cluster reaches it with nothing to wait for.
+// cluster reaches it with nothing to wait for.  A warp's lanes must execute the
+// `.aligned` forms together, which nothing promises behind a branch that they did not all take.
 __device__ __forceinline__ void cluster_sync_all() {
+  __syncwarp();
   asm volatile(
       "barrier.cluster.arrive.release.aligned;\n\t"
       "barrier.cluster.wait.acquire.aligned;" ::
