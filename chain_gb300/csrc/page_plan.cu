@@ -273,6 +273,7 @@ __device__ __forceinline__ int entries(const PageTrimArgs &a, int b, Cut c, long
 template <int C>
 __global__ void __launch_bounds__(THREADS, 1) trim_kernel(const PageTrimArgs a) {
   constexpr int BATCH = 8;  // loads under way
+  static_assert(C > 1 || ONE_ENTRIES <= 32 * 32 * BATCH, "a warp's piece of one block's table is one batch");
   __shared__ long long warps[32];
   __shared__ int off[ONE_BATCH + 1], shift[ONE_BATCH];  // entries before a sequence's; an entry's place less its number
   __shared__ int puts[32], totals[C];                   // entries that name a page: of the warps, of the blocks
@@ -333,9 +334,11 @@ __global__ void __launch_bounds__(THREADS, 1) trim_kernel(const PageTrimArgs a) 
   }
   long long to = (long long)count + base + before;
   for (int e0 = lo; e0 < hi; e0 += 32 * BATCH) {
-    if (step > 32 * BATCH) {  // else they are still there
-      if (e0 == lo) seq = -1;
-      load(e0);
+    if constexpr (C > 1) {
+      if (step > 32 * BATCH) {  // else they are still there
+        if (e0 == lo) seq = -1;
+        load(e0);
+      }
     }
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
