@@ -196,6 +196,14 @@ __device__ __forceinline__ float tmem_ld32_max(uint32_t taddr, uint32_t (&r)[32]
   return top;
 }
 
+// What a row's sums give: 1 / l and the LSE.  l is 0 where the row sees no key (a sum has at least 2^0 from its largest
+// score), and NaN where a score is NaN or +infinity: a maximum does not show that, the sum does, so every
+// join keeps it, and the row's O and LSE become NaN with it.
+__device__ __forceinline__ float inverse(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l == 0.0f ? -INFINITY : (m + lg2(l)) * 0.69314718055994531f;
+}
+
 // Each lane holds 64 bytes of its own row and `at`, their place in memory.
 // Four lanes exchange 16-byte chunks, so that one store writes 64 bytes of each of
 // eight rows: a lane storing its own row would touch 32 lines an instruction,
@@ -967,6 +975,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           w[0] = ex2(m - top);
           w[1] = ex2(o.x - top);
           l = l * w[0] + o.y * w[1];
+        } else {
+          l += o.y;  // 0 or NaN
         }
         m = top;
       }
@@ -997,7 +1007,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           __syncwarp();
         }
         if (!sums_out) {
-          const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+          const float inv = inverse(l);
           w[0] *= inv;
           w[1] *= inv;
           wp *= inv;
@@ -1053,7 +1063,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         if (valid) {
           if (!sums_out)
-            p.LSE[qhead * p.lse_shead + u.tok0 + tok] = l > 0.0f ? (m + lg2(l)) * 0.69314718055994531f : -INFINITY;
+            p.LSE[qhead * p.lse_shead + u.tok0 + tok] = lse_of(m, l);
           else if (MODE == SHARED && whole)
             p.pre_ml[u.head * pre_pitch + pre_row] = make_float2(m, l);
           else
@@ -1284,7 +1294,7 @@ __global__ void __launch_bounds__(32 * WARPS, TokenLayout<D, WARPS>::BLOCKS) pag
             pre[c * pre_pitch] = make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
           if ((threadIdx.x & 7) == 0) p.pre_ml[done.head * pre_pitch + pre_row] = make_float2(top, sum);
         } else if (done.slot < 0) {
-          const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+          const float inv = inverse(sum);
           const int64_t qhead = (int64_t)done.head * p.G + row - tok * p.G;
           uint4 *dst = reinterpret_cast<uint4 *>(p.O + ((int64_t)done.tok0 + tok) * p.o_stok + qhead * p.o_shead + c0);
 #pragma unroll
@@ -1293,8 +1303,7 @@ __global__ void __launch_bounds__(32 * WARPS, TokenLayout<D, WARPS>::BLOCKS) pag
                                 pack_bf16(x[8 * c + 4] * inv, x[8 * c + 5] * inv),
                                 pack_bf16(x[8 * c + 6] * inv, x[8 * c + 7] * inv));
           if ((threadIdx.x & 7) == 0)
-            p.LSE[qhead * p.lse_shead + done.tok0 + tok] =
-                sum > 0.0f ? (top + lg2(sum)) * 0.69314718055994531f : -INFINITY;
+            p.LSE[qhead * p.lse_shead + done.tok0 + tok] = lse_of(top, sum);
         } else {
           const int64_t slot = (int64_t)blockIdx.x * 2 + done.slot;
           float4 *dst = reinterpret_cast<float4 *>(p.part_o) + slot * (TOK_ROWS * D / 4) + row;
@@ -1503,7 +1512,11 @@ __device__ __forceinline__ void combine_rows(const Params &p, const Boundary &bd
     float top = m;
 #pragma unroll
     for (int i = 0; i < PB; ++i) top = fmaxf(top, x[i].x);
-    if (top == -INFINITY) continue;
+    if (top == -INFINITY) {
+#pragma unroll
+      for (int i = 0; i < PB; ++i) l += x[i].y;  // 0 or NaN
+      continue;
+    }
     const float w0 = ex2(m - top);
     m = top;
     l *= w0;
@@ -1562,15 +1575,14 @@ __device__ __forceinline__ void combine_rows(const Params &p, const Boundary &bd
       o[q].w = o[q].w * w0 + y.w * w1;
     }
   }
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const float inv = inverse(l);
   if (group == 0) {
 #pragma unroll
     for (int q = 0; q < Q; ++q)
       rows[lane % ROWS][warp * Q + q] =
           make_uint2(pack_bf16(o[q].x * inv, o[q].y * inv), pack_bf16(o[q].z * inv, o[q].w * inv));
     if (warp == 0 && valid)
-      p.LSE[((int64_t)bd.head * p.G + r % BM - rt * p.G) * p.lse_shead + bd.tok0 + tok] =
-          l > 0.0f ? (m + lg2(l)) * 0.69314718055994531f : -INFINITY;
+      p.LSE[((int64_t)bd.head * p.G + r % BM - rt * p.G) * p.lse_shead + bd.tok0 + tok] = lse_of(m, l);
   }
   __syncthreads();
   for (int i = warp; i < ROWS; i += 8) {
@@ -1644,7 +1656,11 @@ __device__ __forceinline__ void join_parts(const Params &p, int c, int first, in
     float top = m;
 #pragma unroll
     for (int i = 0; i < PB; ++i) top = fmaxf(top, x[i].x);
-    if (top == -INFINITY) continue;
+    if (top == -INFINITY) {
+#pragma unroll
+      for (int i = 0; i < PB; ++i) l += x[i].y;  // 0 or NaN
+      continue;
+    }
     const float w0 = ex2(m - top);
     m = top;
     l *= w0;

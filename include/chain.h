@@ -564,6 +564,8 @@ int chain_qk_norm_rope_append(const chain_tensor_t *Q, const chain_tensor_t *K,
  *              GPU need one each.
  * Cached K and V must be finite at positions below kv_lens[b]; slots of later
  * positions may hold anything, NaN included.  A missing page counts as keys and values of zeros.
+ * A row of Q that is not finite, and sees a key, gets NaN in O and LSE where its scores are NaN or +infinity;
+ * other rows are not touched by it.
  * Arithmetic: Q K^T, the softmax's statistics and P V accumulate in fp32;
  * P enters the P V product as a pair of bf16 (P and what its rounding left), as in
  * chain_fwd, so that O's own rounding is the only one to bf16.  A call with H / Hkv at most 16 and total at
