@@ -1597,6 +1597,7 @@ __device__ __forceinline__ void combine_rows(const Params &p, const Boundary &bd
 
 template <int D, int RUNS, int SLOT, int MODE>
 __global__ void __launch_bounds__(256, 4) paged_combine_kernel(const Params p) {
+  static_assert(MODE != SHARED, "the prefix's parts are joined by shared_join_kernel");
   __shared__ uint2 rows[32][D / 4 + 1];
   pdl_wait();  // the parts and boundaries
   const int c = blockIdx.x + 1, y = blockIdx.y;
@@ -1797,8 +1798,10 @@ cudaError_t launch_join(const PagedAttnArgs &a, const Params &p, cudaStream_t st
   // no sequence is longer than a key tile: no unit is cut
   if (((int64_t)a.seqs.max_pages << a.seqs.page_shift) <= BN) return cudaSuccess;
   const dim3 grid(RUNS - 1, SLOT < 32 ? 1 : SLOT / 32);
-  if constexpr (MODE == SHARED) return launch_kernel(shared_join_kernel<D, RUNS, SLOT>, grid, 256, 0, true, st, p);
-  return launch_kernel(paged_combine_kernel<D, RUNS, SLOT, MODE>, grid, 256, 0, true, st, p);
+  if constexpr (MODE == SHARED)
+    return launch_kernel(shared_join_kernel<D, RUNS, SLOT>, grid, 256, 0, true, st, p);
+  else
+    return launch_kernel(paged_combine_kernel<D, RUNS, SLOT, MODE>, grid, 256, 0, true, st, p);
 }
 
 template <int D, int WARPS, int MODE>
