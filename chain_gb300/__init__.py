@@ -734,8 +734,8 @@ def attention_fwd_paged_prefix(q, k_cache, v_cache, cu_seqlens, kv_lens, page_ta
     o = _dense_like(q)
     lse = torch.empty(q.shape[1], q.shape[0], dtype=torch.float32, device=q.device)
     if workspace is None:
-        workspace = torch.empty(max(chain_fwd_paged_prefix_workspace_size(q, k_cache), 16), dtype=torch.uint8,
-                                device=q.device)
+        size = chain_fwd_paged_prefix_workspace_size if prefix_lens.shape[0] else chain_fwd_paged_workspace_size
+        workspace = torch.empty(max(size(q, k_cache), 16), dtype=torch.uint8, device=q.device)
     chain_fwd_paged_prefix(q, k_cache, v_cache, cu_seqlens, kv_lens, page_table, prefix_cu, prefix_lens,
                            MASK_CAUSAL if causal else MASK_NONE, scale, o, lse, workspace)
     return o, lse

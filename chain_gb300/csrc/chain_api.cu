@@ -1216,8 +1216,8 @@ int chain_fwd_paged_prefix(const chain_tensor_t *Q, const chain_tensor_t *Kc, co
     return CHAIN_ERR_ARG;
   if (groups > kMaxPagedBatch) return CHAIN_ERR_UNSUPPORTED;
   if (!work) return CHAIN_OK;
-  if (!workspace || !aligned16(workspace) || ws_bytes < prefix_attn_workspace(x.a.d, x.a.total, x.a.H))
-    return CHAIN_ERR_ARG;
+  const size_t need = groups == 0 ? paged_attn_workspace(x.a.d) : prefix_attn_workspace(x.a.d, x.a.total, x.a.H);
+  if (!workspace || !aligned16(workspace) || ws_bytes < need) return CHAIN_ERR_ARG;
   x.a.workspace = workspace;
   x.group_cu = prefix_cu; x.group_lens = prefix_lens; x.groups = groups;
   DevInfo *di = nullptr;

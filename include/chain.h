@@ -597,8 +597,9 @@ int chain_fwd_paged(const chain_tensor_t *Q, const chain_tensor_t *Kc, const cha
  *                sequences that have new tokens name the same pages for the positions below
  *                prefix_lens[g].  Any number, also inside a page.  groups at most 8192
  *                (else CHAIN_ERR_UNSUPPORTED); with groups = 0 the call is chain_fwd_paged.
- *   workspace    at least chain_fwd_paged_prefix_workspace_size(Q, Kc) bytes, 16-byte aligned,
- *                contents ignored on entry; calls that may overlap on the GPU need one each.
+ *   workspace    at least chain_fwd_paged_prefix_workspace_size(Q, Kc) bytes (with groups = 0
+ *                chain_fwd_paged_workspace_size(Q, Kc)), 16-byte aligned, contents
+ *                ignored on entry; calls that may overlap on the GPU need one each.
  * Every new token must see its group's whole prefix: prefix_lens[g] at most kv_lens[b] - n_b
  * with CAUSAL, kv_lens[b] with NONE.  A sequence with new tokens for which it is not so, or
  * a negative prefix_lens[g] (taken as 0), is reported by the next chain_check() as CHAIN_ERR_ARG, and the

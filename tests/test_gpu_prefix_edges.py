@@ -1,6 +1,7 @@
 """GPU: attention over a paged cache behind shared prefixes, where nothing is left behind the prefix and where a page
 ends behind it.  Tolerances: those of test_gpu_prefix, by the same check."""
 import pytest
+import torch
 
 import chain_synth as cs
 from test_gpu_paged import cg, check  # noqa: F401  (cg: the fixture)
@@ -37,3 +38,16 @@ def test_several_groups_whose_prefix_is_all(cg, P):
     o, lse = cg.attention_fwd_paged_prefix(q.cuda(), c.kcd, c.vcd, *c.args, causal=False)
     assert cg.chain_check()[0] == 0
     check(c, q, o, lse, False, 128 ** -0.5)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("news", [[1, 1, 1], [20, 1, 33]])
+def test_without_groups_it_is_the_plain_call(cg, news, causal):
+    c = Shared([], [300, 5000, 64], news, 2, 128, 64, 75).fill().cuda()
+    q = cs.normal((c.total, 8, 128), 76).cuda()
+    ref = cg.attention_fwd_paged(q, c.kcd, c.vcd, *c.args[:3], causal=causal)
+    ws = torch.empty(cg.chain_fwd_paged_workspace_size(q, c.kcd), dtype=torch.uint8, device="cuda")
+    for given in (ws, None):
+        got = cg.attention_fwd_paged_prefix(q, c.kcd, c.vcd, *c.args, causal=causal, workspace=given)
+        assert all(torch.equal(a, b) for a, b in zip(got, ref))
+    assert cg.chain_check()[0] == 0
