@@ -725,7 +725,7 @@ def attention_fwd_paged_prefix(q, k_cache, v_cache, cu_seqlens, kv_lens, page_ta
     """attention_fwd_paged of sequences that share prefixes: those of group g, prefix_cu[g] to prefix_cu[g + 1] - 1
     (int32 [groups + 1]), have their first prefix_lens[g] (int32 [groups]) positions in the same pages, all of
     them before any new token.  Returns (O [total, H, d], LSE [H, total]) as attention_fwd_paged does; a shared
-    prefix is read and multiplied once."""
+    prefix is read and multiplied for its group's tokens together (see include/chain.h for how many at a time)."""
     if stream is not None:
         with _current(stream):
             return attention_fwd_paged_prefix(q, k_cache, v_cache, cu_seqlens, kv_lens, page_table, prefix_cu,

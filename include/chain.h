@@ -587,9 +587,12 @@ int chain_fwd_paged(const chain_tensor_t *Q, const chain_tensor_t *Kc, const cha
 /*
  * chain_fwd_paged_prefix -- chain_fwd_paged for a batch whose sequences share long
  * prefixes (one system prompt or document before many requests, one prompt
- * sampled many times), whose keys and values are read and multiplied once
- * for all of them.  (An addition of this library.)  All of chain_fwd_paged, its cache, arguments, masks
- * and results, and
+ * sampled many times), whose keys and values are read and multiplied for the group's tokens together, not for
+ * each sequence: once for each 2 floor(128 / G) of them, G = H / Hkv (once for each floor(16 / G) where the groups have at
+ * most 16 rows, tokens times G, on the average).  Two kinds of calls read them for each sequence all the same, where that is
+ * faster: tables that can name few keys (batch * max_pages * page * Hkv * d at most 2^25; the lengths are on the device), and
+ * those with 4 floor(128 / G) new tokens a sequence or more on the average.  (An addition of this library.)  All
+ * of chain_fwd_paged, its cache, arguments, masks and results, and
  *   prefix_cu    DEVICE int32 [groups + 1], nondecreasing: group g is the sequences
  *                [prefix_cu[g], prefix_cu[g+1]), clamped to [0, batch].  Sequences of
  *                no group share nothing.
@@ -601,8 +604,8 @@ int chain_fwd_paged(const chain_tensor_t *Q, const chain_tensor_t *Kc, const cha
  *                chain_fwd_paged_workspace_size(Q, Kc)), 16-byte aligned, contents
  *                ignored on entry; calls that may overlap on the GPU need one each.
  * Every new token must see its group's whole prefix: prefix_lens[g] at most kv_lens[b] - n_b
- * with CAUSAL, kv_lens[b] with NONE.  A sequence with new tokens for which it is not so, or
- * a negative prefix_lens[g] (taken as 0), is reported by the next chain_check() as CHAIN_ERR_ARG, and the
+ * with CAUSAL, kv_lens[b] with NONE.  A sequence with new tokens for which it is not so, or whose
+ * group's prefix_lens[g] is negative (taken as 0), is reported by the next chain_check() as CHAIN_ERR_ARG, and the
  * rows of a group that a prefix is too long for are not valid; nothing outside the pool or the table is accessed.
  * Arithmetic: as chain_fwd_paged; a row's sums over the prefix (whole tiles of 128 keys of it) and over
  * what its sequence has behind are held in fp32 and joined before the rounding of O.  Results are
@@ -646,10 +649,10 @@ int chain_fwd_paged_prefix(const chain_tensor_t *Q, const chain_tensor_t *Kc, co
  *                GPU need one each.
  * Reported by the next chain_check() as CHAIN_ERR_ARG: a negative length (taken as 0), a
  * cached length above max_pages * page (taken as that), tokens beyond `rows` (left out), a stack whose count
- * is not in [0, capacity] (taken as the nearer end), a stack that runs out and a table that is full: pages that are
- * not there are entries of -1 (none is written beyond the table), slots in them -1, and
- * free_count_out is 0.  Whole numbers: the result does not depend on the
- * order of execution.  Asynchronous on `stream`.
+ * is not in [0, capacity] (taken as the nearer end), a stack that runs out and a table that is full.  Pages that are
+ * not there are entries of -1 (none is written beyond the table), and slots in them -1.  A stack that runs
+ * out leaves free_count_out 0; a full table takes the pages that it has room for, and free_count_out is what they
+ * leave.  Whole numbers: the result does not depend on the order of execution.  Asynchronous on `stream`.
  */
 size_t chain_page_plan_workspace_size(int batch);
 int chain_page_plan(const int32_t *new_lens, const int32_t *kv_lens, int32_t *page_table,
