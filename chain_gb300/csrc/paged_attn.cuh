@@ -640,7 +640,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       // sequence has no keys or the table names no page
       const int *table = p.s.table + u.b * p.s.table_stride;
       const int pool = (int)p.s.num_pages;
-      auto keys_at = [&](int at) { return ((long long)at << p.s.page_shift) < u.len; };
+      // A sequence that has nothing behind its prefix still has one tile, and the page that the prefix ends in may hold
+      // anything there: no page of it has keys.  (A tile that the sequence's end falls into: see `tail`.)
+      const int len = u.j0 * BN < u.len ? u.len : 0;
+      auto keys_at = [&](int at) { return ((long long)at << p.s.page_shift) < len; };
       auto entry = [&](int at) { return keys_at(at) ? __ldg(table + at) : pool; };
       auto checked = [&](int pg, int at) {
         if (pg >= 0 && pg < pool) return pg;
@@ -673,10 +676,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           pages = checked(ahead, first + lane);
           ahead = entry(first + 32 + lane);
         }
-        int pg = __shfl_sync(0xffffffffu, pages, (e + part) & 31);
-        // A sequence that has nothing behind its prefix still has one tile, and the page that the prefix ends in may hold
-        // anything there: such boxes are the pool's end too.  (A tile that `len` falls into: see `tail`.)
-        if (j * BN + part * rows >= u.len) pg = pool;
+        const int pg = __shfl_sync(0xffffffffu, pages, (e + part) & 31);
         const int at = page > BN ? (j * BN) & (page - 1) : 0;
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
