@@ -21,7 +21,8 @@
 //   128-row tiles, whose tensor pipe is 66% busy, then memory;
 //   6 tokens of 8 heads to a K/V head behind 131,072: 58 us [34, 8, 10, 7], bytes 20: the chain of copies
 //   and products at one query tile, and three starts;
-//   32 chunks of up to 64 tokens behind 16,384: 325 us [280, 14, 32, 3], operations 181 and, with P's low part, 271.
+//   32 chunks of up to 64 tokens behind 16,384: 325 us [280, 14, 32, 3], operations 181 and, with P's low part, 271;
+//   without a mask the same within 2%; at d = 64 274 to 283 us, operations 91 (136 with the low part).
 // Measured for SHARED and dropped, each right: V turned into f16 in shared memory by warps of its own, so that P
 // enters as one f16 (322 us -> 336 then: what passes between the warps counts; without P's low part at all the 32
 // chunks would take 273 of 325 now); 32- and 64-row tiles in
@@ -34,7 +35,8 @@ namespace {
 // Two passes and one, 32 heads on 8, d = 128, second-level cache cold: single tokens, 64 sequences of 512
 // positions (128 MB in all) 44 us and 34, of 1,024 44 and 46, of 2,048 46 and 69; 16 of 2,048 35 and 31, of 4,096 37
 // and 43.  32 sequences of 1,024 (128 MB), 16 new tokens each 66 and 50, 64 each 98 and 70.  Query tiles that are
-// full: 4 sequences of 16,128 (252 MB), 128 new tokens each 177 and 151.
+// full: 4 sequences of 16,128 (252 MB), 128 new tokens each 177 and 151.  What a table can name stands for what the
+// lengths are, which only the device knows: 5 tokens behind 600 positions take 20 us with a table of ten pages and 36 with one of 512.
 constexpr int64_t ALONE_BYTES = int64_t(1) << 27;
 
 size_t rows_bytes(int64_t rows, int d) { return (size_t)rows * d * sizeof(float); }
