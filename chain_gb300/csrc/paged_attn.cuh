@@ -875,6 +875,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
                   if (kv0 + d + e >= lim) s[e] = __float_as_uint(-INFINITY);
+                __syncwarp();  // the lanes' limits differ, the store is the whole warp's
                 tmem_st32(tS + d, s);
               }
               tmem_wait_st();
@@ -1011,6 +1012,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           w[0] *= inv;
           w[1] *= inv;
           wp *= inv;
+          __syncwarp();  // the division may part the lanes; the loads below are the whole warp's
         }
         const int64_t qhead = (int64_t)u.head * p.G + rhead;
         __nv_bfloat16 *orow = p.O + ((int64_t)u.tok0 + tok) * p.o_stok + qhead * p.o_shead;
